@@ -1,5 +1,5 @@
-"""ctypes binding of libmoe.so (the C ABI declared in include/moe.h and
-include/fp8_fp4_gemm.h).
+"""ctypes binding of libmoe.so (the C ABI declared in include/moe.h, include/moe_serving.h,
+include/fp8_fp4_gemm.h and include/fp8_gemm.h).
 
 Argument marshalling only: every function passes device pointers, sizes and a HIP
 stream to the library and raises MoEError on a non-zero status. Tensors are torch
@@ -23,12 +23,23 @@ MOE_ERR_TOKENS = -5
 MOE_ERR_HIP = -6
 MOE_ERR_SCRATCH = -7
 
+# element types of logits and GEMM outputs, and what the router's softmax runs over
+MOE_BF16 = 0
+MOE_F32 = 1
+MOE_ROUTER_SOFTMAX_CHOSEN = 0
+MOE_ROUTER_SOFTMAX_ALL = 1
+# most tokens of one moe_forward_few call
+MOE_FEW_MAX_TOKENS = 32
+
 EXPORTED = ("moe_packed_weights_bytes", "moe_prepare_weights", "moe_workspace_bytes",
             "moe_forward", "moe_forward_events", "moe_forward_noalloc", "moe_workspace_layout", "moe_read_diagnostics",
             "moe_status_string", "moe_version",
             "moe_gemm_packed_b_bytes", "moe_gemm_prepare_b", "moe_gemm_workspace_bytes",
             "moe_fp8_fp4_gemm", "moe_m_grouped_fp8_fp4_gemm_contiguous",
-            "moe_m_grouped_fp8_fp4_gemm_masked", "moe_cast_to_fp8")
+            "moe_m_grouped_fp8_fp4_gemm_masked", "moe_cast_to_fp8",
+            "moe_topk_router", "moe_few_workspace_bytes", "moe_forward_few",
+            "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_m_grouped_fp8_gemm_contiguous",
+            "moe_m_grouped_fp8_gemm_masked")
 
 
 class MoEError(RuntimeError):
@@ -102,6 +113,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_m_grouped_fp8_fp4_gemm_masked.restype = ctypes.c_int
     lib.moe_cast_to_fp8.argtypes = [P, I32, I32, P, P, P]
     lib.moe_cast_to_fp8.restype = ctypes.c_int
+    F32 = ctypes.c_float
+    lib.moe_topk_router.argtypes = [P, P, P, I32, I32, I32, I32, I32, F32, P]
+    lib.moe_topk_router.restype = ctypes.c_int
+    lib.moe_few_workspace_bytes.argtypes = [shp]
+    lib.moe_few_workspace_bytes.restype = S
+    lib.moe_forward_few.argtypes = [P, P, P, P, P, I32, shp, P, P, S, P]
+    lib.moe_forward_few.restype = ctypes.c_int
+    lib.moe_fp8_gemm_workspace_bytes.argtypes = [I32, I32]
+    lib.moe_fp8_gemm_workspace_bytes.restype = S
+    lib.moe_fp8_gemm.argtypes = [P, I32, P, P, I32, I32, I32, P, P, P, S, P]
+    lib.moe_fp8_gemm.restype = ctypes.c_int
+    lib.moe_m_grouped_fp8_gemm_contiguous.argtypes = [P, I32, P, P, P, I32, I32, I32, I32, P, P, P, S, P]
+    lib.moe_m_grouped_fp8_gemm_contiguous.restype = ctypes.c_int
+    lib.moe_m_grouped_fp8_gemm_masked.argtypes = [P, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, S, P]
+    lib.moe_m_grouped_fp8_gemm_masked.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -293,3 +319,57 @@ def gemm_call_raw(name: str, *args) -> int:
     """Unchecked call of one of the GEMM / cast entry points with raw arguments; returns the
     status (for error-path tests)."""
     return getattr(load_library(), name)(*args)
+
+
+# ---------------------------------------------------------------------------
+# Router and few-token forward (include/moe_serving.h)
+# ---------------------------------------------------------------------------
+
+
+def moe_topk_router(topk_idx, topk_weights, logits, logits_type: int, num_tokens: int, num_experts: int,
+                    num_topk: int, softmax_over: int, weight_scale: float = 1.0, stream=None) -> None:
+    _check(load_library().moe_topk_router(_ptr(topk_idx), _ptr(topk_weights), _ptr(logits), int(logits_type),
+                                          int(num_tokens), int(num_experts), int(num_topk), int(softmax_over),
+                                          float(weight_scale), _stream(stream)), "moe_topk_router")
+
+
+def moe_few_workspace_bytes(shape: moe_shape_t) -> int:
+    return load_library().moe_few_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_forward_few(y, x_fp8, x_sf, topk_idx, topk_weights, num_tokens: int, shape: moe_shape_t, packed,
+                    workspace, stream=None) -> None:
+    """moe_forward for at most MOE_FEW_MAX_TOKENS tokens, in two kernels."""
+    _check(load_library().moe_forward_few(
+        _ptr(y), _ptr(x_fp8), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_weights), int(num_tokens),
+        ctypes.byref(shape), _ptr(packed), _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_forward_few")
+
+
+# ---------------------------------------------------------------------------
+# FP8 x FP8 GEMMs with 128-block scales (include/fp8_gemm.h)
+# ---------------------------------------------------------------------------
+
+
+def moe_fp8_gemm_workspace_bytes(max_rows: int, groups: int) -> int:
+    return load_library().moe_fp8_gemm_workspace_bytes(int(max_rows), int(groups))
+
+
+def moe_fp8_gemm(d, d_type: int, a, a_sf, m: int, n: int, k: int, b, b_sf, workspace, stream=None) -> None:
+    _check(load_library().moe_fp8_gemm(_ptr(d), int(d_type), _ptr(a), _ptr(a_sf), int(m), int(n), int(k), _ptr(b),
+                                       _ptr(b_sf), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "moe_fp8_gemm")
+
+
+def moe_m_grouped_fp8_gemm_contiguous(d, d_type: int, a, a_sf, group_of_row, m: int, groups: int, n: int, k: int,
+                                      b, b_sf, workspace, stream=None) -> None:
+    _check(load_library().moe_m_grouped_fp8_gemm_contiguous(
+        _ptr(d), int(d_type), _ptr(a), _ptr(a_sf), _ptr(group_of_row), int(m), int(groups), int(n), int(k), _ptr(b),
+        _ptr(b_sf), _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_m_grouped_fp8_gemm_contiguous")
+
+
+def moe_m_grouped_fp8_gemm_masked(d, d_type: int, a, a_sf, masked_m, groups: int, max_m: int, expected_m: int,
+                                  n: int, k: int, b, b_sf, workspace, stream=None) -> None:
+    _check(load_library().moe_m_grouped_fp8_gemm_masked(
+        _ptr(d), int(d_type), _ptr(a), _ptr(a_sf), _ptr(masked_m), int(groups), int(max_m), int(expected_m), int(n),
+        int(k), _ptr(b), _ptr(b_sf), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+        "moe_m_grouped_fp8_gemm_masked")

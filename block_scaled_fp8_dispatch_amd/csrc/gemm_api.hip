@@ -1,10 +1,11 @@
-// C ABI of the plain FP8 x FP4 GEMMs and the FP8 cast (include/fp8_fp4_gemm.h): argument
-// checks, workspace layout, and the launches. Host code only; the kernels are the grouped
+// C ABI of the plain FP8 x FP4 GEMMs and the FP8 cast (include/fp8_fp4_gemm.h) and of the
+// FP8 x FP8 GEMMs (include/fp8_gemm.h): argument checks, workspace layout, and the launches. Host code only; the kernels are the grouped
 // GEMM of gemm.hip in its plain mode (dense: rows and tiles derived in the kernel, K split
 // over several workgroups when the output has few tiles), the routing kernels of route.hip
 // (contiguous layout: rows grouped by their group id, stable in row order, each group padded
 // to the row-tile size), the layout kernel of route.hip (masked layout), and cast.hip.
 #include "fp8_fp4_gemm.h"
+#include "fp8_gemm.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -16,6 +17,8 @@ constexpr int kGemmMinBlockM = 64;
 constexpr size_t kSplitPartialBytes = size_t(16) << 20;
 // Split K only when the output tiles would fill fewer than this many workgroups
 constexpr int kSplitBelowTiles = 128;
+// Largest K of the FP8 x FP8 GEMMs: a tile's 256 rows of B stay within 32-bit offsets
+constexpr int kFp8MaxK = 1 << 22;
 // Workgroups split-K aims for (the CUs of one MI355X)
 constexpr int kSplitTargetWorkgroups = 256;
 
@@ -132,6 +135,34 @@ void split_plan(int tiles, int BM, int K, int& splits, int& ks_split) {
         splits = 1;
         ks_split = nks;
     }
+}
+
+// FP8 x FP8: N any positive number, B unpacked
+bool fp8_shape_ok(int G, int N, int K, int d_type) {
+    if (G < 1 || G > MOE_MAX_EXPERTS || N < 1) return false;
+    if (K < 128 || K % 128 != 0 || K > kFp8MaxK) return false;
+    return d_type == MOE_BF16 || d_type == MOE_F32;
+}
+
+GemmFp8Args fp8_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int N, int K, const uint8_t* b,
+                     const uint8_t* b_sf, uint8_t* ws, const GemmWs& W, int tiles_bound) {
+    GemmFp8Args g{};
+    g.a = a;
+    g.a_sf = a_sf;
+    g.b = b;
+    g.b_sf = b_sf;
+    g.K = K;
+    g.N = N;
+    g.sf_stride = 4 * cdiv(K, 512);
+    g.dense_rows = 0;
+    g.perm = reinterpret_cast<const int32_t*>(ws + W.perm);
+    g.meta = reinterpret_cast<const int32_t*>(ws + W.meta);
+    g.tile_expert = reinterpret_cast<const int32_t*>(ws + W.tile_expert);
+    g.tile_row0 = reinterpret_cast<const int32_t*>(ws + W.tile_row0);
+    g.max_tiles = tiles_bound < W.max_tiles ? tiles_bound : W.max_tiles;
+    g.d = d;
+    g.out_f32 = d_type == MOE_F32;
+    return g;
 }
 
 }  // namespace
@@ -262,6 +293,74 @@ int moe_cast_to_fp8(const uint16_t* x, int32_t rows, int32_t cols, uint8_t* x_fp
     if (rows == 0) return MOE_OK;
     if (launch_cast_fp8(x, rows, cols, x_fp8, x_sf, stream) != hipSuccess) return MOE_ERR_HIP;
     return MOE_OK;
+}
+
+size_t moe_fp8_gemm_workspace_bytes(int32_t max_rows, int32_t groups) {
+    return moe_gemm_workspace_bytes(max_rows, groups);
+}
+
+int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, int32_t m, int32_t n, int32_t k,
+                 const uint8_t* b, const uint8_t* b_sf, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!d || !a || !a_sf || !b || !b_sf || !workspace) return MOE_ERR_NULL;
+    if (!fp8_shape_ok(1, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(b) || !aligned16(b_sf) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (!rows_ok(m, 1, k)) return MOE_ERR_TOKENS;
+    const GemmWs W = gemm_ws(m, 1);
+    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (m == 0) return MOE_OK;
+    const int BM = 64;
+    GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, static_cast<uint8_t*>(workspace), W, cdiv(m, BM));
+    g.dense_rows = m;
+    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
+                                      const int32_t* group_of_row, int32_t m, int32_t groups, int32_t n, int32_t k,
+                                      const uint8_t* b, const uint8_t* b_sf, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+    if (!d || !a || !a_sf || !group_of_row || !b || !b_sf || !workspace) return MOE_ERR_NULL;
+    if (!fp8_shape_ok(groups, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(group_of_row) || !aligned16(b) ||
+        !aligned16(b_sf) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (!rows_ok(m, groups, k)) return MOE_ERR_TOKENS;
+    const GemmWs W = gemm_ws(m, groups);
+    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (m == 0) return MOE_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int BM = 64;
+    auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+    if (launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets), i32(W.perm),
+                     i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream) != hipSuccess)
+        return MOE_ERR_HIP;
+    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, cdiv(m, BM) + groups);
+    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
+                                  const int32_t* masked_m, int32_t groups, int32_t max_m, int32_t expected_m, int32_t n,
+                                  int32_t k, const uint8_t* b, const uint8_t* b_sf, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+    if (!d || !a || !a_sf || !masked_m || !b || !b_sf || !workspace) return MOE_ERR_NULL;
+    if (!fp8_shape_ok(groups, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(masked_m) || !aligned16(b) ||
+        !aligned16(b_sf) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (max_m < 0) return MOE_ERR_TOKENS;
+    const long long rows = (long long)groups * max_m;
+    if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
+    const GemmWs W = gemm_ws((int)rows, groups);
+    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (max_m == 0) return MOE_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int BM = 64;
+    if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
+                           reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
+                           reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
+        return MOE_ERR_HIP;
+    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, groups * cdiv(max_m, BM));
+    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

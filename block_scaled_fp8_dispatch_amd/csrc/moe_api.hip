@@ -18,24 +18,6 @@ constexpr int kMinBlockM = 64;
 // faster for 1 % of the forward; at k=8 it costs more than it saves.
 constexpr int kDispatchCopyMaxTopk = 2;
 
-bool shape_ok(const moe_shape_t* s) {
-    if (!s) return false;
-    if (s->num_experts < 1 || s->num_experts > MOE_MAX_EXPERTS) return false;
-    if (s->hidden < 128 || s->hidden % 128 != 0) return false;
-    if (s->intermediate < 128 || s->intermediate % 128 != 0) return false;
-    if (s->num_topk < 1 || s->num_topk > MOE_MAX_TOPK || s->num_topk > s->num_experts) return false;
-    if (s->max_tokens < 0) return false;
-    const uint64_t slots = (uint64_t)s->max_tokens * (uint64_t)s->num_topk;
-    if (slots >= (1ull << 31)) return false;
-    const uint64_t ppad = slots + (uint64_t)s->num_experts * (kMaxBlockM - 1);
-    // 32-bit row offsets inside the GEMM kernels
-    if ((uint64_t)s->max_tokens * (uint64_t)s->hidden >= (1ull << 32)) return false;
-    if (ppad * (uint64_t)s->intermediate >= (1ull << 32)) return false;
-    if (s->num_topk <= kDispatchCopyMaxTopk && ppad * (uint64_t)s->hidden >= (1ull << 32))
-        return false;
-    return true;
-}
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Row-tile class from the mean rows per expert; MOE_BLOCK_M (64, 128 or 256) overrides it
@@ -95,6 +77,25 @@ WsLayout ws_layout(const moe_shape_t& s) {
 }
 
 }  // namespace
+
+bool shape_ok(const moe_shape_t* s) {
+    if (!s) return false;
+    if (s->num_experts < 1 || s->num_experts > MOE_MAX_EXPERTS) return false;
+    if (s->hidden < 128 || s->hidden % 128 != 0) return false;
+    if (s->intermediate < 128 || s->intermediate % 128 != 0) return false;
+    if (s->num_topk < 1 || s->num_topk > MOE_MAX_TOPK || s->num_topk > s->num_experts) return false;
+    if (s->max_tokens < 0) return false;
+    const uint64_t slots = (uint64_t)s->max_tokens * (uint64_t)s->num_topk;
+    if (slots >= (1ull << 31)) return false;
+    const uint64_t ppad = slots + (uint64_t)s->num_experts * (kMaxBlockM - 1);
+    // 32-bit row offsets inside the GEMM kernels
+    if ((uint64_t)s->max_tokens * (uint64_t)s->hidden >= (1ull << 32)) return false;
+    if (ppad * (uint64_t)s->intermediate >= (1ull << 32)) return false;
+    if (s->num_topk <= kDispatchCopyMaxTopk && ppad * (uint64_t)s->hidden >= (1ull << 32))
+        return false;
+    return true;
+}
+
 }  // namespace moe
 
 using namespace moe;

@@ -47,6 +47,9 @@ __host__ __device__ inline uint32_t blocked_scale_word(uint32_t p, uint32_t w, u
 }
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// Whether the forward accepts the shape (moe_api.hip)
+bool shape_ok(const moe_shape_t* s);
+
 // Offsets of the four regions of the packed weight buffer.
 struct PackedLayout {
     size_t w1d, w1s, w2d, w2s, total;
@@ -157,6 +160,40 @@ hipError_t launch_cast_fp8(const uint16_t* x, int rows, int cols, uint8_t* q, ui
 hipError_t launch_gather(const uint8_t* x, const uint8_t* x_sf, const int32_t* perm,
                          const int32_t* meta, int k, int H, int sfs, int hblk, int max_rows,
                          uint8_t* xg, uint8_t* xg_sf, hipStream_t stream);
+
+// Top-k router (router.hip)
+hipError_t launch_router(const void* logits, int logits_type, int T, int E, int k, int over_all, float scale,
+                         int32_t* idx, float* w, hipStream_t stream);
+
+// The forward of a few tokens (few.hip): workspace regions and launches
+struct FewLayout {
+    size_t h8, h_sf, total;
+};
+FewLayout few_layout(const moe_shape_t& s);
+hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t* x, const uint8_t* x_sf,
+                      const int32_t* idx, const float* weights, int T, const uint8_t* packed, uint8_t* ws, uint16_t* y,
+                      hipStream_t stream);
+
+// FP8 x FP8 GEMM with 128-block scales (gemm_fp8.hip)
+struct GemmFp8Args {
+    const uint8_t* a;          // e4m3 rows of K bytes
+    const uint8_t* a_sf;       // rows of sf_stride UE8M0 bytes
+    const uint8_t* b;          // e4m3 [G][N][K]
+    const uint8_t* b_sf;       // [G][ceil(N/128)][sf_stride]
+    int K, N;
+    int sf_stride;             // 4*ceil(K/512)
+    // Row tiles: dense_rows > 0: rows 0 .. dense_rows-1 in tiles of block_m; otherwise the
+    // lists of the routing (perm: A and D row of each padded row, -1 padding)
+    int dense_rows;
+    const int32_t* perm;
+    const int32_t* meta;
+    const int32_t* tile_expert;
+    const int32_t* tile_row0;
+    int max_tiles;
+    void* d;
+    int out_f32;
+};
+hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream);
 
 // Combine (combine.hip)
 hipError_t launch_combine(const uint16_t* stage, const int32_t* topk_idx, const float* topk_weights,

@@ -1,0 +1,70 @@
+/*
+ * fp8_gemm.h -- C ABI of the FP8 x FP8 GEMMs with one scale per block of 128, in the same
+ * library as the MoE forward (libmoe.so, MI355X / gfx950): the FP8-weight counterparts of the
+ * FP8 x FP4 GEMMs of fp8_fp4_gemm.h (zevenfang.github.io 2026/04/23 section 二: the dense,
+ * M-grouped contiguous and M-grouped masked families; chenxutan.com/d/1930 section 11.1: a
+ * scale per block; section 4.2: FP32 accumulation).
+ *
+ *   D[m, n] = sum over k of  A[m, k] * 2^(a_sf[m, k/128] - 127)
+ *                          * B[n, k] * 2^(b_sf[n/128, k/128] - 127)
+ *
+ * Formats: A is OCP e4m3fn, rows of K bytes, with UE8M0 bytes per 1x128 block along K,
+ * 4*ceil(K/512) bytes per row, as moe_cast_to_fp8 writes them. B is e4m3fn [G][N][K], read as
+ * it is (no packing), with one UE8M0 byte per 128x128 block, [G][ceil(N/128)][4*ceil(K/512)]
+ * (byte j of a row = block j along K; bytes past K/128 are ignored). D is bf16 (the FP32 sum
+ * rounded once to nearest even) or FP32, as d_type (MOE_BF16, MOE_F32 of moe_serving.h) says.
+ *
+ * Shapes: K a positive multiple of 128, at most 2^22; N any positive number; G (groups) in
+ * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); B of any size.
+ *
+ * Memory, errors and streams as in moe.h: device pointers, 16-byte aligned, owned by the
+ * caller; host-detectable problems return a negative MOE_ERR_* status before any launch;
+ * every call is asynchronous on `stream`. Calls that share a workspace must not overlap.
+ * Results are deterministic.
+ */
+#ifndef MOE_FP8_GEMM_H
+#define MOE_FP8_GEMM_H
+
+#include "moe.h"
+#include "moe_serving.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Workspace bytes of a call whose A has up to `max_rows` rows in `groups` groups (dense: m
+ * rows, 1 group; contiguous: m rows; masked: groups * max_m rows). Holds the row and tile
+ * lists and a fixed area for the FP32 partial sums of products whose K is split over several
+ * workgroups (added in a fixed order). Contents need no initialisation. 0 if unsupported. */
+size_t moe_fp8_gemm_workspace_bytes(int32_t max_rows, int32_t groups);
+
+/* Dense: d [m][n] = A [m][k] . B [n][k]^T. m = 0 launches nothing. */
+int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, int32_t m,
+                 int32_t n, int32_t k, const uint8_t* b, const uint8_t* b_sf, void* workspace,
+                 size_t workspace_bytes, hipStream_t stream);
+
+/* M-grouped, contiguous layout: row r of A is multiplied by B[group_of_row[r]].
+ *   group_of_row  i32 [m] device; rows whose id is outside [0, groups) are skipped, their D
+ *                 rows not written. Rows of one group need not be adjacent or aligned. */
+int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
+                                      const uint8_t* a_sf, const int32_t* group_of_row,
+                                      int32_t m, int32_t groups, int32_t n, int32_t k,
+                                      const uint8_t* b, const uint8_t* b_sf, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* M-grouped, masked layout: for each group g and i < clamp(masked_m[g], 0, max_m),
+ * d[g, i, :] = A[g, i, :] . B[g]^T; other rows of d are not written.
+ *   a u8 [groups][max_m][k], a_sf u8 [groups][max_m][4*ceil(k/512)], d [groups][max_m][n]
+ *   masked_m  i32 [groups] device (read on the device: the call never synchronises)
+ *   expected_m  the expected rows per group, a hint that picks the row-tile size. */
+int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
+                                  const int32_t* masked_m, int32_t groups, int32_t max_m,
+                                  int32_t expected_m, int32_t n, int32_t k, const uint8_t* b,
+                                  const uint8_t* b_sf, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_FP8_GEMM_H */

@@ -6,3 +6,4 @@ library and its binding) never does, and this package never imports the product.
 """
 from .moe_oracle import *  # noqa: F401,F403
 from .gemm_oracle import *  # noqa: F401,F403
+from .serving_oracle import *  # noqa: F401,F403

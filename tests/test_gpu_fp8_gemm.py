@@ -1,0 +1,221 @@
+"""GPU parity of the FP8 x FP8 GEMMs (dense, M-grouped contiguous, masked) with 128-block scales.
+
+Acceptance of FP32 outputs, as the FP8 x FP4 GEMMs': each element within the FP32 accumulation
+bound of the exact sum, gamma_{K-1} * sum |a b|, and one rounding (2^-24 relative).
+
+bf16 outputs may run on the FP8 matrix instruction, which adds the products of each 8 consecutive
+K after aligning them to the largest of the 8, dropping what lies more than 13 bits below the
+largest one's leading bit (a property of gfx950's unit, measured with one large and one small product).
+Each of the 8 is then off by less than 2^-13 of the group's largest product, the group by less than
+8 * 2^-13 of it, and the largest product is at most max|a| max|b| over the group; so the bound
+gains 2^-10 * sum over groups of max|a| max|b|, plus bf16's half step (2^-8 relative).
+
+Rows and columns that must not be written keep the poison value."""
+import numpy as np
+import pytest
+import torch
+
+from conftest import gpu_available
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+import block_scaled_fp8_dispatch_amd as moe  # noqa: E402
+import oracle  # noqa: E402
+
+POISON = {moe.MOE_BF16: 0x7FBF, moe.MOE_F32: 0x7FBFBFBF}
+
+
+def make(rows, N, K, G=1, seed=0):
+    """e4m3 codes of every magnitude and scale bytes spread over 2^-6 .. 2^6, on the host."""
+    rng = np.random.default_rng(seed)
+
+    def codes(*shape):
+        c = rng.integers(0, 256, shape).astype(np.uint8)
+        c[(c & 0x7F) == 0x7F] = 0x38
+        return c
+
+    sfw = 4 * -(-K // 512)
+    a_sf = rng.integers(121, 134, (rows, sfw)).astype(np.uint8)
+    b_sf = rng.integers(121, 134, (G, -(-N // 128), sfw)).astype(np.uint8)
+    # bytes past K/128 are ignored: any value, NaN's included
+    a_sf[:, K // 128:] = 255
+    b_sf[:, :, K // 128:] = 255
+    return codes(rows, K), a_sf, codes(G, N, K), b_sf
+
+
+def alignment_bound(a, a_sf, b, b_sf, K):
+    A = np.abs(oracle.dequant_fp8_rows(a, a_sf, K)).reshape(len(a), K // 8, 8).max(2)
+    B = np.abs(oracle.dequant_fp8_blocks(b, b_sf, K)).reshape(len(b), K // 8, 8).max(2)
+    return 2.0 ** -10 * (A @ B.T)
+
+
+class Problem:
+    def __init__(self, rows, N, K, G, d_type, seed=0):
+        self.rows, self.N, self.K, self.G, self.d_type = rows, N, K, G, d_type
+        self.a, self.a_sf, self.b, self.b_sf = make(rows, N, K, G, seed)
+        self.dev = [torch.from_numpy(v).cuda() for v in (self.a, self.a_sf, self.b, self.b_sf)]
+        self.ws = torch.empty(moe.moe_fp8_gemm_workspace_bytes(rows, G), dtype=torch.uint8, device="cuda")
+        # guard elements past the end catch stores beyond the last one
+        ty = torch.int32 if d_type == moe.MOE_F32 else torch.int16
+        self.d = torch.empty(rows * N + 512, dtype=ty, device="cuda")
+
+    def _done(self):
+        torch.cuda.synchronize()
+        out = self.d.cpu().numpy()
+        assert (out[self.rows * self.N:] == POISON[self.d_type]).all(), "a store went past the end"
+        out = out[: self.rows * self.N].reshape(self.rows, self.N)
+        return out.view(np.uint32 if self.d_type == moe.MOE_F32 else np.uint16)
+
+    def _clear(self):
+        self.d.fill_(POISON[self.d_type])
+        self.ws.fill_(0xFF)
+
+    def dense(self):
+        self._clear()
+        a, a_sf, b, b_sf = self.dev
+        moe.moe_fp8_gemm(self.d, self.d_type, a, a_sf, self.rows, self.N, self.K, b, b_sf, self.ws)
+        return self._done()
+
+    def contiguous(self, grp):
+        self._clear()
+        a, a_sf, b, b_sf = self.dev
+        moe.moe_m_grouped_fp8_gemm_contiguous(self.d, self.d_type, a, a_sf, torch.from_numpy(grp).cuda(), self.rows, self.G,
+                                              self.N, self.K, b, b_sf, self.ws)
+        return self._done()
+
+    def masked(self, cnt, max_m, expected_m):
+        self._clear()
+        a, a_sf, b, b_sf = self.dev
+        moe.moe_m_grouped_fp8_gemm_masked(self.d, self.d_type, a, a_sf, torch.from_numpy(cnt).cuda(), self.G, max_m,
+                                          expected_m, self.N, self.K, b, b_sf, self.ws)
+        return self._done()
+
+    def alignment(self, rows, g):
+        return alignment_bound(self.a[rows], self.a_sf[rows], self.b[g], self.b_sf[g], self.K)
+
+    def check(self, d, rows, g=0):
+        """d[rows] against the oracle's product of those rows with group g's B."""
+        rows = np.asarray(rows)
+        if len(rows) == 0:
+            return
+        ref = oracle.fp8_gemm(self.a[rows], self.a_sf[rows], self.b[g], self.b_sf[g], self.K)
+        if self.d_type == moe.MOE_F32:
+            ok = oracle.gemm_f32_within_bound(d[rows].view(np.float32), ref["exact"], ref["bound"])
+        else:
+            ok = oracle.gemm_bf16_within_bound(d[rows], ref["exact"], ref["bound"] + self.alignment(rows, g))
+        assert ok.all(), f"{(~ok).sum()} of {ok.size} off, first at {np.argwhere(~ok)[0]} of group {g}"
+
+
+@pytest.mark.parametrize("d_type", [moe.MOE_BF16, moe.MOE_F32])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 128), (1, 16, 128), (2, 7, 256), (77, 273, 384), (64, 64, 512), (65, 129, 640), (33, 256, 2048),
+    (128, 32, 7168), (130, 511, 1152), (200, 1040, 4096), (256, 256, 128), (257, 300, 256), (1000, 528, 1152),
+    (31, 2049, 1024), (16, 513, 5120), (600, 255, 896), (5, 100, 18432), (513, 777, 1664), (1024, 1280, 640),
+])
+def test_dense(M, N, K, d_type):
+    print(f"[fp8] dense {M} {N} {K} {d_type}", flush=True)
+    p = Problem(M, N, K, 1, d_type, seed=M + N)
+    d = p.dense()
+    p.check(d, np.arange(M))
+    assert np.array_equal(p.dense(), d), "two calls gave different bytes"
+
+
+@pytest.mark.parametrize("d_type", [moe.MOE_BF16, moe.MOE_F32])
+@pytest.mark.parametrize("M,N,K,G", [(700, 512, 512, 3), (90, 129, 256, 5), (5000, 264, 384, 7), (1, 40, 128, 2),
+                                     (2600, 520, 640, 2)])
+def test_contiguous(M, N, K, G, d_type):
+    print(f"[fp8] contiguous {M} {N} {K} {G} {d_type}", flush=True)
+    p = Problem(M, N, K, G, d_type, seed=M)
+    rng = np.random.default_rng(M)
+    grp = rng.integers(0, G, size=M).astype(np.int32)            # interleaved, unaligned
+    grp[rng.random(M) < 0.1] = -1
+    if M > 400:
+        grp[[5, 6, 400]] = [G, -9, 1 << 30]                      # outside [0, G): skipped
+        grp[grp == 1] = 0                                        # an empty group
+    d = p.contiguous(grp)
+    for g in range(G):
+        p.check(d, np.nonzero(grp == g)[0], g)
+    skipped = np.nonzero((grp < 0) | (grp >= G))[0]
+    assert (d[skipped] == POISON[p.d_type]).all(), "a skipped row was written"
+    none = p.contiguous(np.full(M, -1, dtype=np.int32))
+    assert (none == POISON[p.d_type]).all()
+
+
+@pytest.mark.parametrize("d_type", [moe.MOE_BF16, moe.MOE_F32])
+@pytest.mark.parametrize("G,max_m,N,K", [(5, 70, 272, 640), (3, 300, 150, 384), (9, 1, 33, 256), (2, 700, 512, 1280)])
+def test_masked(G, max_m, N, K, d_type):
+    print(f"[fp8] masked {G} {max_m} {N} {K} {d_type}", flush=True)
+    p = Problem(G * max_m, N, K, G, d_type, seed=G)
+    cnt = np.random.default_rng(G).integers(0, max_m + 1, size=G).astype(np.int32)
+    cnt[0], cnt[1] = -4, max_m + 100                             # clamped
+    c = np.clip(cnt, 0, max_m)
+    first = None
+    for em in (1, 33, 200, 600, 4096):
+        d = p.masked(cnt, max_m, em)
+        for g in range(G):
+            p.check(d, g * max_m + np.arange(c[g]), g)
+            assert (d[g * max_m + c[g]: (g + 1) * max_m] == POISON[p.d_type]).all(), "a row past the count was written"
+        first = d if first is None else first
+    assert np.array_equal(p.masked(cnt, max_m, 1), first), "two calls gave different bytes"
+    assert (p.masked(np.zeros(G, dtype=np.int32), max_m, 8) == POISON[p.d_type]).all()
+
+
+def test_most_groups():
+    G, N, K = 1024, 40, 256
+    p = Problem(G * 3, N, K, G, moe.MOE_BF16, seed=9)
+    cnt = np.random.default_rng(1).integers(-1, 4, size=G).astype(np.int32)
+    d = p.masked(cnt, 3, 1)
+    c = np.clip(cnt, 0, 3)
+    for g in range(0, G, 37):
+        p.check(d, g * 3 + np.arange(c[g]), g)
+    rows = np.arange(G * 3)
+    assert (d[(rows % 3) >= c[rows // 3]] == POISON[moe.MOE_BF16]).all()
+
+
+@pytest.mark.parametrize("M", [3, 40, 300, 700])
+def test_nan_and_extreme_scales_stay_in_place(M):
+    """A NaN code or a NaN scale byte reaches its row (A) or its column / 128-column block (B) only; a
+    padding row's contents reach nothing; scales 2^-60 and 2^60 cancel exactly."""
+    N, K = 300, 512
+    p = Problem(M, N, K, 1, moe.MOE_F32, seed=M)
+    clean = p.dense().view(np.float32)
+    a, a_sf, b, b_sf = (v.clone() for v in p.dev)
+    a[1, 200] = 0x7F
+    a_sf[2, 3] = 255
+    b[0, 17, 5] = 0xFF
+    b_sf[0, 2, 1] = 255
+    p.dev = [a, a_sf, b, b_sf]
+    d = p.dense().view(np.float32)
+    bad = np.zeros((M, N), dtype=bool)
+    bad[[1, 2]] = True
+    bad[:, 17] = True
+    bad[:, 256:] = True
+    assert np.isnan(d[bad]).all()
+    assert np.array_equal(d[~bad], clean[~bad])
+    a, a_sf, b, b_sf = Problem(M, N, K, 1, moe.MOE_F32, seed=M).dev
+    p.dev = [a, a_sf[:, :] - 60, b, b_sf[:, :] + 60]
+    assert np.array_equal(p.dense().view(np.float32), clean)
+
+
+def test_b_beyond_4gb():
+    """B above 4 GiB: the last groups lie past 32-bit byte offsets from its start."""
+    G, N, K = 150, 4096, 7168
+    b = torch.randint(0, 0x7E, (G, N, K), dtype=torch.uint8, device="cuda")
+    b_sf = torch.randint(121, 134, (G, N // 128, 4 * (K // 512)), dtype=torch.uint8, device="cuda")
+    assert b.numel() > 2 ** 32
+    ha, ha_sf, _, _ = make(G * 4, 16, K, seed=2)
+    a, a_sf = torch.from_numpy(ha).cuda(), torch.from_numpy(ha_sf).cuda()
+    cnt = torch.full((G,), 3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_fp8_gemm_workspace_bytes(G * 4, G), dtype=torch.uint8, device="cuda")
+    d = torch.full((G * 4, N), POISON[moe.MOE_BF16], dtype=torch.int16, device="cuda")
+    moe.moe_m_grouped_fp8_gemm_masked(d, moe.MOE_BF16, a, a_sf, cnt, G, 4, 3, N, K, b, b_sf, ws)
+    torch.cuda.synchronize()
+    out = d.cpu().numpy().view(np.uint16).reshape(G, 4, N)
+    for g in (0, 74, 146, 149):
+        args = (ha[g * 4: g * 4 + 3], ha_sf[g * 4: g * 4 + 3], b[g].cpu().numpy(), b_sf[g].cpu().numpy(), K)
+        ref = oracle.fp8_gemm(*args)
+        assert oracle.gemm_bf16_within_bound(out[g, :3], ref["exact"], ref["bound"] + alignment_bound(*args)).all()
+        assert (out[g, 3] == POISON[moe.MOE_BF16]).all()
+    del b, d
+    torch.cuda.empty_cache()
