@@ -309,7 +309,7 @@ int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     const GemmWs W = gemm_ws(m, 1);
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
-    const int BM = 64;
+    const int BM = d_type == MOE_F32 ? 64 : gemm_block_m(m);
     GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, static_cast<uint8_t*>(workspace), W, cdiv(m, BM));
     g.dense_rows = m;
     return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
@@ -329,7 +329,7 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = 64;
+    const int BM = d_type == MOE_F32 ? 64 : gemm_block_m(m / groups);
     auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
     if (launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets), i32(W.perm),
                      i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream) != hipSuccess)
@@ -354,7 +354,7 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = 64;
+    const int BM = d_type == MOE_F32 ? 64 : gemm_block_m(expected_m);
     if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
                            reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
                            reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)

@@ -9,9 +9,20 @@
 // at half its rate: an e4m3 value times its block's power of two is exact in bf16 (3 mantissa
 // bits of 7, the exponent range of FP32), and that instruction's sums are FP32's.
 //
-// A workgroup of 4 waves owns 64 rows x 64 columns, wave w rows 16w .. 16w+15. Operands go
-// from memory straight to registers in the instruction's layout: lane 16g + i holds bytes
-// [16g, 16g+16) and [64+16g, 64+16g+16) of row (column) i's 128.
+// Tiled kernel (bf16 outputs). A workgroup of 4 waves owns a BM x 256 tile of D. Both operands
+// of a K step (BM x 128 and 256 x 128 bytes) go straight from memory into LDS rings
+// (direct-to-LDS buffer loads, XOR-swizzled 16-byte chunks); rows of B are placed so that the
+// 16 rows of a fragment are adjacent and a lane ends up with adjacent columns of D. There is
+// one barrier per K step, before its last row of MFMAs: it waits for this wave's loads of the
+// next step. Behind it the next step's B fragments are read into the registers of the current
+// ones, each right after its last use, and the loads that refill the slots just freed go out,
+// one per MFMA, on into the next step: B of DB and A of DA steps ahead, so that a load has
+// DB - 1 (DA - 1) steps less that window to arrive. Scales come one 32-bit word per 4 K steps;
+// the instruction's byte select picks the step.
+//
+// Workgroups go round-robin to the 8 XCDs; each XCD owns a contiguous range of tile ids, which
+// walk groups of 4 row tiles across all column tiles, so the tiles resident on one XCD share
+// rows of A and B in its L2.
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -21,6 +32,7 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 
 __device__ inline v8i load_frag(const uint8_t* p) {
     const v4i lo = *reinterpret_cast<const v4i*>(p);
@@ -104,16 +116,317 @@ __global__ __launch_bounds__(256) void gemm_fp8_simple(GemmFp8Args p) {
     }
 }
 
+
+template <int N>
+struct IntC {
+    static constexpr int value = N;
+};
+
+constexpr int kRsrcWord3 = 0x00020000;   // raw buffer descriptor: byte offsets, no swizzle
+constexpr int kAllRecords = -1;
+constexpr int kGroupM = 4;
+#define MOE_LPTR(p) ((__attribute__((address_space(3))) void*)(p))
+
+// acc += A x B, both e4m3, scales from byte OPS of their words. As asm so that the accumulators
+// stay in their registers; the operands are only ever written by LDS or buffer loads, and the
+// kernel separates the accumulators' other accesses by s_nop, so no hazard needs padding.
+template <int OPS>
+__device__ inline void mfma_scaled(v4f& acc, const v8i& a, const v8i& b, uint32_t sa, uint32_t sb) {
+    if constexpr (OPS == 0)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                     : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+    else if constexpr (OPS == 1)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
+                     : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+    else if constexpr (OPS == 2)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0]"
+                     : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
+                     : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+}
+
+// Tile id of this workgroup: each XCD (workgroup id mod 8) owns a contiguous range of ids.
+// -1: none left.
+__device__ inline int xcd_tile(int total) {
+    const int xcd = blockIdx.x & 7, li = blockIdx.x >> 3;
+    const int per = total >> 3, rem = total & 7;
+    if (li >= per + (xcd < rem ? 1 : 0)) return -1;
+    return xcd * per + (xcd < rem ? xcd : rem) + li;
+}
+
+template <int BM, int WAVES_M, int WAVES_N>
+struct Fp8Cfg {
+    static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
+    static constexpr int FM = WM / 16, FN = WN / 16;
+    static constexpr int A_BYTES = BM * kBK, B_BYTES = kBN * kBK;
+    // ring slots: all of the CU's 160 KB
+    static constexpr int DB = BM == 256 ? 2 : BM == 128 ? 3 : 4;
+    static constexpr int DA = BM == 256 ? 3 : 4;
+    static constexpr int LDS_BYTES = DA * A_BYTES + DB * B_BYTES;
+    static constexpr int A_DMA = A_BYTES / 1024 / 4, B_DMA = B_BYTES / 1024 / 4;   // 1 KB loads per wave and step
+    static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024, "");
+    static_assert(DA == DB || DA == DB + 1, "issue order written for these");
+    static_assert(WN == 64 || WN == 128, "one scale block of B per wave");
+};
+
+template <int BM, int WAVES_M, int WAVES_N>
+__global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
+    // gfx950 buffer descriptors are a device-only type: the host pass sees an empty kernel
+#if defined(__HIP_DEVICE_COMPILE__)
+    using C = Fp8Cfg<BM, WAVES_M, WAVES_N>;
+    constexpr int WM = C::WM, WN = C::WN, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
+    constexpr int A_DMA = C::A_DMA, B_DMA = C::B_DMA;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
+    uint8_t* const bring = smem + DA * C::A_BYTES;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int g = lane >> 4, l = lane & 15;
+
+    // ---- tile ------------------------------------------------------------------------------
+    const bool dense = args.dense_rows > 0;
+    int num_mt = dense ? (args.dense_rows + BM - 1) / BM : __builtin_amdgcn_readfirstlane(args.meta[0]);
+    if (num_mt > args.max_tiles) num_mt = args.max_tiles;
+    const int NT = (args.N + kBN - 1) / kBN;
+    const int v = xcd_tile(num_mt * NT);
+    if (v < 0) return;
+    const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
+    const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
+    const int mt = mt0 + vin % gm, nt = vin / gm;
+    const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
+    const int row0 = dense ? mt * BM : __builtin_amdgcn_readfirstlane(args.tile_row0[mt]);
+    const int nks = args.K / kBK;
+    // A and D row of tile row r, -1 on padding
+    auto d_row = [&](int r) __attribute__((always_inline)) -> int {
+        if (dense) return row0 + r < args.dense_rows ? row0 + r : -1;
+        return args.perm[row0 + r];
+    };
+    auto a_row = [&](int r) __attribute__((always_inline)) -> uint32_t {
+        const int d = d_row(r);
+        return d < 0 ? 0u : (uint32_t)d;      // padding rows read row 0 and are never stored
+    };
+
+    // ---- per-lane offsets --------------------------------------------------------------------
+    // Load j of wave w fills LDS rows 8*(w*DMA + j) .. +7 of a tile; lane l lands at row + l/8,
+    // physical 16-byte chunk l%8, which holds logical chunk (l%8) ^ (row%8).
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    uint32_t a_off[A_DMA], b_off[B_DMA];
+#pragma unroll
+    for (int j = 0; j < A_DMA; ++j) a_off[j] = a_row(8 * (wave * A_DMA + j) + (lane >> 3)) * (uint32_t)args.K + chunk * 16;
+    // LDS row 16*f + j of B (fragment f, lane column j) is column base + j*FN + f%FN of D, so that
+    // a lane's FN fragments hold FN adjacent columns; rows past N read row N-1 and are not stored
+#pragma unroll
+    for (int j = 0; j < B_DMA; ++j) {
+        const int r = 8 * (wave * B_DMA + j) + (lane >> 3);
+        const int f = r >> 4;
+        const int n = nt * kBN + (f / FN) * WN + (r & 15) * FN + f % FN;
+        b_off[j] = (uint32_t)(min(n, args.N - 1) - nt * kBN) * (uint32_t)args.K + chunk * 16;
+    }
+    uint32_t sa_off[FM];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)args.sf_stride;
+    const int nblk = (args.N + 127) / 128;
+    const int blk = min((nt * kBN + wn * WN) >> 7, nblk - 1);
+    const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)args.a, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)args.a_sf, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(args.b + ((size_t)group * args.N + (size_t)nt * kBN) * args.K), 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(args.b_sf + ((size_t)group * nblk + blk) * args.sf_stride), 0, kAllRecords, kRsrcWord3);
+
+    auto load_a = [&](int ks, int j) __attribute__((always_inline)) {
+        const int kc = min(ks, nks - 1);      // steps past the last reload it into a free slot
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, MOE_LPTR(smem + (ks % DA) * C::A_BYTES + (wave * A_DMA + j) * 1024), 16,
+                                                 a_off[j], kc * kBK, 0, 0);
+    };
+    auto load_b = [&](int ks, int j) __attribute__((always_inline)) {
+        const int kc = min(ks, nks - 1);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(bring + (ks % DB) * C::B_BYTES + (wave * B_DMA + j) * 1024), 16,
+                                                 b_off[j], kc * kBK, 0, 0);
+    };
+    uint32_t sa[2][FM], sb[2];
+    auto load_scale = [&](int kb, int i, int set) __attribute__((always_inline)) {
+        if (i < FM) sa[set][i] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[i], kb * 4, 0);
+        else sb[set] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, 0, kb * 4, 0);
+    };
+    const uint32_t rd_lo = (uint32_t)(l * kBK + ((g ^ (l & 7)) << 4));
+    const uint32_t rd_hi = (uint32_t)(l * kBK + (((g + 4) ^ (l & 7)) << 4));
+    auto read = [&](const uint8_t* p) __attribute__((always_inline)) -> v8i {
+        const v4i lo = *reinterpret_cast<const v4i*>(p + rd_lo);
+        const v4i hi = *reinterpret_cast<const v4i*>(p + rd_hi);
+        return (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    };
+    auto read_a = [&](int ks, int f) __attribute__((always_inline)) -> v8i {
+        return read(smem + (ks % DA) * C::A_BYTES + (wm * FM + f) * 16 * kBK);
+    };
+    auto read_b = [&](int ks, int f) __attribute__((always_inline)) -> v8i {
+        return read(bring + (ks % DB) * C::B_BYTES + (wn * FN + f) * 16 * kBK);
+    };
+
+    v4f acc[FM][FN];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) {
+            acc[fm][fn] = (v4f){0.f, 0.f, 0.f, 0.f};
+            asm volatile("" : "+a"(acc[fm][fn]));
+        }
+    asm volatile("s_nop 7" ::: "memory");   // accumulator writes -> first MFMA
+
+    // prologue: the scale words of block 0, then the loads that the steps before step 0 would
+    // have issued (step s: B of s+DB, then A of s+DA)
+    constexpr int NS = FM + 1, SOPS = 4 - DB;
+    const int last_kb = (nks - 1) >> 2;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) load_scale(0, i, 0);
+    if constexpr (DA == DB + 1) {
+#pragma unroll
+        for (int j = 0; j < A_DMA; ++j) load_a(0, j);
+    }
+#pragma unroll
+    for (int s = 0; s < DB - 1; ++s) {
+#pragma unroll
+        for (int j = 0; j < B_DMA; ++j) load_b(s, j);
+#pragma unroll
+        for (int j = 0; j < A_DMA; ++j) load_a(s + DA - DB, j);
+    }
+    // of the step before step 0 only what goes out in its last row; step 0 issues the rest
+#pragma unroll
+    for (int op = 0; op < FN; ++op) {
+        if (op < B_DMA) load_b(DB - 1, op);
+        else if (op < B_DMA + A_DMA) load_a(DA - 1, op - B_DMA);
+    }
+    // everything after A and B of step 0
+    constexpr int PART = FN < A_DMA + B_DMA ? FN : A_DMA + B_DMA;
+    constexpr int WAIT0 = PART + (DB - 2) * (A_DMA + B_DMA) + (DA == DB ? 0 : A_DMA);
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (WAIT0 & 15) | (((WAIT0 >> 4) & 3) << 14));
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(WAIT0) : "memory");
+    v8i bq[FN], a_cur, a_nx;
+#pragma unroll
+    for (int f = 0; f < FN; ++f) bq[f] = read_b(0, f);
+    a_nx = read_a(0, 0);
+
+    // One K step. Its barrier stands before the last row of MFMAs: this wave's loads of step
+    // ks+1 have landed (in flight may be what was issued after B of ks+1), its LDS reads of step
+    // ks are done. Then go, one per MFMA, through the rest of this step and the next one's
+    // first rows, the loads into the slots that are free now.
+    // One K step. Its barrier stands before the last row of MFMAs: this wave's loads of step
+    // ks+1 have landed (in flight may be what was issued after B of ks+1), its LDS reads of step
+    // ks are done. Then go, one per MFMA, through the last row and the next step's first rows,
+    // the loads into the slots that are free now: the next block's scale words (in one step
+    // of four), B of step ks+DB, A of step ks+DA.
+    auto step = [&](int ks, auto ops_c, auto set_c) __attribute__((always_inline)) {
+        constexpr int OPS = decltype(ops_c)::value, SET = decltype(set_c)::value;
+        auto issue = [&](int kp, int ns, int op) __attribute__((always_inline)) {
+            if (op < ns) load_scale(min((kp >> 2) + 1, last_kb), op, SET ^ 1);
+            else if (op < ns + B_DMA) load_b(kp + DB, op - ns);
+            else if (op < ns + B_DMA + A_DMA) load_a(kp + DA, op - ns - B_DMA);
+        };
+        constexpr int NS_HERE = OPS == SOPS ? NS : 0, NS_PREV = (OPS + 3) % 4 == SOPS ? NS : 0;
+        static_assert(NS + B_DMA + A_DMA <= FM * FN, "a step's loads fit between its MFMAs");
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+            if (fm == FM - 1) {
+                // issued after B of step ks+1: its A (where A runs further ahead), and the issues
+                // of steps ks+2-DB .. ks-1
+                constexpr int SCW = DB >= 3 && (OPS + 3) % 4 == SOPS ? NS : DB >= 4 && (OPS + 2) % 4 == SOPS ? NS : 0;
+                constexpr int WN_ = (DA == DB ? 0 : A_DMA) + (DB - 2) * (A_DMA + B_DMA) + SCW;
+                static_assert(WN_ < 64, "vmcnt range");
+                __builtin_amdgcn_s_waitcnt(0x0070 | (WN_ & 15) | (((WN_ >> 4) & 3) << 14));
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
+            }
+            a_cur = a_nx;
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) {
+                mfma_scaled<OPS>(acc[fm][fn], a_cur, bq[fn], sa[SET][fm], sb[SET]);
+                if (fn == 0) a_nx = fm + 1 < FM ? read_a(ks, fm + 1) : read_a(ks + 1, 0);
+                if (fm == FM - 1) {
+                    bq[fn] = read_b(ks + 1, fn);
+                    issue(ks, NS_HERE, fn);
+                } else {
+                    issue(ks - 1, NS_PREV, FN + fm * FN + fn);
+                }
+                __builtin_amdgcn_sched_barrier(0x7);
+            }
+        }
+    };
+
+    // 8 steps per iteration: two 4-step scale blocks, one per scale set
+    int ks0 = 0;
+    for (; ks0 + 8 <= nks; ks0 += 8) {
+        step(ks0, IntC<0>{}, IntC<0>{});
+        step(ks0 + 1, IntC<1>{}, IntC<0>{});
+        step(ks0 + 2, IntC<2>{}, IntC<0>{});
+        step(ks0 + 3, IntC<3>{}, IntC<0>{});
+        step(ks0 + 4, IntC<0>{}, IntC<1>{});
+        step(ks0 + 5, IntC<1>{}, IntC<1>{});
+        step(ks0 + 6, IntC<2>{}, IntC<1>{});
+        step(ks0 + 7, IntC<3>{}, IntC<1>{});
+    }
+    if (ks0 < nks) step(ks0, IntC<0>{}, IntC<0>{});
+    if (ks0 + 1 < nks) step(ks0 + 1, IntC<1>{}, IntC<0>{});
+    if (ks0 + 2 < nks) step(ks0 + 2, IntC<2>{}, IntC<0>{});
+    if (ks0 + 3 < nks) step(ks0 + 3, IntC<3>{}, IntC<0>{});
+    if (ks0 + 4 < nks) step(ks0 + 4, IntC<0>{}, IntC<1>{});
+    if (ks0 + 5 < nks) step(ks0 + 5, IntC<1>{}, IntC<1>{});
+    if (ks0 + 6 < nks) step(ks0 + 6, IntC<2>{}, IntC<1>{});
+    // the last steps' reloads must land before the workgroup's LDS is given back
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // the accumulators' reads stay behind the wait states that the last MFMA's result needs
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) asm volatile("" : "+a"(acc[fm][fn]));
+
+    // ---- epilogue: rows 16*fm + 4g + r, columns col0 .. col0 + FN-1 ----------------------------
+    const int col0 = nt * kBN + wn * WN + l * FN;
+    uint16_t* const d = static_cast<uint16_t*>(args.d);
+    const bool wide = args.N % 8 == 0;          // rows and chunks aligned, a chunk wholly in or out
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
+            if (row < 0) continue;
+            uint32_t pk[FN / 2];
+#pragma unroll
+            for (int q = 0; q < FN / 2; ++q) {
+                const v2f x = {acc[fm][2 * q][r], acc[fm][2 * q + 1][r]};
+                pk[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
+            }
+            uint16_t* dst = d + (size_t)row * args.N + col0;
+            if (wide) {
+                if (col0 < args.N) {
+                    if constexpr (FN == 8) *reinterpret_cast<v4i*>(dst) = (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]};
+                    else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < FN; ++q)
+                    if (col0 + q < args.N) dst[q] = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
+            }
+        }
+    }
+#endif
+}
+
 }  // namespace
 
 hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream) {
-    const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, 64) : a.max_tiles;
-    const size_t grid = mt * (size_t)cdiv(a.N, 64);
-    if (grid == 0) return hipSuccess;
-    if (a.out_f32)
+    const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, block_m) : a.max_tiles;
+    if (a.out_f32) {
+        const size_t grid = mt * (size_t)cdiv(a.N, 64);
         gemm_fp8_simple<true><<<(unsigned)grid, 256, 0, stream>>>(a);
-    else
-        gemm_fp8_simple<false><<<(unsigned)grid, 256, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    // one workgroup per possible tile; those past the tiles in use return at once
+    const size_t grid = mt * (size_t)cdiv(a.N, kBN);
+    if (block_m == 256) gemm_fp8_tiled<256, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else if (block_m == 128) gemm_fp8_tiled<128, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else gemm_fp8_tiled<64, 1, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
