@@ -167,7 +167,7 @@ hipError_t launch_router(const void* logits, int logits_type, int T, int E, int 
 
 // The forward of a few tokens (few.hip): workspace regions and launches
 struct FewLayout {
-    size_t h8, h_sf, total;
+    size_t h8, h_sf, rows, segs, n_used, total;
 };
 FewLayout few_layout(const moe_shape_t& s);
 hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t* x, const uint8_t* x_sf,

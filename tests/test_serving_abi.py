@@ -35,7 +35,7 @@ def test_router_refusals():
 def test_few_sizes_and_refusals():
     s = moe.make_shape(32, 7168, 2048, 8, 64)
     nb = moe.moe_few_workspace_bytes(s)
-    assert nb == 32 * 8 * 2048 + 32 * 8 * 16
+    assert nb >= 32 * 8 * 2048 + 32 * 8 * 16
     assert nb <= moe.moe_workspace_bytes(s)
     assert moe.moe_few_workspace_bytes(moe.make_shape(32, 7168, 2048, 8, 3)) < nb
     for shape in (moe.make_shape(4, 128, 128, 2, 1), moe.make_shape(1024, 256, 384, 64, 40), moe.make_shape(8, 640, 128, 1, 7)):
