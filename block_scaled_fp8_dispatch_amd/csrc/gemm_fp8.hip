@@ -34,11 +34,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
-__device__ inline v8i load_frag(const uint8_t* p) {
-    const v4i lo = *reinterpret_cast<const v4i*>(p);
-    const v4i hi = *reinterpret_cast<const v4i*>(p + 64);
-    return (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-}
+constexpr int kGroupM = 4;
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -56,66 +52,14 @@ __device__ inline v8bf to_bf16(int w0, int w1, float scale) {
     return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void gemm_fp8_simple(GemmFp8Args p) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, l = lane & 15;
-    const int NT = (p.N + 63) / 64;
-    const int mt = (int)(blockIdx.x / NT), nt = (int)(blockIdx.x % NT);
-    const bool dense = p.dense_rows > 0;
-    if (!dense && mt >= min(p.meta[0], p.max_tiles)) return;
-    const int group = dense ? 0 : p.tile_expert[mt];
-    const int row0 = dense ? mt * 64 : p.tile_row0[mt];
-    auto d_row = [&](int r) { return dense ? (row0 + r < p.dense_rows ? row0 + r : -1) : p.perm[row0 + r]; };
-    const int ar = d_row(16 * wave + l);
-    const size_t arow = ar < 0 ? 0 : (size_t)ar;      // padding rows read row 0 and are not stored
-    const uint8_t* a = p.a + arow * p.K + 16 * g;
-    const uint8_t* sa = p.a_sf + arow * p.sf_stride;
-    const uint8_t *b[4], *sb[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const int n = min(nt * 64 + 16 * f + l, p.N - 1);
-        b[f] = p.b + ((size_t)group * p.N + n) * p.K + 16 * g;
-        sb[f] = p.b_sf + ((size_t)group * ((p.N + 127) / 128) + n / 128) * p.sf_stride;
-    }
-    v4f acc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = (v4f){0.f, 0.f, 0.f, 0.f};
-    for (int ks = 0; ks < p.K / 128; ++ks) {
-        const v8i av = load_frag(a + ks * 128);
-        const int s = sa[ks];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const v8i bv = load_frag(b[f] + ks * 128);
-            if constexpr (F32) {
-                // the same 8 consecutive codes of a lane on both sides: any order of K will do
-#pragma unroll
-                for (int q = 0; q < 8; q += 2)
-                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(av[q], av[q + 1], scale_f32(s)),
-                                                                     to_bf16(bv[q], bv[q + 1], scale_f32(sb[f][ks])), acc[f],
-                                                                     0, 0, 0);
-            } else {
-                acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[f], 0, 0, 0, s, 0, (int)sb[f][ks]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int row = d_row(16 * wave + 4 * g + r);
-        if (row < 0) continue;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int n = nt * 64 + 16 * f + l;
-            if (n >= p.N) continue;
-            if constexpr (F32)
-                static_cast<float*>(p.d)[(size_t)row * p.N + n] = acc[f][r];
-            else
-                static_cast<uint16_t*>(p.d)[(size_t)row * p.N + n] = __builtin_bit_cast(uint16_t, (__bf16)acc[f][r]);
-        }
-    }
+// Workgroups go round-robin to the XCDs: tile id of this workgroup with each XCD (workgroup id
+// mod 8) owning a contiguous range of ids. -1: none left.
+__device__ inline int xcd_tile(int total) {
+    const int xcd = blockIdx.x & 7, li = blockIdx.x >> 3;
+    const int per = total >> 3, rem = total & 7;
+    if (li >= per + (xcd < rem ? 1 : 0)) return -1;
+    return xcd * per + (xcd < rem ? xcd : rem) + li;
 }
-
 
 template <int N>
 struct IntC {
@@ -124,8 +68,209 @@ struct IntC {
 
 constexpr int kRsrcWord3 = 0x00020000;   // raw buffer descriptor: byte offsets, no swizzle
 constexpr int kAllRecords = -1;
-constexpr int kGroupM = 4;
 #define MOE_LPTR(p) ((__attribute__((address_space(3))) void*)(p))
+
+// Skinny kernel: few rows, or too few tiles for the tiled kernel. A workgroup owns a BM x BN tile
+// of D and its WAVES waves share K, wave w taking steps w, w + WAVES, ... and keeping sums of its
+// own. Each wave fills two LDS slots of its own (rows of A and B as the tiled kernel lays them
+// out), so there is no barrier before the end: it waits for the older slot, reads and multiplies
+// it, and refills it two of its steps ahead. The waves' sums meet in LDS, the upper half of the
+// waves onto the lower, then those in wave order.
+//
+// Operands straight from memory to registers instead were tried: a fragment read takes half a
+// line of 16 rows at a time, and the chunks in flight do not fit the registers.
+template <int BM, int BN, int WAVES>
+struct SkinnyCfg {
+    static constexpr int FM = BM / 16, FN = BN / 16;
+    static constexpr int SLOT = (BM + BN) * kBK;
+    static constexpr int A_DMA = BM / 8, B_DMA = BN / 8, NS = FM + 1;
+    static constexpr int PITCH = BN + 4;           // floats per row of a wave's sums
+    static constexpr int LDS_BYTES = 2 * WAVES * SLOT;
+    static_assert(LDS_BYTES <= 160 * 1024 && BN <= 128, "");
+    static_assert(WAVES / 2 * BM * PITCH * 4 <= LDS_BYTES, "the sums reuse the slots");
+};
+
+template <int BM, int BN, int WAVES, bool F32>
+__global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using C = SkinnyCfg<BM, BN, WAVES>;
+    constexpr int FM = C::FM, FN = C::FN, SUB = 64 / BM, PITCH = C::PITCH;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, l = lane & 15;
+    const bool dense = p.dense_rows > 0;
+    int num_mt = dense ? (p.dense_rows + 63) / 64 : __builtin_amdgcn_readfirstlane(p.meta[0]);
+    if (num_mt > p.max_tiles) num_mt = p.max_tiles;
+    const int NT = (p.N + BN - 1) / BN;
+    const int v = xcd_tile(num_mt * SUB * NT);
+    if (v < 0) return;
+    // groups of 4 row tiles across all column tiles: their rows of A stay in the XCD's L2
+    const int set = v / (kGroupM * SUB * NT), mt0 = set * kGroupM, gm = min(kGroupM, num_mt - mt0) * SUB;
+    const int vin = v - set * kGroupM * SUB * NT;
+    const int mt = mt0 + vin % gm / SUB, sub = vin % gm % SUB, nt = vin / gm;
+    const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(p.tile_expert[mt]);
+    const int row0 = (dense ? mt * 64 : __builtin_amdgcn_readfirstlane(p.tile_row0[mt])) + sub * BM;
+    auto d_row = [&](int r) __attribute__((always_inline)) -> int {
+        if (dense) return row0 + r < p.dense_rows ? row0 + r : -1;
+        return p.perm[row0 + r];
+    };
+    auto a_row = [&](int r) __attribute__((always_inline)) -> uint32_t {
+        const int d = d_row(r);
+        return d < 0 ? 0u : (uint32_t)d;           // padding rows read row 0 and are never stored
+    };
+    // padding comes last in a row tile: nothing but padding here
+    if (__builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
+
+    uint8_t* const mine = smem + wave * 2 * C::SLOT;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    uint32_t a_off[C::A_DMA], b_off[C::B_DMA], sa_off[FM];
+#pragma unroll
+    for (int j = 0; j < C::A_DMA; ++j) a_off[j] = a_row(8 * j + (lane >> 3)) * (uint32_t)p.K + chunk * 16;
+#pragma unroll
+    for (int j = 0; j < C::B_DMA; ++j)
+        b_off[j] = (uint32_t)(min(nt * BN + 8 * j + (lane >> 3), p.N - 1) - nt * BN) * (uint32_t)p.K + chunk * 16;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa_off[f] = a_row(f * 16 + l) * (uint32_t)p.sf_stride;
+    const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)p.a_sf, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.b + ((size_t)group * p.N + (size_t)nt * BN) * p.K), 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.b_sf + ((size_t)group * ((p.N + 127) / 128) + nt * BN / 128) * p.sf_stride), 0, kAllRecords, kRsrcWord3);
+
+    uint32_t sa[2][FM], sb[2];
+    auto issue = [&](int ks, auto slot_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot_c)::value;
+        uint8_t* dst = mine + S * C::SLOT;
+#pragma unroll
+        for (int f = 0; f < FM; ++f) sa[S][f] = __builtin_amdgcn_raw_buffer_load_b8(rs_asf, sa_off[f], ks, 0);
+        sb[S] = __builtin_amdgcn_raw_buffer_load_b8(rs_bsf, 0, ks, 0);
+#pragma unroll
+        for (int j = 0; j < C::B_DMA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(dst + BM * kBK + j * 1024), 16, b_off[j], ks * kBK, 0, 0);
+#pragma unroll
+        for (int j = 0; j < C::A_DMA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, MOE_LPTR(dst + j * 1024), 16, a_off[j], ks * kBK, 0, 0);
+    };
+    const uint32_t rd_lo = (uint32_t)(l * kBK + ((g ^ (l & 7)) << 4));
+    const uint32_t rd_hi = (uint32_t)(l * kBK + (((g + 4) ^ (l & 7)) << 4));
+    auto read = [&](const uint8_t* q) __attribute__((always_inline)) -> v8i {
+        const v4i lo = *reinterpret_cast<const v4i*>(q + rd_lo);
+        const v4i hi = *reinterpret_cast<const v4i*>(q + rd_hi);
+        return (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    };
+    v4f acc[FM][FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+    const int nks = p.K / kBK;
+    // step ks of this wave, in slot S: wait until only the younger slot's loads (if any) are in
+    // flight, multiply, refill
+    auto step = [&](int ks, auto slot_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot_c)::value;
+        constexpr int W = C::NS + C::A_DMA + C::B_DMA;
+        static_assert(W < 64, "vmcnt range");
+        if (ks + WAVES < nks) {
+            __builtin_amdgcn_s_waitcnt(0x0F70 | (W & 15) | (((W >> 4) & 3) << 14));
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(W) : "memory");
+        } else {
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        const uint8_t* src = mine + S * C::SLOT;
+        if constexpr (F32) {
+            v8bf bv[FN][4];
+#pragma unroll
+            for (int n = 0; n < FN; ++n) {
+                const v8i w = read(src + (BM + n * 16) * kBK);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) bv[n][q] = to_bf16(w[2 * q], w[2 * q + 1], scale_f32((int)sb[S]));
+            }
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                const v8i w = read(src + f * 16 * kBK);
+                // the same 8 consecutive codes of a lane on both sides: any order of K will do
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v8bf av = to_bf16(w[2 * q], w[2 * q + 1], scale_f32((int)sa[S][f]));
+#pragma unroll
+                    for (int n = 0; n < FN; ++n)
+                        acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[n][q], acc[f][n], 0, 0, 0);
+                }
+            }
+        } else {
+            v8i bv[FN];
+#pragma unroll
+            for (int n = 0; n < FN; ++n) bv[n] = read(src + (BM + n * 16) * kBK);
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                const v8i av = read(src + f * 16 * kBK);
+#pragma unroll
+                for (int n = 0; n < FN; ++n)
+                    acc[f][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv[n], acc[f][n], 0, 0, 0, (int)sa[S][f], 0,
+                                                                                 (int)sb[S]);
+            }
+        }
+        if (ks + 2 * WAVES < nks) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the slot's reads are done
+            issue(ks + 2 * WAVES, slot_c);
+        }
+    };
+    if (wave < nks) issue(wave, IntC<0>{});
+    if (wave + WAVES < nks) issue(wave + WAVES, IntC<1>{});
+    for (int ks = wave; ks < nks; ks += 2 * WAVES) {
+        step(ks, IntC<0>{});
+        if (ks + WAVES < nks) step(ks + WAVES, IntC<1>{});
+    }
+    __syncthreads();                               // the sums reuse the slots of all waves
+    float* const sums = reinterpret_cast<float*>(smem);
+    auto at = [&](int w, int r, int n) __attribute__((always_inline)) -> float& { return sums[(w * BM + r) * PITCH + n]; };
+    if (wave >= WAVES / 2) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int n = 0; n < FN; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) at(wave - WAVES / 2, f * 16 + 4 * g + r, n * 16 + l) = acc[f][n][r];
+    }
+    __syncthreads();
+    if (wave < WAVES / 2) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int n = 0; n < FN; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) at(wave, f * 16 + 4 * g + r, n * 16 + l) += acc[f][n][r];
+    }
+    __syncthreads();
+    // four adjacent columns per thread
+    const bool wide = p.N % 4 == 0;                // rows and chunks aligned, a chunk wholly in or out
+    for (int i = tid; i < BM * BN / 4; i += WAVES * 64) {
+        const int r = i / (BN / 4), c = i % (BN / 4) * 4, n = nt * BN + c;
+        const int row = d_row(r);
+        if (row < 0 || n >= p.N) continue;
+        v4f x = *reinterpret_cast<const v4f*>(&at(0, r, c));
+#pragma unroll
+        for (int w = 1; w < WAVES / 2; ++w) x += *reinterpret_cast<const v4f*>(&at(w, r, c));
+        const size_t to = (size_t)row * p.N + n;
+        if constexpr (F32) {
+            float* d = static_cast<float*>(p.d) + to;
+            if (wide) *reinterpret_cast<v4f*>(d) = x;
+            else
+                for (int q = 0; q < 4 && n + q < p.N; ++q) d[q] = x[q];
+        } else {
+            uint16_t* d = static_cast<uint16_t*>(p.d) + to;
+            const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x.x, x.y}), v2bf));
+            const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x.z, x.w}), v2bf));
+            if (wide) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+            else
+                for (int q = 0; q < 4 && n + q < p.N; ++q) d[q] = (uint16_t)((q < 2 ? lo : hi) >> (16 * (q & 1)));
+        }
+    }
+#endif
+}
 
 // acc += A x B, both e4m3, scales from byte OPS of their words. As asm so that the accumulators
 // stay in their registers; the operands are only ever written by LDS or buffer loads, and the
@@ -144,15 +289,6 @@ __device__ inline void mfma_scaled(v4f& acc, const v8i& a, const v8i& b, uint32_
     else
         asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
                      : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
-}
-
-// Tile id of this workgroup: each XCD (workgroup id mod 8) owns a contiguous range of ids.
-// -1: none left.
-__device__ inline int xcd_tile(int total) {
-    const int xcd = blockIdx.x & 7, li = blockIdx.x >> 3;
-    const int per = total >> 3, rem = total & 7;
-    if (li >= per + (xcd < rem ? 1 : 0)) return -1;
-    return xcd * per + (xcd < rem ? xcd : rem) + li;
 }
 
 template <int BM, int WAVES_M, int WAVES_N>
@@ -415,18 +551,24 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 
 }  // namespace
 
+namespace {
+template <int BM, int BN, int WAVES>
+void launch_skinny(size_t tiles64, const GemmFp8Args& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(tiles64 * (64 / BM) * (size_t)cdiv(a.N, BN));
+    if (a.out_f32) gemm_fp8_skinny<BM, BN, WAVES, true><<<grid, WAVES * 64, 0, stream>>>(a);
+    else gemm_fp8_skinny<BM, BN, WAVES, false><<<grid, WAVES * 64, 0, stream>>>(a);
+}
+}  // namespace
+
 hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream) {
     const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, block_m) : a.max_tiles;
-    if (a.out_f32) {
-        const size_t grid = mt * (size_t)cdiv(a.N, 64);
-        gemm_fp8_simple<true><<<(unsigned)grid, 256, 0, stream>>>(a);
-        return hipGetLastError();
-    }
     // one workgroup per possible tile; those past the tiles in use return at once
     const size_t grid = mt * (size_t)cdiv(a.N, kBN);
     if (block_m == 256) gemm_fp8_tiled<256, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
     else if (block_m == 128) gemm_fp8_tiled<128, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
-    else gemm_fp8_tiled<64, 1, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else if (!a.out_f32 && grid >= 256) gemm_fp8_tiled<64, 1, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else if (mt * (size_t)cdiv(a.N, 64) >= 64) launch_skinny<64, 64, 4>(mt, a, stream);
+    else launch_skinny<32, 32, 8>(mt, a, stream);
     return hipGetLastError();
 }
 
