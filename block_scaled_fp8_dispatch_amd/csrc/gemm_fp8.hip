@@ -549,6 +549,156 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 #endif
 }
 
+// FP32 outputs with enough tiles: 128 x 256 of D per workgroup, 2 x 2 waves of 64 x 128, LDS rings of
+// three steps. Each step converts its operands to bf16 (exact) and feeds
+// v_mfma_f32_16x16x32_bf16. One barrier per step: behind it the loads of two steps ahead go into
+// the slot that every wave has finished reading.
+constexpr int kF32Rows = 128;
+
+__global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = kF32Rows, FM = 4, FN = 8, SLOTS = 3, A_BYTES = BM * kBK, B_BYTES = kBN * kBK;
+    constexpr int A_DMA = A_BYTES / 4096, B_DMA = B_BYTES / 4096;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[SLOTS * (A_BYTES + B_BYTES)];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int g = lane >> 4, l = lane & 15;
+    const bool dense = args.dense_rows > 0;
+    int num_mt = dense ? (args.dense_rows + BM - 1) / BM : __builtin_amdgcn_readfirstlane(args.meta[0]);
+    if (num_mt > args.max_tiles) num_mt = args.max_tiles;
+    const int NT = (args.N + kBN - 1) / kBN;
+    const int v = xcd_tile(num_mt * NT);
+    if (v < 0) return;
+    const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
+    const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
+    const int mt = mt0 + vin % gm, nt = vin / gm;
+    const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
+    const int row0 = dense ? mt * BM : __builtin_amdgcn_readfirstlane(args.tile_row0[mt]);
+    const int nks = args.K / kBK;
+    auto d_row = [&](int r) __attribute__((always_inline)) -> int {
+        if (dense) return row0 + r < args.dense_rows ? row0 + r : -1;
+        return args.perm[row0 + r];
+    };
+    auto a_row = [&](int r) __attribute__((always_inline)) -> uint32_t {
+        const int d = d_row(r);
+        return d < 0 ? 0u : (uint32_t)d;           // padding rows read row 0 and are never stored
+    };
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    uint32_t a_off[A_DMA], b_off[B_DMA], sa_off[FM];
+#pragma unroll
+    for (int j = 0; j < A_DMA; ++j) a_off[j] = a_row(8 * (wave * A_DMA + j) + (lane >> 3)) * (uint32_t)args.K + chunk * 16;
+    // B rows in fragment order, as in the tiled kernel: a lane ends up with 8 adjacent columns
+#pragma unroll
+    for (int j = 0; j < B_DMA; ++j) {
+        const int r = 8 * (wave * B_DMA + j) + (lane >> 3), f = r >> 4;
+        const int n = nt * kBN + (f / FN) * 128 + (r & 15) * FN + f % FN;
+        b_off[j] = (uint32_t)(min(n, args.N - 1) - nt * kBN) * (uint32_t)args.K + chunk * 16;
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa_off[f] = a_row(wm * 64 + f * 16 + l) * (uint32_t)args.sf_stride;
+    const int nblk = (args.N + 127) / 128, blk = min(nt * 2 + wn, nblk - 1);
+    const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)args.a, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)args.a_sf, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(args.b + ((size_t)group * args.N + (size_t)nt * kBN) * args.K), 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(args.b_sf + ((size_t)group * nblk + blk) * args.sf_stride), 0, kAllRecords, kRsrcWord3);
+    uint32_t sa[2][FM], sb[2];
+    // loads of step ks into ring slot ks % 3; the scale bytes into set S
+    auto issue = [&](int ks, auto set_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(set_c)::value;
+        const int kc = min(ks, nks - 1);           // steps past the last reload it into a free slot
+        uint8_t* dst = smem + (ks % SLOTS) * (A_BYTES + B_BYTES);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) sa[S][f] = __builtin_amdgcn_raw_buffer_load_b8(rs_asf, sa_off[f], kc, 0);
+        sb[S] = __builtin_amdgcn_raw_buffer_load_b8(rs_bsf, 0, kc, 0);
+#pragma unroll
+        for (int j = 0; j < B_DMA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(dst + A_BYTES + (wave * B_DMA + j) * 1024), 16, b_off[j],
+                                                     kc * kBK, 0, 0);
+#pragma unroll
+        for (int j = 0; j < A_DMA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, MOE_LPTR(dst + (wave * A_DMA + j) * 1024), 16, a_off[j], kc * kBK, 0,
+                                                     0);
+    };
+    const uint32_t rd_lo = (uint32_t)(l * kBK + ((g ^ (l & 7)) << 4));
+    const uint32_t rd_hi = (uint32_t)(l * kBK + (((g + 4) ^ (l & 7)) << 4));
+    auto read = [&](const uint8_t* p) __attribute__((always_inline)) -> v8i {
+        const v4i lo = *reinterpret_cast<const v4i*>(p + rd_lo);
+        const v4i hi = *reinterpret_cast<const v4i*>(p + rd_hi);
+        return (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    };
+    v4f acc[FM][FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+    // the scale bytes of a step are copied out of their set before the set is loaded again
+    auto step = [&](int ks, auto set_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(set_c)::value;
+        constexpr int W = FM + 1 + A_DMA + B_DMA;  // the loads of step ks+1
+        __builtin_amdgcn_s_waitcnt(0x0070 | (W & 15) | (((W >> 4) & 3) << 14));
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(W) : "memory");
+        float fa[FM];
+#pragma unroll
+        for (int f = 0; f < FM; ++f) fa[f] = scale_f32((int)sa[S][f]);
+        const float fb = scale_f32((int)sb[S]);
+        issue(ks + 2, set_c);
+        const uint8_t* src = smem + (ks % SLOTS) * (A_BYTES + B_BYTES);
+        v8bf av[FM][4];
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            const v8i w = read(src + (wm * FM + f) * 16 * kBK);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) av[f][q] = to_bf16(w[2 * q], w[2 * q + 1], fa[f]);
+        }
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+            const v8i w = read(src + A_BYTES + (wn * FN + n) * 16 * kBK);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v8bf bv = to_bf16(w[2 * q], w[2 * q + 1], fb);
+#pragma unroll
+                for (int f = 0; f < FM; ++f) acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[f][q], bv, acc[f][n], 0, 0, 0);
+            }
+        }
+    };
+    issue(0, IntC<0>{});
+    issue(1, IntC<1>{});
+    for (int ks = 0; ks < nks; ks += 2) {
+        step(ks, IntC<0>{});
+        if (ks + 1 < nks) step(ks + 1, IntC<1>{});
+    }
+    // the last steps' reloads must land before the workgroup's LDS is given back
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+
+    const int col0 = nt * kBN + wn * 128 + l * FN;
+    float* const d = static_cast<float*>(args.d);
+    const bool wide = args.N % 8 == 0;             // rows and chunks aligned, a chunk wholly in or out
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = d_row(wm * 64 + f * 16 + 4 * g + r);
+            if (row < 0) continue;
+            float* dst = d + (size_t)row * args.N + col0;
+            if (wide) {
+                if (col0 < args.N) {
+                    *reinterpret_cast<v4f*>(dst) = (v4f){acc[f][0][r], acc[f][1][r], acc[f][2][r], acc[f][3][r]};
+                    *reinterpret_cast<v4f*>(dst + 4) = (v4f){acc[f][4][r], acc[f][5][r], acc[f][6][r], acc[f][7][r]};
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < FN; ++n)
+                    if (col0 + n < args.N) dst[n] = acc[f][n][r];
+            }
+        }
+    }
+#endif
+}
+
 }  // namespace
 
 namespace {
@@ -564,7 +714,8 @@ hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream
     const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, block_m) : a.max_tiles;
     // one workgroup per possible tile; those past the tiles in use return at once
     const size_t grid = mt * (size_t)cdiv(a.N, kBN);
-    if (block_m == 256) gemm_fp8_tiled<256, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
+    if (a.out_f32 && block_m == kF32Rows) gemm_fp8_tiled_f32<<<(unsigned)grid, 256, 0, stream>>>(a);
+    else if (block_m == 256) gemm_fp8_tiled<256, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
     else if (block_m == 128) gemm_fp8_tiled<128, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
     else if (!a.out_f32 && grid >= 256) gemm_fp8_tiled<64, 1, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
     else if (mt * (size_t)cdiv(a.N, 64) >= 64) launch_skinny<64, 64, 4>(mt, a, stream);

@@ -111,7 +111,7 @@ class Problem:
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 128), (1, 16, 128), (2, 7, 256), (77, 273, 384), (64, 64, 512), (65, 129, 640), (33, 256, 2048),
     (128, 32, 7168), (130, 511, 1152), (200, 1040, 4096), (256, 256, 128), (257, 300, 256), (1000, 528, 1152),
-    (31, 2049, 1024), (16, 513, 5120), (600, 255, 896), (5, 100, 18432), (513, 777, 1664), (1024, 1280, 640),
+    (31, 2049, 1024), (16, 513, 5120), (600, 255, 896), (5, 100, 18432), (513, 777, 1664), (1024, 1280, 640), (2048, 2080, 384), (1900, 2561, 1280),
 ])
 def test_dense(M, N, K, d_type):
     print(f"[fp8] dense {M} {N} {K} {d_type}", flush=True)
