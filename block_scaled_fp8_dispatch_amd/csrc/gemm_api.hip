@@ -144,17 +144,15 @@ bool fp8_shape_ok(int G, int N, int K, int d_type) {
     return d_type == MOE_BF16 || d_type == MOE_F32;
 }
 
-// Row-tile size: bf16 outputs by the expected rows per group, as the FP8 x FP4 GEMMs. FP32
-// outputs have one tiled kernel (128 rows), taken where its tiles fill half the CUs; smaller
-// products go to the skinny kernel (64 rows).
-int fp8_block_m(long long rows_per_group, int groups, int N, int d_type) {
-    if (d_type != MOE_F32) return gemm_block_m(rows_per_group);
-    return rows_per_group >= 64 && (rows_per_group + 127) / 128 * groups * cdiv(N, 256) >= 128 ? 128 : 64;
+// Whether the smallest tiles (32 x 32) of the product can be numbered
+bool fp8_grid_ok(long long rows, int G, int N) {
+    return (rows / 32 + 2ll * G) * cdiv(N, 32) < (1ll << 31);
 }
 
 GemmFp8Args fp8_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int N, int K, const uint8_t* b,
-                     const uint8_t* b_sf, uint8_t* ws, const GemmWs& W, int tiles_bound) {
+                     const uint8_t* b_sf, uint8_t* ws, const GemmWs& W, int block_m, int tiles_bound) {
     GemmFp8Args g{};
+    g.block_m = block_m;
     g.a = a;
     g.a_sf = a_sf;
     g.b = b;
@@ -314,13 +312,15 @@ int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(b) || !aligned16(b_sf) || !aligned16(workspace))
         return MOE_ERR_ALIGN;
     if (!rows_ok(m, 1, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(m, 1, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws(m, 1);
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
-    const int BM = fp8_block_m(m, 1, n, d_type);
-    GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, static_cast<uint8_t*>(workspace), W, cdiv(m, BM));
+    const Fp8Plan plan = fp8_plan(1, m, false, n, k, d_type == MOE_F32);
+    const int BM = plan.block_m;
+    GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
     g.dense_rows = m;
-    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
@@ -333,17 +333,19 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
         !aligned16(b_sf) || !aligned16(workspace))
         return MOE_ERR_ALIGN;
     if (!rows_ok(m, groups, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(m, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws(m, groups);
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = fp8_block_m(m / groups, groups, n, d_type);
+    const Fp8Plan plan = fp8_plan(groups, (double)m / groups, true, n, k, d_type == MOE_F32);
+    const int BM = plan.block_m;
     auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
     if (launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets), i32(W.perm),
                      i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream) != hipSuccess)
         return MOE_ERR_HIP;
-    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, cdiv(m, BM) + groups);
-    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, cdiv(m, BM) + groups);
+    return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
@@ -358,17 +360,20 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (max_m < 0) return MOE_ERR_TOKENS;
     const long long rows = (long long)groups * max_m;
     if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(rows + 64ll * groups, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws((int)rows, groups);
     if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = fp8_block_m(expected_m, groups, n, d_type);
+    const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;
+    const Fp8Plan plan = fp8_plan(groups, rows_each, true, n, k, d_type == MOE_F32);
+    const int BM = plan.block_m;
     if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
                            reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
                            reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
         return MOE_ERR_HIP;
-    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, groups * cdiv(max_m, BM));
-    return launch_gemm_fp8(BM, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, groups * cdiv(max_m, BM));
+    return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

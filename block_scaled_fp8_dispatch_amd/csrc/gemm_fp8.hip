@@ -23,6 +23,8 @@
 // Workgroups go round-robin to the 8 XCDs; each XCD owns a contiguous range of tile ids, which
 // walk groups of 4 row tiles across all column tiles, so the tiles resident on one XCD share
 // rows of A and B in its L2.
+#include <cmath>
+
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -35,6 +37,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kGroupM = 4;
+constexpr int kCus = 256;                 // compute units of an MI355X
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -50,6 +53,27 @@ __device__ inline v8bf to_bf16(int w0, int w1, float scale) {
     const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
     const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
     return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Stores the first `left` of n adjacent columns of a row. A row may start at any element, so the
+// wide store's address is aligned to the element only, which the hardware takes (one store per
+// element instead: 8192 x 7001 x 2048 176 us against 142; aligned chunks taken apart: 142 against
+// 147).
+template <int n, class T>
+__device__ inline void store_columns(T* dst, const T (&x)[n], int left) {
+    if (left >= n) {
+        if constexpr (sizeof(x) == 16) {
+            if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+                __builtin_memcpy(__builtin_assume_aligned(dst, 16), x, sizeof(x));
+                return;
+            }
+        }
+        __builtin_memcpy(dst, x, sizeof(x));
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if (i < left) dst[i] = x[i];
+    }
 }
 
 // Workgroups go round-robin to the XCDs: tile id of this workgroup with each XCD (workgroup id
@@ -246,27 +270,22 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     }
     __syncthreads();
     // four adjacent columns per thread
-    const bool wide = p.N % 4 == 0;                // rows and chunks aligned, a chunk wholly in or out
     for (int i = tid; i < BM * BN / 4; i += WAVES * 64) {
         const int r = i / (BN / 4), c = i % (BN / 4) * 4, n = nt * BN + c;
         const int row = d_row(r);
-        if (row < 0 || n >= p.N) continue;
+        if (row < 0) continue;
         v4f x = *reinterpret_cast<const v4f*>(&at(0, r, c));
 #pragma unroll
         for (int w = 1; w < WAVES / 2; ++w) x += *reinterpret_cast<const v4f*>(&at(w, r, c));
         const size_t to = (size_t)row * p.N + n;
         if constexpr (F32) {
-            float* d = static_cast<float*>(p.d) + to;
-            if (wide) *reinterpret_cast<v4f*>(d) = x;
-            else
-                for (int q = 0; q < 4 && n + q < p.N; ++q) d[q] = x[q];
+            const float out[4] = {x.x, x.y, x.z, x.w};
+            store_columns<4>(static_cast<float*>(p.d) + to, out, p.N - n);
         } else {
-            uint16_t* d = static_cast<uint16_t*>(p.d) + to;
             const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x.x, x.y}), v2bf));
             const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x.z, x.w}), v2bf));
-            if (wide) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
-            else
-                for (int q = 0; q < 4 && n + q < p.N; ++q) d[q] = (uint16_t)((q < 2 ? lo : hi) >> (16 * (q & 1)));
+            const uint16_t out[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+            store_columns<4>(static_cast<uint16_t*>(p.d) + to, out, p.N - n);
         }
     }
 #endif
@@ -306,7 +325,8 @@ struct Fp8Cfg {
     static_assert(WN == 64 || WN == 128, "one scale block of B per wave");
 };
 
-template <int BM, int WAVES_M, int WAVES_N>
+// STREAM: B is read by one row tile only, through non-temporal loads
+template <int BM, int WAVES_M, int WAVES_N, bool STREAM>
 __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty kernel
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -321,17 +341,34 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     const int g = lane >> 4, l = lane & 15;
 
     // ---- tile ------------------------------------------------------------------------------
+    // Tile ids walk groups of 4 row tiles (of args.block_m rows) across all column tiles. The last
+    // round of 256 tiles, when it would be at most half full (256-row tiles only), is left to
+    // the second launch (tail), whose workgroups take parts of BM rows of those tiles: 64 rows
+    // where that still is one round, else 128.
     const bool dense = args.dense_rows > 0;
-    int num_mt = dense ? (args.dense_rows + BM - 1) / BM : __builtin_amdgcn_readfirstlane(args.meta[0]);
+    const int bm = args.block_m;
+    int num_mt = dense ? (args.dense_rows + bm - 1) / bm : __builtin_amdgcn_readfirstlane(args.meta[0]);
     if (num_mt > args.max_tiles) num_mt = args.max_tiles;
     const int NT = (args.N + kBN - 1) / kBN;
-    const int v = xcd_tile(num_mt * NT);
-    if (v < 0) return;
+    const int total = num_mt * NT;
+    const int rem = bm == 256 ? total % kCus : 0;
+    const int main_total = rem <= kCus / 2 ? total - rem : total;
+    int v, part = 0;
+    if (!args.tail) {
+        v = xcd_tile(main_total);
+        if (v < 0) return;
+    } else {
+        if (BM != (rem <= kCus / 4 ? 64 : 128)) return;
+        const int u = xcd_tile((total - main_total) * (256 / BM));
+        if (u < 0) return;
+        v = main_total + u / (256 / BM);
+        part = u % (256 / BM);
+    }
     const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
     const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
     const int mt = mt0 + vin % gm, nt = vin / gm;
     const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
-    const int row0 = dense ? mt * BM : __builtin_amdgcn_readfirstlane(args.tile_row0[mt]);
+    const int row0 = (dense ? mt * bm : __builtin_amdgcn_readfirstlane(args.tile_row0[mt])) + part * BM;
     const int nks = args.K / kBK;
     // A and D row of tile row r, -1 on padding
     auto d_row = [&](int r) __attribute__((always_inline)) -> int {
@@ -342,6 +379,9 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
         const int d = d_row(r);
         return d < 0 ? 0u : (uint32_t)d;      // padding rows read row 0 and are never stored
     };
+
+    // padding comes last in a row tile: nothing but padding here
+    if (args.tail && __builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
 
     // ---- per-lane offsets --------------------------------------------------------------------
     // Load j of wave w fills LDS rows 8*(w*DMA + j) .. +7 of a tile; lane l lands at row + l/8,
@@ -379,7 +419,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     auto load_b = [&](int ks, int j) __attribute__((always_inline)) {
         const int kc = min(ks, nks - 1);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(bring + (ks % DB) * C::B_BYTES + (wave * B_DMA + j) * 1024), 16,
-                                                 b_off[j], kc * kBK, 0, 0);
+                                                 b_off[j], kc * kBK, 0, STREAM ? 2 : 0);
     };
     uint32_t sa[2][FM], sb[2];
     auto load_scale = [&](int kb, int i, int set) __attribute__((always_inline)) {
@@ -520,32 +560,36 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     // ---- epilogue: rows 16*fm + 4g + r, columns col0 .. col0 + FN-1 ----------------------------
     const int col0 = nt * kBN + wn * WN + l * FN;
     uint16_t* const d = static_cast<uint16_t*>(args.d);
-    const bool wide = args.N % 8 == 0;          // rows and chunks aligned, a chunk wholly in or out
+    auto store = [&](auto aligned_c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
+        for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
-            if (row < 0) continue;
-            uint32_t pk[FN / 2];
+            for (int r = 0; r < 4; ++r) {
+                const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
+                if (row < 0) continue;
+                uint32_t pk[FN / 2];
 #pragma unroll
-            for (int q = 0; q < FN / 2; ++q) {
-                const v2f x = {acc[fm][2 * q][r], acc[fm][2 * q + 1][r]};
-                pk[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
-            }
-            uint16_t* dst = d + (size_t)row * args.N + col0;
-            if (wide) {
-                if (col0 < args.N) {
+                for (int q = 0; q < FN / 2; ++q) {
+                    const v2f x = {acc[fm][2 * q][r], acc[fm][2 * q + 1][r]};
+                    pk[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
+                }
+                uint16_t* dst = d + (size_t)row * args.N + col0;
+                if constexpr (decltype(aligned_c)::value) {
+                    if (col0 >= args.N) continue;
                     if constexpr (FN == 8) *reinterpret_cast<v4i*>(dst) = (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]};
                     else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-                }
-            } else {
+                } else {
+                    uint16_t out[FN];
 #pragma unroll
-                for (int q = 0; q < FN; ++q)
-                    if (col0 + q < args.N) dst[q] = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
+                    for (int q = 0; q < FN; ++q) out[q] = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
+                    store_columns<FN>(dst, out, args.N - col0);
+                }
             }
         }
-    }
+    };
+    // where every row and chunk is aligned and a chunk wholly in or out, plain wide stores
+    if (args.N % 8 == 0) store(IntC<1>{});
+    else store(IntC<0>{});
 #endif
 }
 
@@ -676,50 +720,107 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
 
     const int col0 = nt * kBN + wn * 128 + l * FN;
     float* const d = static_cast<float*>(args.d);
-    const bool wide = args.N % 8 == 0;             // rows and chunks aligned, a chunk wholly in or out
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = d_row(wm * 64 + f * 16 + 4 * g + r);
             if (row < 0) continue;
-            float* dst = d + (size_t)row * args.N + col0;
-            if (wide) {
-                if (col0 < args.N) {
-                    *reinterpret_cast<v4f*>(dst) = (v4f){acc[f][0][r], acc[f][1][r], acc[f][2][r], acc[f][3][r]};
-                    *reinterpret_cast<v4f*>(dst + 4) = (v4f){acc[f][4][r], acc[f][5][r], acc[f][6][r], acc[f][7][r]};
-                }
-            } else {
+            float out[FN];
 #pragma unroll
-                for (int n = 0; n < FN; ++n)
-                    if (col0 + n < args.N) dst[n] = acc[f][n][r];
-            }
+            for (int n = 0; n < FN; ++n) out[n] = acc[f][n][r];
+            store_columns<FN>(d + (size_t)row * args.N + col0, out, args.N - col0);
         }
     }
 #endif
 }
 
-}  // namespace
-
-namespace {
 template <int BM, int BN, int WAVES>
 void launch_skinny(size_t tiles64, const GemmFp8Args& a, hipStream_t stream) {
     const unsigned grid = (unsigned)(tiles64 * (64 / BM) * (size_t)cdiv(a.N, BN));
     if (a.out_f32) gemm_fp8_skinny<BM, BN, WAVES, true><<<grid, WAVES * 64, 0, stream>>>(a);
     else gemm_fp8_skinny<BM, BN, WAVES, false><<<grid, WAVES * 64, 0, stream>>>(a);
 }
+
+// Microseconds of a round of 256 workgroups of each kernel, as fixed + per-step (128 K) parts,
+// fitted to 16 products from 256 x 256 x 2048 to 4096 x 4096 x 7168 timed with every kernel (each
+// prediction within 15 % of its measurement; for instance 1000 x 1000 x 7168, bf16: 78, 43, 33, 22
+// and 33 us; 4096 x 4096 x 7168: 96, 107, 151, 272 and 467 us; 64 x 7168 x 7168: 71, 42, 33, 19 and
+// 18 us).
+struct Cost {
+    Fp8Kernel kernel;
+    int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
+    double fixed, step;
+};
+constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 6.0, 1.45},
+                          {Fp8Kernel::kTiled128, 128, 128, 256, 4.0, 0.83},
+                          {Fp8Kernel::kTiled64, 64, 64, 256, 4.9, 0.57},
+                          {Fp8Kernel::kSkinny64, 64, 64, 64, 4.0, 0.2275},
+                          {Fp8Kernel::kSkinny32, 64, 32, 32, 1.6, 0.10}};
+constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 8.0, 1.92},
+                         {Fp8Kernel::kSkinny64, 64, 64, 64, 4.2, 0.335},
+                         {Fp8Kernel::kSkinny32, 64, 32, 32, 2.0, 0.109}};
+
+template <size_t NK>
+Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, bool ragged, int N, int K) {
+    Fp8Plan best{};
+    double least = 0;
+    const int steps = K / 128;
+    for (const Cost& c : costs) {
+        // groups of unknown length end in a tile that is half full on average
+        const double mt = groups * (ragged ? rows / c.bm + 0.5 : std::ceil(rows / c.bm));
+        const double tiles = std::ceil(mt) * std::ceil((double)N / c.bn);
+        double rounds = std::floor(tiles / kCus), t = 0;
+        const double rem = tiles - rounds * kCus;
+        if (rem > 0) {
+            // the second launch of the 256-row tiles: kBf16[2] and kBf16[1]
+            if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 4) t = kBf16[2].fixed + kBf16[2].step * steps;
+            else if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 2) t = kBf16[1].fixed + kBf16[1].step * steps;
+            else rounds += 1;
+        }
+        t += rounds * (c.fixed + c.step * steps);
+        if (best.block_m == 0 || t < least) {
+            best = Fp8Plan{c.kernel, c.block_m, rows <= c.block_m};
+            least = t;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
-hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream) {
-    const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, block_m) : a.max_tiles;
+Fp8Plan fp8_plan(int groups, double rows_per_group, bool ragged, int N, int K, bool out_f32) {
+    return out_f32 ? cheapest(kF32, groups, rows_per_group, ragged, N, K)
+                   : cheapest(kBf16, groups, rows_per_group, ragged, N, K);
+}
+
+hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_t stream) {
+    const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, plan.block_m) : a.max_tiles;
     // one workgroup per possible tile; those past the tiles in use return at once
     const size_t grid = mt * (size_t)cdiv(a.N, kBN);
-    if (a.out_f32 && block_m == kF32Rows) gemm_fp8_tiled_f32<<<(unsigned)grid, 256, 0, stream>>>(a);
-    else if (block_m == 256) gemm_fp8_tiled<256, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
-    else if (block_m == 128) gemm_fp8_tiled<128, 2, 2><<<(unsigned)grid, 256, 0, stream>>>(a);
-    else if (!a.out_f32 && grid >= 256) gemm_fp8_tiled<64, 1, 4><<<(unsigned)grid, 256, 0, stream>>>(a);
-    else if (mt * (size_t)cdiv(a.N, 64) >= 64) launch_skinny<64, 64, 4>(mt, a, stream);
-    else launch_skinny<32, 32, 8>(mt, a, stream);
+    switch (plan.kernel) {
+        case Fp8Kernel::kTiled256: {
+            gemm_fp8_tiled<256, 2, 2, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            GemmFp8Args t = a;
+            t.tail = 1;
+            // the leftover tiles' number is known on the host for a dense product only
+            const size_t rem = grid % kCus;
+            const bool dense = a.dense_rows > 0;
+            if (!dense || (rem > 0 && rem <= kCus / 4)) gemm_fp8_tiled<64, 1, 4, false><<<kCus, 256, 0, stream>>>(t);
+            if (!dense || (rem > kCus / 4 && rem <= kCus / 2)) gemm_fp8_tiled<128, 2, 2, false><<<kCus, 256, 0, stream>>>(t);
+            break;
+        }
+        case Fp8Kernel::kTiled128:
+            if (a.out_f32) gemm_fp8_tiled_f32<<<(unsigned)grid, 256, 0, stream>>>(a);
+            else gemm_fp8_tiled<128, 2, 2, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            break;
+        case Fp8Kernel::kTiled64:
+            if (plan.stream) gemm_fp8_tiled<64, 1, 4, true><<<(unsigned)grid, 256, 0, stream>>>(a);
+            else gemm_fp8_tiled<64, 1, 4, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            break;
+        case Fp8Kernel::kSkinny64: launch_skinny<64, 64, 4>(mt, a, stream); break;
+        case Fp8Kernel::kSkinny32: launch_skinny<32, 32, 8>(mt, a, stream); break;
+    }
     return hipGetLastError();
 }
 

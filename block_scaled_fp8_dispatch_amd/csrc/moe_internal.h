@@ -175,6 +175,7 @@ hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t
                       hipStream_t stream);
 
 // FP8 x FP8 GEMM with 128-block scales (gemm_fp8.hip)
+enum class Fp8Kernel { kTiled256, kTiled128, kTiled64, kSkinny64, kSkinny32 };
 struct GemmFp8Args {
     const uint8_t* a;          // e4m3 rows of K bytes
     const uint8_t* a_sf;       // rows of sf_stride UE8M0 bytes
@@ -182,18 +183,28 @@ struct GemmFp8Args {
     const uint8_t* b_sf;       // [G][ceil(N/128)][sf_stride]
     int K, N;
     int sf_stride;             // 4*ceil(K/512)
-    // Row tiles: dense_rows > 0: rows 0 .. dense_rows-1 in tiles of block_m; otherwise the
-    // lists of the routing (perm: A and D row of each padded row, -1 padding)
+    // Row tiles of block_m rows: dense_rows > 0: rows 0 .. dense_rows-1; otherwise the lists of
+    // the routing (perm: A and D row of each padded row, -1 padding)
+    int block_m;
     int dense_rows;
     const int32_t* perm;
     const int32_t* meta;
     const int32_t* tile_expert;
     const int32_t* tile_row0;
     int max_tiles;
+    int tail;                  // the tiled kernels' second launch: the last tiles, in parts
     void* d;
     int out_f32;
 };
-hipError_t launch_gemm_fp8(int block_m, const GemmFp8Args& a, hipStream_t stream);
+// The kernel for groups of about rows_per_group rows (ragged: known on the device only), the
+// height of its row tiles, and whether one row tile per group reads B
+struct Fp8Plan {
+    Fp8Kernel kernel;
+    int block_m;
+    bool stream;
+};
+Fp8Plan fp8_plan(int groups, double rows_per_group, bool ragged, int N, int K, bool out_f32);
+hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_t stream);
 
 // Combine (combine.hip)
 hipError_t launch_combine(const uint16_t* stage, const int32_t* topk_idx, const float* topk_weights,

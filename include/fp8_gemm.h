@@ -15,7 +15,8 @@
  * rounded once to nearest even) or FP32, as d_type (MOE_BF16, MOE_F32 of moe_serving.h) says.
  *
  * Shapes: K a positive multiple of 128, at most 2^22; N any positive number; G (groups) in
- * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); B of any size.
+ * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); fewer than 2^31 tiles
+ * of 32 x 32 in D (MOE_ERR_SHAPE); B of any size.
  *
  * Memory, errors and streams as in moe.h: device pointers, 16-byte aligned, owned by the
  * caller; host-detectable problems return a negative MOE_ERR_* status before any launch;

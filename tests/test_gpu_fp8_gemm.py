@@ -121,9 +121,30 @@ def test_dense(M, N, K, d_type):
     assert np.array_equal(p.dense(), d), "two calls gave different bytes"
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (4096, 4112, 256),     # 256-row tiles: 272, a last round of 16 in parts of 64 rows
+    (4100, 5636, 128),     # the same, ragged both ways, rows at every alignment
+    (5000, 4871, 256),     # a last round of 144 stays whole
+    (4600, 4867, 128),     # a last round of 106 in parts of 128 rows
+])
+def test_dense_many_tiles(M, N, K):
+    """Outputs of more than one round of 256-row tiles, against torch's float64 product on the GPU
+    (same bound, on every element)."""
+    print(f"[fp8] dense {M} {N} {K}", flush=True)
+    p = Problem(M, N, K, 1, moe.MOE_BF16, seed=M)
+    d = torch.from_numpy(p.dense().view(np.int16).copy()).cuda().view(torch.bfloat16).double()
+    A = torch.from_numpy(oracle.dequant_fp8_rows(p.a, p.a_sf, K)).cuda()
+    B = torch.from_numpy(oracle.dequant_fp8_blocks(p.b[0], p.b_sf[0], K)).cuda()
+    exact = A @ B.t()
+    gamma = (K - 1) * 2.0 ** -24 / (1 - (K - 1) * 2.0 ** -24)
+    bound = gamma * (A.abs() @ B.abs().t())
+    bound += 2.0 ** -10 * (A.abs().view(M, K // 8, 8).amax(2) @ B.abs().view(N, K // 8, 8).amax(2).t())
+    assert ((d - exact).abs() <= bound + 2.0 ** -8 * (exact.abs() + bound) + 2.0 ** -134).all()
+
+
 @pytest.mark.parametrize("d_type", [moe.MOE_BF16, moe.MOE_F32])
 @pytest.mark.parametrize("M,N,K,G", [(700, 512, 512, 3), (90, 129, 256, 5), (5000, 264, 384, 7), (1, 40, 128, 2),
-                                     (2600, 520, 640, 2)])
+                                     (2600, 520, 640, 2), (9000, 2055, 256, 5)])
 def test_contiguous(M, N, K, G, d_type):
     print(f"[fp8] contiguous {M} {N} {K} {G} {d_type}", flush=True)
     p = Problem(M, N, K, G, d_type, seed=M)
