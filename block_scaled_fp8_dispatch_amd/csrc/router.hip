@@ -2,12 +2,22 @@
 // over the chosen ones): per token the k largest of E logits in descending order, ties to the
 // lowest expert, and their softmax weights.
 //
-// One wave per token; lane l holds the logits of experts l, 64 + l, .... Each logit becomes an
-// unsigned key that orders like the value (0 for -inf and NaN, which are never chosen; -0 and
-// +0 share a key, as they compare equal). k rounds: the wave's largest key (DPP maximum), the
-// lowest expert that holds it (ballots in ascending expert order), which then drops out. Lane
-// j keeps round j's choice, so the softmax over the chosen and the stores are one pass over
-// the lanes (k <= 64).
+// Each logit becomes an unsigned key that orders like the value (0 for -inf and NaN, which are
+// never chosen; -0 and +0 share a key, as they compare equal).
+//
+// router_kernel (k <= 16): 16 lanes per token up to E = 256 (32 or 64 beyond), at most 16 experts
+// per lane, as up to four lists in descending order. A key keeps its upper bits and carries its
+// expert in the lower ones (16 bits for bf16 logits, which lose nothing; log2 of the experts held
+// for FP32), so a round is one maximum over the heads and the token's lanes (DPP), and the list
+// whose head it was moves up; the expert comes out of the key. For FP32 logits with bits below the
+// kept ones, neighbours in the resulting order that agree in the kept bits, the best one left over
+// included, send the wave to the exact path; elsewhere the order is that of the whole keys.
+//
+// router_wave_kernel (and that exact path): one wave per token, lane l holding experts l, 64 + l,
+// ...: k rounds of the wave's largest key and the lowest expert that holds it.
+//
+// Bound by vector instructions rather than by memory: about 7 per token and round against 21
+// with a wave per token.
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -26,45 +36,55 @@ __device__ inline float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ inline uint32_t wave_max(uint32_t m) {
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)m);
+// One DPP step: v, combined by the caller, of the lane that CTRL names; lanes without one (or
+// in rows outside ROWS) get `old`
+template <int CTRL, int ROWS = 0xF>
+__device__ inline uint32_t dpp(uint32_t old, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
 }
 
+// Largest of the 64 lanes' values, uniform: neighbours, pairs, half rows and rows mirrored, then
+// lane 15 of each row into the next and lane 31 into the upper half
+__device__ inline uint32_t wave_max(uint32_t m) {
+    m = max(m, dpp<0xB1>(0, m));
+    m = max(m, dpp<0x4E>(0, m));
+    m = max(m, dpp<0x141>(0, m));
+    m = max(m, dpp<0x140>(0, m));
+    m = max(m, dpp<0x142, 0xA>(0, m));
+    m = max(m, dpp<0x143, 0xC>(0, m));
+    return (uint32_t)__builtin_amdgcn_readlane((int)m, 63);
+}
+
+// Sum of the 64 lanes' values, uniform, by the same steps
 __device__ inline float wave_sum(float v) {
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    const auto add = [](float x, uint32_t y) __attribute__((always_inline)) { return x + __uint_as_float(y); };
+    v = add(v, dpp<0xB1>(0, __float_as_uint(v)));
+    v = add(v, dpp<0x4E>(0, __float_as_uint(v)));
+    v = add(v, dpp<0x141>(0, __float_as_uint(v)));
+    v = add(v, dpp<0x140>(0, __float_as_uint(v)));
+    v = add(v, dpp<0x142, 0xA>(0, __float_as_uint(v)));
+    v = add(v, dpp<0x143, 0xC>(0, __float_as_uint(v)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // exp(x - m) for x <= m, 1 at x == m (also where both are +inf)
 __device__ inline float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
-// V: experts per lane (E <= 64 * V)
+template <bool BF16>
+__device__ inline float load_logit(const void* logits, size_t i) {
+    if constexpr (BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[i] << 16);
+    else return static_cast<const float*>(logits)[i];
+}
+
+// One token by the whole wave. V: experts per lane (E <= 64 * V)
 template <int V, bool BF16>
-__global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __restrict__ logits, int T, int E, int k,
-                                                                int over_all, float scale,
-                                                                int32_t* __restrict__ topk_idx,
-                                                                float* __restrict__ topk_weights) {
-    const int t = (int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6));
-    if (t >= T) return;
-    const int lane = threadIdx.x & 63;
+__device__ inline void route_token(const void* __restrict__ logits, int t, int E, int k, int over_all, float scale, int lane,
+                                   int32_t* __restrict__ topk_idx, float* __restrict__ topk_weights) {
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 64 + lane;
-        float x = -INFINITY;
-        if (e < E) {
-            if constexpr (BF16)
-                x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[(size_t)t * E + e] << 16);
-            else
-                x = static_cast<const float*>(logits)[(size_t)t * E + e];
-        }
-        key[i] = order_key(x);
+        key[i] = order_key(e < E ? load_logit<BF16>(logits, (size_t)t * E + e) : -INFINITY);
     }
     uint32_t first = 0;
     float denom = 0.f;
@@ -86,20 +106,23 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
                 denom = wave_sum(s);
             }
         }
-        bool found = false;
+        // the first i, then the lowest lane, that holds m
+        uint64_t hit = __ballot(key[0] == m);
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint64_t b = found ? 0ull : __ballot(key[i] == m);
-            if (b) {
-                found = true;
-                const int l = __ffsll((unsigned long long)b) - 1;
-                if (lane == l) key[i] = 0;
-                if (lane == j) {
-                    my_idx = i * 64 + l;
-                    my_key = m;
-                }
+        for (int i = 1; i < V; ++i) {
+            const uint64_t h = __ballot(key[i] == m);
+            if (!hit) {
+                hit = h;
+                at = i;
             }
         }
+        const int l = __ffsll((unsigned long long)hit) - 1;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (at == i) key[i] = lane == l ? 0 : key[i];         // uniform branch
+        my_idx = lane == j ? at * 64 + l : my_idx;
+        my_key = lane == j ? m : my_key;
     }
     const float e = my_idx >= 0 ? exp_below(key_value(my_key), key_value(first)) : 0.f;
     if (!over_all) denom = wave_sum(e);
@@ -109,20 +132,163 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     }
 }
 
+template <int V, bool BF16>
+__global__ __launch_bounds__(kRouterThreads) void router_wave_kernel(const void* __restrict__ logits, int T, int E, int k,
+                                                                     int over_all, float scale,
+                                                                     int32_t* __restrict__ topk_idx,
+                                                                     float* __restrict__ topk_weights) {
+    const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6)));
+    if (t < T) route_token<V, BF16>(logits, t, E, k, over_all, scale, threadIdx.x & 63, topk_idx, topk_weights);
+}
+
+// The largest (sum) of a token's L lanes, in each of them: within rows of 16 by DPP, across rows
+// by swapping the odd rows, then the halves
+template <int L>
+__device__ inline uint32_t lanes_max(uint32_t m) {
+    m = max(m, dpp<0xB1>(0, m));
+    m = max(m, dpp<0x4E>(0, m));
+    m = max(m, dpp<0x141>(0, m));
+    m = max(m, dpp<0x140>(0, m));
+    if constexpr (L >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+        m = max(p[0], p[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        m = max(p[0], p[1]);
+    }
+    return m;
+}
+
+template <int L>
+__device__ inline float lanes_sum(float v) {
+    v += __uint_as_float(dpp<0xB1>(0, __float_as_uint(v)));
+    v += __uint_as_float(dpp<0x4E>(0, __float_as_uint(v)));
+    v += __uint_as_float(dpp<0x141>(0, __float_as_uint(v)));
+    v += __uint_as_float(dpp<0x140>(0, __float_as_uint(v)));
+    if constexpr (L >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    return v;
+}
+
+// 64/L tokens per wave, V experts per lane (E <= L * V), k <= 16.
+template <int L, int V, bool BF16>
+__global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __restrict__ logits, int T, int E, int k,
+                                                                int over_all, float scale,
+                                                                int32_t* __restrict__ topk_idx,
+                                                                float* __restrict__ topk_weights) {
+    constexpr int kTokens = 64 / L;                        // per wave
+    constexpr int LISTS = V < 4 ? V : 4, D = V / LISTS;
+    constexpr uint32_t IDX = BF16 ? 0xffffu : L * V - 1;   // bits of the packed key that hold the expert
+    static_assert((IDX & (IDX + 1)) == 0 && (int)IDX + 1 >= L * V, "");
+    const int lane = threadIdx.x & 63, l = lane & (L - 1);
+    const int t0 = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6))) * kTokens;
+    if (t0 >= T) return;
+    const int t = t0 + lane / L;
+    float x[V];
+    uint32_t h[LISTS][D], low = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + l;
+        x[i] = t < T && e < E ? load_logit<BF16>(logits, (size_t)t * E + e) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t key = order_key(x[i]);
+        low |= key ? __float_as_uint(x[i]) & IDX : 0u;
+        h[i / D][i % D] = key ? (key & ~IDX) | (IDX - (uint32_t)(i * L + l)) : 0u;
+    }
+    // every list in descending order
+    auto order = [&](uint32_t& a, uint32_t& b) __attribute__((always_inline)) {
+        const uint32_t hi = max(a, b);
+        b = min(a, b);
+        a = hi;
+    };
+#pragma unroll
+    for (int s = 0; s < LISTS; ++s) {
+        if constexpr (D == 2) order(h[s][0], h[s][1]);
+        if constexpr (D == 4) {
+            order(h[s][0], h[s][1]);
+            order(h[s][2], h[s][3]);
+            order(h[s][0], h[s][2]);
+            order(h[s][1], h[s][3]);
+            order(h[s][1], h[s][2]);
+        }
+    }
+    auto head = [&]() __attribute__((always_inline)) -> uint32_t {
+        uint32_t m = h[0][0];
+#pragma unroll
+        for (int s = 1; s < LISTS; ++s) m = max(m, h[s][0]);
+        return lanes_max<L>(m);
+    };
+    uint32_t mine = 0;
+    for (int j = 0; j < k; ++j) {
+        const uint32_t m = head();
+#pragma unroll
+        for (int s = 0; s < LISTS; ++s) {
+            const bool hit = h[s][0] == m;
+#pragma unroll
+            for (int d = 0; d < D; ++d) h[s][d] = hit ? (d + 1 < D ? h[s][d + 1] : 0u) : h[s][d];
+        }
+        mine = l == j ? m : mine;
+    }
+    // Where a logit has bits below the packed ones, two neighbours in the order that agree in the
+    // bits kept may be in the wrong order: those tokens' wave starts over with whole keys.
+    if (!BF16 && __ballot(low != 0)) {
+        const uint32_t left = head(), right = dpp<0x101>(0, mine);    // the best left over, the next lane's
+        const uint32_t next = l == k - 1 ? left : right;
+        if (__ballot(l < k && mine != 0 && next != 0 && ((mine ^ next) & ~IDX) == 0)) {
+            for (int i = 0; i < kTokens && t0 + i < T; ++i)
+                route_token<(L * V + 63) / 64, BF16>(logits, t0 + i, E, k, over_all, scale, lane, topk_idx, topk_weights);
+            return;
+        }
+    }
+    const int idx = mine ? (int)(IDX - (mine & IDX)) : -1;
+    const float v = idx >= 0 && t < T ? load_logit<BF16>(logits, (size_t)t * E + idx) : -INFINITY;
+    const float top = __shfl(v, lane & ~(L - 1), 64);
+    const float e = idx >= 0 ? exp_below(v, top) : 0.f;
+    float denom;
+    if (over_all) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += x[i] > -INFINITY ? exp_below(x[i], top) : 0.f;      // false for a NaN
+        denom = lanes_sum<L>(s);
+    } else {
+        denom = lanes_sum<16>(e);                  // the chosen sit in the token's first 16 lanes
+    }
+    if (l < k && t < T) {
+        topk_idx[(size_t)t * k + l] = idx;
+        topk_weights[(size_t)t * k + l] = idx >= 0 ? e / denom * scale : 0.f;
+    }
+}
+
 template <bool BF16>
 void launch(const void* logits, int T, int E, int k, int over_all, float scale, int32_t* idx, float* w,
             hipStream_t stream) {
-    const unsigned grid = (unsigned)((T + kRouterThreads / 64 - 1) / (kRouterThreads / 64));
-    if (E <= 64)
-        router_kernel<1, BF16><<<grid, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
-    else if (E <= 128)
-        router_kernel<2, BF16><<<grid, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
-    else if (E <= 256)
-        router_kernel<4, BF16><<<grid, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
-    else if (E <= 512)
-        router_kernel<8, BF16><<<grid, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
-    else
-        router_kernel<16, BF16><<<grid, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
+    auto grid = [&](int tokens) { return (unsigned)(((long long)T + 4 * tokens - 1) / (4 * tokens)); };
+    auto run = [&](auto kernel, int tokens) {
+        kernel<<<grid(tokens), kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
+    };
+    if (k <= 16) {
+        if (E <= 32) run(router_kernel<16, 2, BF16>, 4);
+        else if (E <= 64) run(router_kernel<16, 4, BF16>, 4);
+        else if (E <= 128) run(router_kernel<16, 8, BF16>, 4);
+        else if (E <= 256) run(router_kernel<16, 16, BF16>, 4);
+        else if (E <= 512) run(router_kernel<32, 16, BF16>, 2);
+        else run(router_kernel<64, 16, BF16>, 1);
+    } else {
+        if (E <= 64) run(router_wave_kernel<1, BF16>, 1);
+        else if (E <= 128) run(router_wave_kernel<2, BF16>, 1);
+        else if (E <= 256) run(router_wave_kernel<4, BF16>, 1);
+        else if (E <= 512) run(router_wave_kernel<8, BF16>, 1);
+        else run(router_wave_kernel<16, BF16>, 1);
+    }
 }
 
 }  // namespace

@@ -83,6 +83,27 @@ def test_ties_masks_and_extremes(E, over_all):
     check(x.to(torch.bfloat16).cuda(), 5, over_all, -1.0)
 
 
+@pytest.mark.parametrize("E", [8, 24, 60, 100, 256, 300, 1000])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_neighbours_in_the_last_bits(E, sign):
+    """Logits that differ only in their last bits, among the chosen and at the border, next to tokens
+    whose logits end in zero bits, in every order."""
+    g = torch.Generator().manual_seed(E)
+    rows = []
+    for spread in (1, 2, 7, 300):                       # steps of 2^-23 between neighbours
+        v = 1.0 + torch.randperm(E, generator=g).float() * spread * 2.0 ** -23
+        rows += [v, torch.where(torch.rand(E, generator=g) < 0.3, v, torch.ones(E)), v.round()]
+    v = torch.randn(E, generator=g)
+    v[torch.randperm(E, generator=g)[: min(5, E - 2)]] = 3.0 + torch.arange(min(5, E - 2)).float() * 2.0 ** -22
+    rows += [v, torch.randn(E, generator=g).to(torch.bfloat16).float(), torch.zeros(E)]
+    x = (torch.stack(rows) * sign).cuda()
+    for k in (1, 4, 8):
+        check(x, k, False)
+    if E >= 24:
+        check(x, 16, True)
+        check(x, 17, True)
+
+
 def test_many_tokens_and_graph():
     g = torch.Generator(device="cuda").manual_seed(5)
     xs = [torch.randn(4097, 32, generator=g, device="cuda") for _ in range(3)]
