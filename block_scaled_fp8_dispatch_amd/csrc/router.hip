@@ -2,22 +2,20 @@
 // over the chosen ones): per token the k largest of E logits in descending order, ties to the
 // lowest expert, and their softmax weights.
 //
-// Each logit becomes an unsigned key that orders like the value (0 for -inf and NaN, which are
-// never chosen; -0 and +0 share a key, as they compare equal).
+// Each logit becomes an integer key that orders like the value (-inf and NaN below all, never
+// chosen; -0 and +0 share a key, as they compare equal).
 //
 // router_kernel (k <= 16): 16 lanes per token up to E = 256 (32 or 64 beyond), at most 16 experts
 // per lane, as up to four lists in descending order. A key keeps its upper bits and carries its
 // expert in the lower ones (16 bits for bf16 logits, which lose nothing; log2 of the experts held
 // for FP32), so a round is one maximum over the heads and the token's lanes (DPP), and the list
 // whose head it was moves up; the expert comes out of the key. For FP32 logits with bits below the
-// kept ones, neighbours in the resulting order that agree in the kept bits, the best one left over
-// included, send the wave to the exact path; elsewhere the order is that of the whole keys.
+// kept ones, where neighbours in the resulting order (the best one left over included) agree in
+// the kept bits, the wave chooses again by whole keys; elsewhere the order is that of the whole
+// keys. A wave takes several passes, the next one's logits loading while it chooses.
 //
-// router_wave_kernel (and that exact path): one wave per token, lane l holding experts l, 64 + l,
-// ...: k rounds of the wave's largest key and the lowest expert that holds it.
-//
-// Bound by vector instructions rather than by memory: about 7 per token and round against 21
-// with a wave per token.
+// router_wave_kernel (k > 16): one wave per token, lane l holding experts l, 64 + l, ...: k rounds
+// of the wave's largest key and the lowest expert that holds it.
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -25,6 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int kRouterThreads = 256;
+constexpr unsigned kRouterGroups = 2048;
 
 __device__ inline uint32_t order_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);                  // -0 -> +0
@@ -65,6 +64,12 @@ __device__ inline float wave_sum(float v) {
     v = add(v, dpp<0x142, 0xA>(0, __float_as_uint(v)));
     v = add(v, dpp<0x143, 0xC>(0, __float_as_uint(v)));
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// A signed key that orders like the value: negative values' magnitude bits inverted, -0 as +0
+__device__ inline int signed_key(float x) {
+    const int bits = __float_as_int(x + 0.0f);
+    return bits ^ (int)((uint32_t)(bits >> 31) >> 1);
 }
 
 // exp(x - m) for x <= m, 1 at x == m (also where both are +inf)
@@ -144,18 +149,18 @@ __global__ __launch_bounds__(kRouterThreads) void router_wave_kernel(const void*
 // The largest (sum) of a token's L lanes, in each of them: within rows of 16 by DPP, across rows
 // by swapping the odd rows, then the halves
 template <int L>
-__device__ inline uint32_t lanes_max(uint32_t m) {
-    m = max(m, dpp<0xB1>(0, m));
-    m = max(m, dpp<0x4E>(0, m));
-    m = max(m, dpp<0x141>(0, m));
-    m = max(m, dpp<0x140>(0, m));
+__device__ inline int lanes_max(int m) {
+    m = max(m, (int)dpp<0xB1>(0, (uint32_t)m));
+    m = max(m, (int)dpp<0x4E>(0, (uint32_t)m));
+    m = max(m, (int)dpp<0x141>(0, (uint32_t)m));
+    m = max(m, (int)dpp<0x140>(0, (uint32_t)m));
     if constexpr (L >= 32) {
-        const auto p = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-        m = max(p[0], p[1]);
+        const auto p = __builtin_amdgcn_permlane16_swap((uint32_t)m, (uint32_t)m, false, false);
+        m = max((int)p[0], (int)p[1]);
     }
     if constexpr (L >= 64) {
-        const auto p = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-        m = max(p[0], p[1]);
+        const auto p = __builtin_amdgcn_permlane32_swap((uint32_t)m, (uint32_t)m, false, false);
+        m = max((int)p[0], (int)p[1]);
     }
     return m;
 }
@@ -183,30 +188,56 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
                                                                 int over_all, float scale,
                                                                 int32_t* __restrict__ topk_idx,
                                                                 float* __restrict__ topk_weights) {
+    // gfx950 buffer descriptors are a device-only type: the host pass sees an empty kernel
+#if defined(__HIP_DEVICE_COMPILE__)
     constexpr int kTokens = 64 / L;                        // per wave
     constexpr int LISTS = V < 4 ? V : 4, D = V / LISTS;
+    constexpr int kNone = -0x7fffffff - 1;                 // below every key: nothing (left)
     constexpr uint32_t IDX = BF16 ? 0xffffu : L * V - 1;   // bits of the packed key that hold the expert
     static_assert((IDX & (IDX + 1)) == 0 && (int)IDX + 1 >= L * V, "");
     const int lane = threadIdx.x & 63, l = lane & (L - 1);
-    const int t0 = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6))) * kTokens;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6)));
+    const int stride = (int)(gridDim.x * (kRouterThreads / 64)) * kTokens;
+    // The logits of a pass, one pass ahead: buffer loads from the pass's first row on, so that one
+    // offset register serves them all. What lies past a row's end is never looked at; past the
+    // last row the loads return 0.
+    constexpr int kBytes = BF16 ? 2 : 4;
+    const uint32_t offset = (uint32_t)(lane / L * E + l) * kBytes;
+    float ahead[V];
+    auto load = [&](int t0) __attribute__((always_inline)) {
+        const size_t rest = (size_t)(T - t0) * E * kBytes;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(static_cast<const uint8_t*>(logits) + (size_t)t0 * E * kBytes), 0,
+            (int)(uint32_t)(rest < 0xffffffffu ? rest : 0xffffffffu), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (BF16)
+                ahead[i] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, offset + i * L * kBytes, 0, 0) << 16);
+            else
+                ahead[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, offset + i * L * kBytes, 0, 0));
+        }
+    };
+    int t0 = wave * kTokens;
     if (t0 >= T) return;
+    load(t0);
+    for (; t0 < T; t0 += stride) {
     const int t = t0 + lane / L;
     float x[V];
-    uint32_t h[LISTS][D], low = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = ahead[i];
+    if (t0 + stride < T) load(t0 + stride);
+    // whether x[i] may be chosen (false for a NaN)
+    auto valid = [&](int i) __attribute__((always_inline)) -> bool { return x[i] > -INFINITY && l < E - i * L; };
+    int h[LISTS][D];
+    uint32_t low = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = i * L + l;
-        x[i] = t < T && e < E ? load_logit<BF16>(logits, (size_t)t * E + e) : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t key = order_key(x[i]);
-        low |= key ? __float_as_uint(x[i]) & IDX : 0u;
-        h[i / D][i % D] = key ? (key & ~IDX) | (IDX - (uint32_t)(i * L + l)) : 0u;
+        low |= __float_as_uint(x[i]);
+        h[i / D][i % D] = valid(i) ? (int)(((uint32_t)signed_key(x[i]) & ~IDX) | (IDX - (uint32_t)(i * L + l))) : kNone;
     }
     // every list in descending order
-    auto order = [&](uint32_t& a, uint32_t& b) __attribute__((always_inline)) {
-        const uint32_t hi = max(a, b);
+    auto order = [&](int& a, int& b) __attribute__((always_inline)) {
+        const int hi = max(a, b);
         b = min(a, b);
         a = hi;
     };
@@ -221,35 +252,49 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
             order(h[s][1], h[s][2]);
         }
     }
-    auto head = [&]() __attribute__((always_inline)) -> uint32_t {
-        uint32_t m = h[0][0];
+    auto head = [&]() __attribute__((always_inline)) -> int {
+        int m = h[0][0];
 #pragma unroll
         for (int s = 1; s < LISTS; ++s) m = max(m, h[s][0]);
         return lanes_max<L>(m);
     };
-    uint32_t mine = 0;
+    int mine = kNone;
     for (int j = 0; j < k; ++j) {
-        const uint32_t m = head();
+        const int m = head();
 #pragma unroll
         for (int s = 0; s < LISTS; ++s) {
             const bool hit = h[s][0] == m;
 #pragma unroll
-            for (int d = 0; d < D; ++d) h[s][d] = hit ? (d + 1 < D ? h[s][d + 1] : 0u) : h[s][d];
+            for (int d = 0; d < D; ++d) h[s][d] = hit ? (d + 1 < D ? h[s][d + 1] : kNone) : h[s][d];
         }
         mine = l == j ? m : mine;
     }
+    int idx = mine != kNone ? (int)(IDX - ((uint32_t)mine & IDX)) : -1;
     // Where a logit has bits below the packed ones, two neighbours in the order that agree in the
-    // bits kept may be in the wrong order: those tokens' wave starts over with whole keys.
-    if (!BF16 && __ballot(low != 0)) {
-        const uint32_t left = head(), right = dpp<0x101>(0, mine);    // the best left over, the next lane's
-        const uint32_t next = l == k - 1 ? left : right;
-        if (__ballot(l < k && mine != 0 && next != 0 && ((mine ^ next) & ~IDX) == 0)) {
-            for (int i = 0; i < kTokens && t0 + i < T; ++i)
-                route_token<(L * V + 63) / 64, BF16>(logits, t0 + i, E, k, over_all, scale, lane, topk_idx, topk_weights);
-            return;
+    // bits kept may be in the wrong order: the wave then chooses again by whole keys.
+    if (!BF16 && __ballot((low & IDX) != 0)) {
+        const int left = head(), right = (int)dpp<0x101>((uint32_t)kNone, (uint32_t)mine);   // best left over, next lane's
+        const int next = l == k - 1 ? left : right;
+        if (__ballot(l < k && mine != kNone && next != kNone && ((uint32_t)(mine ^ next) & ~IDX) == 0)) {
+            int key[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = valid(i) ? signed_key(x[i]) : kNone;
+            idx = -1;
+            for (int j = 0; j < k; ++j) {
+                int m = key[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) m = max(m, key[i]);
+                m = lanes_max<L>(m);
+                int lowest = 0x7fffffff;           // expert among those that hold m
+#pragma unroll
+                for (int i = 0; i < V; ++i) lowest = min(lowest, key[i] == m ? i * L + l : 0x7fffffff);
+                lowest = -lanes_max<L>(-lowest);
+#pragma unroll
+                for (int i = 0; i < V; ++i) key[i] = i * L + l == lowest ? kNone : key[i];
+                if (l == j && m != kNone) idx = lowest;
+            }
         }
     }
-    const int idx = mine ? (int)(IDX - (mine & IDX)) : -1;
     const float v = idx >= 0 && t < T ? load_logit<BF16>(logits, (size_t)t * E + idx) : -INFINITY;
     const float top = __shfl(v, lane & ~(L - 1), 64);
     const float e = idx >= 0 ? exp_below(v, top) : 0.f;
@@ -257,7 +302,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     if (over_all) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += x[i] > -INFINITY ? exp_below(x[i], top) : 0.f;      // false for a NaN
+        for (int i = 0; i < V; ++i) s += valid(i) ? exp_below(x[i], top) : 0.f;
         denom = lanes_sum<L>(s);
     } else {
         denom = lanes_sum<16>(e);                  // the chosen sit in the token's first 16 lanes
@@ -266,14 +311,18 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
         topk_idx[(size_t)t * k + l] = idx;
         topk_weights[(size_t)t * k + l] = idx >= 0 ? e / denom * scale : 0.f;
     }
+    }
+#endif
 }
 
 template <bool BF16>
 void launch(const void* logits, int T, int E, int k, int over_all, float scale, int32_t* idx, float* w,
             hipStream_t stream) {
     auto grid = [&](int tokens) { return (unsigned)(((long long)T + 4 * tokens - 1) / (4 * tokens)); };
-    auto run = [&](auto kernel, int tokens) {
-        kernel<<<grid(tokens), kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
+    // passes: at most 8 waves per SIMD, whose next logits arrive while they choose
+    auto run = [&](auto kernel, int tokens, bool passes = true) {
+        const unsigned g = grid(tokens);
+        kernel<<<passes && g > kRouterGroups ? kRouterGroups : g, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
     };
     if (k <= 16) {
         if (E <= 32) run(router_kernel<16, 2, BF16>, 4);
@@ -283,11 +332,11 @@ void launch(const void* logits, int T, int E, int k, int over_all, float scale, 
         else if (E <= 512) run(router_kernel<32, 16, BF16>, 2);
         else run(router_kernel<64, 16, BF16>, 1);
     } else {
-        if (E <= 64) run(router_wave_kernel<1, BF16>, 1);
-        else if (E <= 128) run(router_wave_kernel<2, BF16>, 1);
-        else if (E <= 256) run(router_wave_kernel<4, BF16>, 1);
-        else if (E <= 512) run(router_wave_kernel<8, BF16>, 1);
-        else run(router_wave_kernel<16, BF16>, 1);
+        if (E <= 64) run(router_wave_kernel<1, BF16>, 1, false);
+        else if (E <= 128) run(router_wave_kernel<2, BF16>, 1, false);
+        else if (E <= 256) run(router_wave_kernel<4, BF16>, 1, false);
+        else if (E <= 512) run(router_wave_kernel<8, BF16>, 1, false);
+        else run(router_wave_kernel<16, BF16>, 1, false);
     }
 }
 
