@@ -145,10 +145,19 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream as a handle, without a torch.cuda.Stream object
+        # (0.35 us a call instead of 2.8)
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
