@@ -310,11 +310,11 @@ __device__ inline void mfma_scaled(v4f& acc, const v8i& a, const v8i& b, uint32_
                      : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
 }
 
-template <int BM, int WAVES_M, int WAVES_N>
+template <int BM, int BN, int WAVES_M, int WAVES_N>
 struct Fp8Cfg {
-    static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
+    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int FM = WM / 16, FN = WN / 16;
-    static constexpr int A_BYTES = BM * kBK, B_BYTES = kBN * kBK;
+    static constexpr int A_BYTES = BM * kBK, B_BYTES = BN * kBK;
     // ring slots: all of the CU's 160 KB
     static constexpr int DB = BM == 256 ? 2 : BM == 128 ? 3 : 4;
     static constexpr int DA = BM == 256 ? 3 : 4;
@@ -322,17 +322,22 @@ struct Fp8Cfg {
     static constexpr int A_DMA = A_BYTES / 1024 / 4, B_DMA = B_BYTES / 1024 / 4;   // 1 KB loads per wave and step
     static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024, "");
     static_assert(DA == DB || DA == DB + 1, "issue order written for these");
-    static_assert(WN == 64 || WN == 128, "one scale block of B per wave");
+    // a wave's columns lie in one scale block of B, or (224 columns) a lane's fragments each
+    // have a scale word of their own
+    static constexpr bool ONE_BLOCK = WN == 64 || WN == 128;
+    static constexpr int NSB = ONE_BLOCK ? 1 : FN;
+    static_assert(BN % (16 * WAVES_N) == 0 && B_BYTES % 4096 == 0, "");
 };
 
-// STREAM: B is read by one row tile only, through non-temporal loads
-template <int BM, int WAVES_M, int WAVES_N, bool STREAM>
+// STREAM: B is read by one row tile only, through non-temporal loads. WIDE: N % 8 == 0, every row
+// and a lane's chunk aligned and a chunk wholly in or out, stored plainly.
+template <int BM, int BN, int WAVES_M, int WAVES_N, bool STREAM, bool WIDE>
 __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty kernel
 #if defined(__HIP_DEVICE_COMPILE__)
-    using C = Fp8Cfg<BM, WAVES_M, WAVES_N>;
+    using C = Fp8Cfg<BM, BN, WAVES_M, WAVES_N>;
     constexpr int WM = C::WM, WN = C::WN, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
-    constexpr int A_DMA = C::A_DMA, B_DMA = C::B_DMA;
+    constexpr int A_DMA = C::A_DMA, B_DMA = C::B_DMA, NSB = C::NSB;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     uint8_t* const bring = smem + DA * C::A_BYTES;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -342,16 +347,16 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 
     // ---- tile ------------------------------------------------------------------------------
     // Tile ids walk groups of 4 row tiles (of args.block_m rows) across all column tiles. The last
-    // round of 256 tiles, when it would be at most half full (256-row tiles only), is left to
+    // round of 256 tiles, when it would be at most half full (256 x 256 tiles only), is left to
     // the second launch (tail), whose workgroups take parts of BM rows of those tiles: 64 rows
     // where that still is one round, else 128.
     const bool dense = args.dense_rows > 0;
     const int bm = args.block_m;
     int num_mt = dense ? (args.dense_rows + bm - 1) / bm : __builtin_amdgcn_readfirstlane(args.meta[0]);
     if (num_mt > args.max_tiles) num_mt = args.max_tiles;
-    const int NT = (args.N + kBN - 1) / kBN;
+    const int NT = (args.N + BN - 1) / BN;
     const int total = num_mt * NT;
-    const int rem = bm == 256 ? total % kCus : 0;
+    const int rem = bm == 256 && BN == 256 ? total % kCus : 0;
     const int main_total = rem <= kCus / 2 ? total - rem : total;
     int v, part = 0;
     if (!args.tail) {
@@ -396,20 +401,25 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     for (int j = 0; j < B_DMA; ++j) {
         const int r = 8 * (wave * B_DMA + j) + (lane >> 3);
         const int f = r >> 4;
-        const int n = nt * kBN + (f / FN) * WN + (r & 15) * FN + f % FN;
-        b_off[j] = (uint32_t)(min(n, args.N - 1) - nt * kBN) * (uint32_t)args.K + chunk * 16;
+        const int n = nt * BN + (f / FN) * WN + (r & 15) * FN + f % FN;
+        b_off[j] = (uint32_t)(min(n, args.N - 1) - nt * BN) * (uint32_t)args.K + chunk * 16;
     }
     uint32_t sa_off[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)args.sf_stride;
     const int nblk = (args.N + 127) / 128;
-    const int blk = min((nt * kBN + wn * WN) >> 7, nblk - 1);
+    uint32_t sb_off[NSB];
+#pragma unroll
+    for (int f = 0; f < NSB; ++f) {
+        const int n = nt * BN + wn * WN + (C::ONE_BLOCK ? 0 : l * FN + f);
+        sb_off[f] = (uint32_t)min(n >> 7, nblk - 1) * (uint32_t)args.sf_stride;
+    }
     const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)args.a, 0, kAllRecords, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)args.a_sf, 0, kAllRecords, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(args.b + ((size_t)group * args.N + (size_t)nt * kBN) * args.K), 0, kAllRecords, kRsrcWord3);
+        (void*)(args.b + ((size_t)group * args.N + (size_t)nt * BN) * args.K), 0, kAllRecords, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(args.b_sf + ((size_t)group * nblk + blk) * args.sf_stride), 0, kAllRecords, kRsrcWord3);
+        (void*)(args.b_sf + (size_t)group * nblk * args.sf_stride), 0, kAllRecords, kRsrcWord3);
 
     auto load_a = [&](int ks, int j) __attribute__((always_inline)) {
         const int kc = min(ks, nks - 1);      // steps past the last reload it into a free slot
@@ -421,10 +431,10 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(bring + (ks % DB) * C::B_BYTES + (wave * B_DMA + j) * 1024), 16,
                                                  b_off[j], kc * kBK, 0, STREAM ? 2 : 0);
     };
-    uint32_t sa[2][FM], sb[2];
+    uint32_t sa[2][FM], sb[2][NSB];
     auto load_scale = [&](int kb, int i, int set) __attribute__((always_inline)) {
         if (i < FM) sa[set][i] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[i], kb * 4, 0);
-        else sb[set] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, 0, kb * 4, 0);
+        else sb[set][i - FM] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, sb_off[i - FM], kb * 4, 0);
     };
     const uint32_t rd_lo = (uint32_t)(l * kBK + ((g ^ (l & 7)) << 4));
     const uint32_t rd_hi = (uint32_t)(l * kBK + (((g + 4) ^ (l & 7)) << 4));
@@ -452,7 +462,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 
     // prologue: the scale words of block 0, then the loads that the steps before step 0 would
     // have issued (step s: B of s+DB, then A of s+DA)
-    constexpr int NS = FM + 1, SOPS = 4 - DB;
+    constexpr int NS = FM + NSB, SOPS = 4 - DB;
     const int last_kb = (nks - 1) >> 2;
 #pragma unroll
     for (int i = 0; i < NS; ++i) load_scale(0, i, 0);
@@ -511,11 +521,18 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
                 static_assert(WN_ < 64, "vmcnt range");
                 __builtin_amdgcn_s_waitcnt(0x0070 | (WN_ & 15) | (((WN_ >> 4) & 3) << 14));
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
+                if constexpr (OPS == 3) {
+                    // the next block's scale words have landed: no wait of the compiler's own for them
+#pragma unroll
+                    for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(sa[SET ^ 1][f]));
+#pragma unroll
+                    for (int f = 0; f < NSB; ++f) asm volatile("" : "+v"(sb[SET ^ 1][f]));
+                }
             }
             a_cur = a_nx;
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn) {
-                mfma_scaled<OPS>(acc[fm][fn], a_cur, bq[fn], sa[SET][fm], sb[SET]);
+                mfma_scaled<OPS>(acc[fm][fn], a_cur, bq[fn], sa[SET][fm], sb[SET][C::ONE_BLOCK ? 0 : fn]);
                 if (fn == 0) a_nx = fm + 1 < FM ? read_a(ks, fm + 1) : read_a(ks + 1, 0);
                 if (fm == FM - 1) {
                     bq[fn] = read_b(ks + 1, fn);
@@ -558,38 +575,34 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
         for (int fn = 0; fn < FN; ++fn) asm volatile("" : "+a"(acc[fm][fn]));
 
     // ---- epilogue: rows 16*fm + 4g + r, columns col0 .. col0 + FN-1 ----------------------------
-    const int col0 = nt * kBN + wn * WN + l * FN;
+    const int col0 = nt * BN + wn * WN + l * FN;
     uint16_t* const d = static_cast<uint16_t*>(args.d);
-    auto store = [&](auto aligned_c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int fm = 0; fm < FM; ++fm) {
+    for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
-                if (row < 0) continue;
-                uint32_t pk[FN / 2];
+        for (int r = 0; r < 4; ++r) {
+            const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
+            if (row < 0) continue;
+            uint32_t pk[(FN + 1) / 2];
 #pragma unroll
-                for (int q = 0; q < FN / 2; ++q) {
-                    const v2f x = {acc[fm][2 * q][r], acc[fm][2 * q + 1][r]};
-                    pk[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
-                }
-                uint16_t* dst = d + (size_t)row * args.N + col0;
-                if constexpr (decltype(aligned_c)::value) {
-                    if (col0 >= args.N) continue;
-                    if constexpr (FN == 8) *reinterpret_cast<v4i*>(dst) = (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]};
-                    else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-                } else {
-                    uint16_t out[FN];
+            for (int q = 0; q < FN; q += 2) {
+                const v2f x = {acc[fm][q][r], acc[fm][q + 1 < FN ? q + 1 : q][r]};
+                pk[q / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
+            }
+            uint16_t* dst = d + (size_t)row * args.N + col0;
+            if constexpr (WIDE) {
+                static_assert(FN == 8 || FN == 4, "");
+                if (col0 >= args.N) continue;
+                if constexpr (FN == 8) *reinterpret_cast<v4i*>(dst) = (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]};
+                else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+            } else {
+                uint16_t out[FN];
 #pragma unroll
-                    for (int q = 0; q < FN; ++q) out[q] = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
-                    store_columns<FN>(dst, out, args.N - col0);
-                }
+                for (int q = 0; q < FN; ++q) out[q] = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
+                store_columns<FN>(dst, out, args.N - col0);
             }
         }
-    };
-    // where every row and chunk is aligned and a chunk wholly in or out, plain wide stores
-    if (args.N % 8 == 0) store(IntC<1>{});
-    else store(IntC<0>{});
+    }
 #endif
 }
 
@@ -598,6 +611,12 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 // v_mfma_f32_16x16x32_bf16. One barrier per step: behind it the loads of two steps ahead go into
 // the slot that every wave has finished reading.
 constexpr int kF32Rows = 128;
+
+// acc += A x B in bf16, the accumulators in place (the builtin moves 104 of 128 of them through other
+// registers every step). The conversions write the operands right before: 2 wait states.
+__device__ inline void mfma_bf16(v4f& acc, const v8bf& a, const v8bf& b) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
 
 __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -677,7 +696,11 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
-        for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < FN; ++n) {
+            acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+            asm volatile("" : "+a"(acc[f][n]));
+        }
+    asm volatile("s_nop 7" ::: "memory");          // accumulator writes -> first MFMA
     // the scale bytes of a step are copied out of their set before the set is loaded again
     auto step = [&](int ks, auto set_c) __attribute__((always_inline)) {
         constexpr int S = decltype(set_c)::value;
@@ -704,7 +727,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
             for (int q = 0; q < 4; ++q) {
                 const v8bf bv = to_bf16(w[2 * q], w[2 * q + 1], fb);
 #pragma unroll
-                for (int f = 0; f < FM; ++f) acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[f][q], bv, acc[f][n], 0, 0, 0);
+                for (int f = 0; f < FM; ++f) mfma_bf16(acc[f][n], av[f][q], bv);
             }
         }
     };
@@ -717,6 +740,12 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
     // the last steps' reloads must land before the workgroup's LDS is given back
     __builtin_amdgcn_s_waitcnt(0x0F70);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // the accumulators' reads stay behind the wait states that the last MFMA's result needs
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) asm volatile("" : "+a"(acc[f][n]));
 
     const int col0 = nt * kBN + wn * 128 + l * FN;
     float* const d = static_cast<float*>(args.d);
@@ -742,6 +771,12 @@ void launch_skinny(size_t tiles64, const GemmFp8Args& a, hipStream_t stream) {
     else gemm_fp8_skinny<BM, BN, WAVES, false><<<grid, WAVES * 64, 0, stream>>>(a);
 }
 
+template <int BM, int WAVES_M, int WAVES_N, bool STREAM>
+void launch_tiled(unsigned grid, const GemmFp8Args& a, hipStream_t stream) {
+    if (a.N % 8 == 0) gemm_fp8_tiled<BM, kBN, WAVES_M, WAVES_N, STREAM, true><<<grid, 256, 0, stream>>>(a);
+    else gemm_fp8_tiled<BM, kBN, WAVES_M, WAVES_N, STREAM, false><<<grid, 256, 0, stream>>>(a);
+}
+
 // Microseconds of a round of 256 workgroups of each kernel, as fixed + per-step (128 K) parts,
 // fitted to 16 products from 256 x 256 x 2048 to 4096 x 4096 x 7168 timed with every kernel (each
 // prediction within 15 % of its measurement; for instance 1000 x 1000 x 7168, bf16: 78, 43, 33, 22
@@ -755,6 +790,7 @@ struct Cost {
 constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 6.0, 1.45},
                           {Fp8Kernel::kTiled128, 128, 128, 256, 4.0, 0.83},
                           {Fp8Kernel::kTiled64, 64, 64, 256, 4.9, 0.57},
+                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 10.0, 1.31},
                           {Fp8Kernel::kSkinny64, 64, 64, 64, 4.0, 0.2275},
                           {Fp8Kernel::kSkinny32, 64, 32, 32, 1.6, 0.10}};
 constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 8.0, 1.92},
@@ -800,23 +836,26 @@ hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_
     const size_t grid = mt * (size_t)cdiv(a.N, kBN);
     switch (plan.kernel) {
         case Fp8Kernel::kTiled256: {
-            gemm_fp8_tiled<256, 2, 2, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            launch_tiled<256, 2, 2, false>((unsigned)grid, a, stream);
             GemmFp8Args t = a;
             t.tail = 1;
             // the leftover tiles' number is known on the host for a dense product only
             const size_t rem = grid % kCus;
             const bool dense = a.dense_rows > 0;
-            if (!dense || (rem > 0 && rem <= kCus / 4)) gemm_fp8_tiled<64, 1, 4, false><<<kCus, 256, 0, stream>>>(t);
-            if (!dense || (rem > kCus / 4 && rem <= kCus / 2)) gemm_fp8_tiled<128, 2, 2, false><<<kCus, 256, 0, stream>>>(t);
+            if (!dense || (rem > 0 && rem <= kCus / 4)) launch_tiled<64, 1, 4, false>(kCus, t, stream);
+            if (!dense || (rem > kCus / 4 && rem <= kCus / 2)) launch_tiled<128, 2, 2, false>(kCus, t, stream);
             break;
         }
+        case Fp8Kernel::kTiled256x224:
+            gemm_fp8_tiled<256, 224, 2, 2, false, false><<<(unsigned)(mt * cdiv(a.N, 224)), 256, 0, stream>>>(a);
+            break;
         case Fp8Kernel::kTiled128:
             if (a.out_f32) gemm_fp8_tiled_f32<<<(unsigned)grid, 256, 0, stream>>>(a);
-            else gemm_fp8_tiled<128, 2, 2, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            else launch_tiled<128, 2, 2, false>((unsigned)grid, a, stream);
             break;
         case Fp8Kernel::kTiled64:
-            if (plan.stream) gemm_fp8_tiled<64, 1, 4, true><<<(unsigned)grid, 256, 0, stream>>>(a);
-            else gemm_fp8_tiled<64, 1, 4, false><<<(unsigned)grid, 256, 0, stream>>>(a);
+            if (plan.stream) launch_tiled<64, 1, 4, true>((unsigned)grid, a, stream);
+            else launch_tiled<64, 1, 4, false>((unsigned)grid, a, stream);
             break;
         case Fp8Kernel::kSkinny64: launch_skinny<64, 64, 4>(mt, a, stream); break;
         case Fp8Kernel::kSkinny32: launch_skinny<32, 32, 8>(mt, a, stream); break;
