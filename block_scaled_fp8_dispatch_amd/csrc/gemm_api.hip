@@ -341,9 +341,14 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     const Fp8Plan plan = fp8_plan(groups, (double)m / groups, true, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
     auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-    if (launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets), i32(W.perm),
-                     i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream) != hipSuccess)
-        return MOE_ERR_HIP;
+    // one launch where one workgroup can hold all ids (8192 rows: 273 -> 248 us for the whole call)
+    const hipError_t grouped =
+        m <= kGroupMaxRows
+            ? launch_group_rows(group_of_row, m, groups, BM, i32(W.perm), i32(W.meta), i32(W.tile_expert),
+                                i32(W.tile_row0), stream)
+            : launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets),
+                           i32(W.perm), i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream);
+    if (grouped != hipSuccess) return MOE_ERR_HIP;
     const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, cdiv(m, BM) + groups);
     return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

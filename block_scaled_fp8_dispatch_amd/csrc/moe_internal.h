@@ -150,6 +150,12 @@ hipError_t launch_gemm_layout(int G, int max_m, const int32_t* masked_m, int blo
                               int pad_rows_cap, int32_t* perm, int32_t* tile_expert,
                               int32_t* tile_row0, int32_t* meta, hipStream_t stream);
 
+// Row list and tile list of the FP8 x FP8 contiguous GEMM in one launch, up to kGroupMaxRows rows
+// (route.hip)
+constexpr int kGroupMaxRows = 16384;
+hipError_t launch_group_rows(const int32_t* ids, int m, int G, int block_m, int32_t* perm, int32_t* meta,
+                             int32_t* tile_expert, int32_t* tile_row0, hipStream_t stream);
+
 // FP8 cast of bf16 rows (cast.hip)
 hipError_t launch_cast_fp8(const uint16_t* x, int rows, int cols, uint8_t* q, uint8_t* sf,
                            hipStream_t stream);

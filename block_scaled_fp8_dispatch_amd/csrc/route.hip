@@ -467,7 +467,102 @@ __global__ __launch_bounds__(1024) void gemm_layout_kernel(int G, int max_m,
     }
 }
 
+// Rows of the FP8 x FP8 contiguous GEMM grouped by their id in one launch: as the routing above,
+// but a row's place within its group does not matter (each row of D depends on its own row of A
+// only), so places are handed out by LDS atomics, one per wave where all its rows are of one
+// group. Full tiles first, then each group's last, partly filled one.
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupPer = kGroupMaxRows / kGroupThreads;
+
+__global__ __launch_bounds__(kGroupThreads) void group_rows_kernel(const int32_t* __restrict__ ids, int m, int G,
+                                                                   int block_m, int32_t* __restrict__ perm,
+                                                                   int32_t* __restrict__ meta,
+                                                                   int32_t* __restrict__ tile_expert,
+                                                                   int32_t* __restrict__ tile_row0) {
+    __shared__ int next[kMaxE];                          // rows of a group, then its next free place
+    __shared__ int row_of[kMaxE], foff[kMaxE + 1], pad_lo[kMaxE], pad_hi[kMaxE];
+    __shared__ int warp_sums[16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    int ev[kGroupPer];
+#pragma unroll
+    for (int i = 0; i < kGroupPer; ++i) {
+        const int s = i * kGroupThreads + tid;
+        const int e = s < m ? ids[s] : -1;
+        ev[i] = e >= 0 && e < G ? e : -1;
+    }
+    if (tid < G) next[tid] = 0;
+    __syncthreads();
+    // takes one place of group e per lane that has one (e >= 0): the lane's place counted from next[e]
+    auto take = [&](int e) __attribute__((always_inline)) -> int {
+        const uint64_t have = __ballot(e >= 0);
+        if (have == 0) return 0;
+        const int e0 = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)have) - 1);
+        if (__ballot(e == e0) == have) {
+            int base = 0;
+            if (lane == 0) base = atomicAdd(&next[e0], __popcll(have));
+            return __builtin_amdgcn_readfirstlane(base) + __popcll(have & ((1ull << lane) - 1));
+        }
+        return e >= 0 ? atomicAdd(&next[e], 1) : 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kGroupPer; ++i) {
+        if (i * kGroupThreads >= m) break;               // uniform
+        take(ev[i]);
+    }
+    __syncthreads();
+    const int c = tid < G ? next[tid] : 0;
+    const int full = c / block_m, part = c % block_m != 0;
+    int n_full = 0, n_part = 0, n_rows = 0;
+    const int f0 = block_exclusive_scan_1024(full, warp_sums, &n_full);
+    __syncthreads();
+    const int p0 = block_exclusive_scan_1024(part, warp_sums, &n_part);
+    __syncthreads();
+    const int r0 = block_exclusive_scan_1024((full + part) * block_m, warp_sums, &n_rows);
+    if (tid < G) {
+        foff[tid] = f0;
+        pad_lo[tid] = r0 + c;
+        pad_hi[tid] = r0 + (full + part) * block_m;
+        row_of[tid] = r0;
+        next[tid] = r0;
+    }
+    if (tid == 0) {
+        foff[G] = n_full;
+        meta[0] = n_full + n_part;
+        meta[3] = n_full;
+    }
+    // the partly filled tile
+    if (part) {
+        tile_expert[n_full + p0] = tid;
+        tile_row0[n_full + p0] = r0 + full * block_m;
+    }
+    __syncthreads();
+    for (int t = tid; t < n_full; t += kGroupThreads) {
+        const int g = upper_group(foff, G, t);
+        tile_expert[t] = g;
+        tile_row0[t] = row_of[g] + (t - foff[g]) * block_m;
+    }
+    // padding rows of perm: kGroupThreads / G threads per group
+    {
+        const int tpe = kGroupThreads / G, g = tid / tpe;
+        if (g < G)
+            for (int r = pad_lo[g] + tid % tpe; r < pad_hi[g]; r += tpe) perm[r] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroupPer; ++i) {
+        if (i * kGroupThreads >= m) break;               // uniform
+        const int place = take(ev[i]);
+        if (ev[i] >= 0) perm[place] = i * kGroupThreads + tid;
+    }
+}
+
 }  // namespace
+
+hipError_t launch_group_rows(const int32_t* ids, int m, int G, int block_m, int32_t* perm, int32_t* meta,
+                             int32_t* tile_expert, int32_t* tile_row0, hipStream_t stream) {
+    if (G < 1 || G > MOE_MAX_EXPERTS || m < 0 || m > kGroupMaxRows) return hipErrorInvalidValue;
+    group_rows_kernel<<<1, kGroupThreads, 0, stream>>>(ids, m, G, block_m, perm, meta, tile_expert, tile_row0);
+    return hipGetLastError();
+}
 
 hipError_t launch_gemm_layout(int G, int max_m, const int32_t* masked_m, int block_m,
                               int pad_rows_cap, int32_t* perm, int32_t* tile_expert,

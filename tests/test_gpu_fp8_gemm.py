@@ -144,7 +144,8 @@ def test_dense_many_tiles(M, N, K):
 
 @pytest.mark.parametrize("d_type", [moe.MOE_BF16, moe.MOE_F32])
 @pytest.mark.parametrize("M,N,K,G", [(700, 512, 512, 3), (90, 129, 256, 5), (5000, 264, 384, 7), (1, 40, 128, 2),
-                                     (2600, 520, 640, 2), (9000, 2055, 256, 5)])
+                                     (2600, 520, 640, 2), (9000, 2055, 256, 5),
+                                     (20000, 130, 128, 3), (16384, 70, 128, 1024), (3000, 64, 128, 513)])
 def test_contiguous(M, N, K, G, d_type):
     print(f"[fp8] contiguous {M} {N} {K} {G} {d_type}", flush=True)
     p = Problem(M, N, K, G, d_type, seed=M)
