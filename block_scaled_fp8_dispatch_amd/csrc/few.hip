@@ -34,8 +34,11 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kMaxT = MOE_FEW_MAX_TOKENS;
-// Largest x kept in LDS (beside 35 KB of few_linear1's own)
+// Largest x kept in LDS (beside 31.5 KB of few_linear1's own)
 constexpr size_t kMaxXLds = 120 * 1024;
+constexpr int kRsrcWord3 = 0x00020000;   // raw buffer descriptor: byte offsets, no swizzle
+constexpr int kAllRecords = -1;
+constexpr int kNt = 2;                   // buffer loads: non-temporal
 
 // A row of a chosen expert: the token's first slot that names it, and its weights' sum
 struct FewRow {
@@ -127,32 +130,39 @@ __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, c
                                     int k1, int lane, const uint8_t* xl, v4f (&ag)[FM], v4f (&au)[FM]) {
     const int g = lane >> 4, l = lane & 15;
     const int xsfs = 4 * ((p.H + 511) / 512);
-    const uint8_t *xa[FM], *xs[FM];
+    // (buffers with 32-bit offsets: at most 32 rows, and 64-bit addresses of each row would spill)
+    uint32_t xa[FM], xs[FM];
     int sw[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         const int t = tok[min(f * 16 + l, cnt - 1)];     // rows past the last repeat it, unused
-        xa[f] = XLDS ? xl + (size_t)t * p.H : p.x + (size_t)t * p.H + 16 * g;
-        xs[f] = p.x_sf + (size_t)t * xsfs;
+        xa[f] = (uint32_t)t * (uint32_t)p.H + (XLDS ? 0 : 16 * g);
+        xs[f] = (uint32_t)t * (uint32_t)xsfs;
         sw[f] = t & 7;
     }
+    const __amdgpu_buffer_rsrc_t rs_x = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_xsf = __builtin_amdgcn_make_buffer_rsrc((void*)p.x_sf, 0, kAllRecords, kRsrcWord3);
     auto load = [&](Chunk<C, FM>& c, int ks) __attribute__((always_inline)) {
         // steps past the last reload it (never multiplied)
         const int kb = min(ks, k1 - 1) >> 2;
-        c.s0 = load_nt_word(bs + (size_t)kb * kBScaleBlockBytes);
-        c.s1 = load_nt_word(bs + (size_t)kb * kBScaleBlockBytes + 8 * 256);
+        const __amdgpu_buffer_rsrc_t rs_s =
+            __builtin_amdgcn_make_buffer_rsrc((void*)(bs + (size_t)kb * kBScaleBlockBytes), 0, kAllRecords, kRsrcWord3);
+        c.s0 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 0, kNt);
+        c.s1 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 8 * 256, kNt);
 #pragma unroll
-        for (int f = 0; f < FM; ++f) c.sa[f] = *reinterpret_cast<const uint32_t*>(xs[f] + 4 * kb);
+        for (int f = 0; f < FM; ++f) c.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_xsf, xs[f], 4 * kb, 0);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int kc = min(ks + i, k1 - 1);
-            c.b0[i] = load_nt(bd + (size_t)kc * kBTileBytes);
-            c.b1[i] = load_nt(bd + (size_t)kc * kBTileBytes + 8 * kFragBytes);
+            const __amdgpu_buffer_rsrc_t rs_b =
+                __builtin_amdgcn_make_buffer_rsrc((void*)(bd + (size_t)kc * kBTileBytes), 0, kAllRecords, kRsrcWord3);
+            c.b0[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 0, kNt));
+            c.b1[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 8 * kFragBytes, kNt));
             if constexpr (XLDS) continue;
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
-                const v4i lo = *reinterpret_cast<const v4i*>(xa[f] + kc * 128);
-                const v4i hi = *reinterpret_cast<const v4i*>(xa[f] + kc * 128 + 64);
+                const v4i lo = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_x, xa[f], kc * 128, 0));
+                const v4i hi = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_x, xa[f] + 64, kc * 128, 0));
                 c.a[f][i] = (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             }
         }
@@ -163,7 +173,7 @@ __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, c
             for (int i = 0; i < C; ++i)
 #pragma unroll
                 for (int f = 0; f < FM; ++f) {
-                    const uint8_t* x = xa[f] + min(ks + i, k1 - 1) * 128;
+                    const uint8_t* x = xl + xa[f] + min(ks + i, k1 - 1) * 128;
                     const v4i lo = *reinterpret_cast<const v4i*>(x + ((g ^ sw[f]) << 4));
                     const v4i hi = *reinterpret_cast<const v4i*>(x + (((g + 4) ^ sw[f]) << 4));
                     c.a[f][i] = (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -226,9 +236,11 @@ __global__ __launch_bounds__(512 * KS, 4) void few_linear1(FewArgs p) {
         const int nth = used + __popcll(b & ((1ull << lane) - 1));    // this lane's expert is the nth chosen
         if (expert < 0) {
             const uint64_t hit = __ballot(m != 0 && nth == u);
-            int before = nth < u ? __popc(m) : 0;
-            for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
-            row_base += before;
+            if (nb == 0) {                             // uniform
+                int before = nth < u ? __popc(m) : 0;
+                for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
+                row_base += before;
+            }
             if (hit) expert = e0 + __ffsll((unsigned long long)hit) - 1;
         }
         used += n;
@@ -254,8 +266,8 @@ __global__ __launch_bounds__(512 * KS, 4) void few_linear1(FewArgs p) {
     if (nb == 0 && tid == 0) p.segs[u] = FewSeg{expert, row_base, cnt};
     __syncthreads();
 
-    const uint8_t* bd = p.w1d + (size_t)expert * p.w1d_expert + (size_t)nb * p.w1d_ntile + cw * kFragBytes + lane * 16;
-    const uint8_t* bs = p.w1s + (size_t)expert * p.w1s_expert + (size_t)nb * p.w1s_ntile + cw * 256 + lane * 4;
+    const uint8_t* bd = p.w1d + (size_t)expert * p.w1d_expert + (size_t)nb * p.w1d_ntile + cw * kFragBytes;
+    const uint8_t* bs = p.w1s + (size_t)expert * p.w1s_expert + (size_t)nb * p.w1s_ntile + cw * 256;
     v4f ag[FM], au[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) ag[f] = au[f] = (v4f){0.f, 0.f, 0.f, 0.f};

@@ -17,8 +17,10 @@ constexpr int kGemmMinBlockM = 64;
 constexpr size_t kSplitPartialBytes = size_t(16) << 20;
 // Split K only when the output tiles would fill fewer than this many workgroups
 constexpr int kSplitBelowTiles = 128;
-// Largest K of the FP8 x FP8 GEMMs: a tile's 256 rows of B stay within 32-bit offsets
+// Largest K of the FP8 x FP8 GEMMs: a tile's 256 rows of B stay within 32-bit offsets; largest N: a
+// last tile's columns can be numbered in 32 bits
 constexpr int kFp8MaxK = 1 << 22;
+constexpr int kFp8MaxN = 1 << 30;
 // Workgroups split-K aims for (the CUs of one MI355X)
 constexpr int kSplitTargetWorkgroups = 256;
 
@@ -139,7 +141,7 @@ void split_plan(int tiles, int BM, int K, int& splits, int& ks_split) {
 
 // FP8 x FP8: N any positive number, B unpacked
 bool fp8_shape_ok(int G, int N, int K, int d_type) {
-    if (G < 1 || G > MOE_MAX_EXPERTS || N < 1) return false;
+    if (G < 1 || G > MOE_MAX_EXPERTS || N < 1 || N > kFp8MaxN) return false;
     if (K < 128 || K % 128 != 0 || K > kFp8MaxK) return false;
     return d_type == MOE_BF16 || d_type == MOE_F32;
 }
@@ -302,7 +304,8 @@ int moe_cast_to_fp8(const uint16_t* x, int32_t rows, int32_t cols, uint8_t* x_fp
 }
 
 size_t moe_fp8_gemm_workspace_bytes(int32_t max_rows, int32_t groups) {
-    return moe_gemm_workspace_bytes(max_rows, groups);
+    if (moe_gemm_workspace_bytes(max_rows, groups) == 0) return 0;
+    return gemm_ws(max_rows, groups).partial;     // the lists only: K is never split over workgroups
 }
 
 int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, int32_t m, int32_t n, int32_t k,
@@ -314,7 +317,7 @@ int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     if (!rows_ok(m, 1, k)) return MOE_ERR_TOKENS;
     if (!fp8_grid_ok(m, 1, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws(m, 1);
-    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     const Fp8Plan plan = fp8_plan(1, m, false, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
@@ -335,7 +338,7 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     if (!rows_ok(m, groups, k)) return MOE_ERR_TOKENS;
     if (!fp8_grid_ok(m, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws(m, groups);
-    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Fp8Plan plan = fp8_plan(groups, (double)m / groups, true, n, k, d_type == MOE_F32);
@@ -367,7 +370,7 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
     if (!fp8_grid_ok(rows + 64ll * groups, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws((int)rows, groups);
-    if (workspace_bytes < W.total) return MOE_ERR_WORKSPACE;
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;

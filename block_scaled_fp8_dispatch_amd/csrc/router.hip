@@ -16,6 +16,10 @@
 //
 // router_wave_kernel (k > 16): one wave per token, lane l holding experts l, 64 + l, ...: k rounds
 // of the wave's largest key and the lowest expert that holds it.
+//
+// 32768 x 256 FP32 logits, top-8: 12.6 us (2.7 TB/s of logits; a copy of the kernel that only loads them
+// takes 7.2), bound by the vector instructions of the key sorts and of the rounds. 128 x 256: 5.2 us,
+// a launch and one chain of dependent rounds. One wave per token takes 22 us for the first.
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -196,16 +200,16 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     constexpr uint32_t IDX = BF16 ? 0xffffu : L * V - 1;   // bits of the packed key that hold the expert
     static_assert((IDX & (IDX + 1)) == 0 && (int)IDX + 1 >= L * V, "");
     const int lane = threadIdx.x & 63, l = lane & (L - 1);
-    const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6)));
-    const int stride = (int)(gridDim.x * (kRouterThreads / 64)) * kTokens;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kRouterThreads / 64) + (threadIdx.x >> 6)));
+    const uint32_t tokens = (uint32_t)T, stride = gridDim.x * (kRouterThreads / 64) * kTokens;
     // The logits of a pass, one pass ahead: buffer loads from the pass's first row on, so that one
     // offset register serves them all. What lies past a row's end is never looked at; past the
     // last row the loads return 0.
     constexpr int kBytes = BF16 ? 2 : 4;
     const uint32_t offset = (uint32_t)(lane / L * E + l) * kBytes;
     float ahead[V];
-    auto load = [&](int t0) __attribute__((always_inline)) {
-        const size_t rest = (size_t)(T - t0) * E * kBytes;
+    auto load = [&](uint32_t t0) __attribute__((always_inline)) {
+        const size_t rest = (size_t)(tokens - t0) * E * kBytes;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(static_cast<const uint8_t*>(logits) + (size_t)t0 * E * kBytes), 0,
             (int)(uint32_t)(rest < 0xffffffffu ? rest : 0xffffffffu), 0x00020000);
@@ -217,15 +221,15 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
                 ahead[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, offset + i * L * kBytes, 0, 0));
         }
     };
-    int t0 = wave * kTokens;
-    if (t0 >= T) return;
+    uint32_t t0 = wave * kTokens;
+    if (t0 >= tokens) return;
     load(t0);
-    for (; t0 < T; t0 += stride) {
-    const int t = t0 + lane / L;
+    for (; t0 < tokens; t0 += stride) {
+    const uint32_t t = t0 + lane / L;
     float x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = ahead[i];
-    if (t0 + stride < T) load(t0 + stride);
+    if (t0 + stride < tokens) load(t0 + stride);
     // whether x[i] may be chosen (false for a NaN)
     auto valid = [&](int i) __attribute__((always_inline)) -> bool { return x[i] > -INFINITY && l < E - i * L; };
     int h[LISTS][D];
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
             }
         }
     }
-    const float v = idx >= 0 && t < T ? load_logit<BF16>(logits, (size_t)t * E + idx) : -INFINITY;
+    const float v = idx >= 0 && t < tokens ? load_logit<BF16>(logits, (size_t)t * E + idx) : -INFINITY;
     const float top = __shfl(v, lane & ~(L - 1), 64);
     const float e = idx >= 0 ? exp_below(v, top) : 0.f;
     float denom;
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     } else {
         denom = lanes_sum<16>(e);                  // the chosen sit in the token's first 16 lanes
     }
-    if (l < k && t < T) {
+    if (l < k && t < tokens) {
         topk_idx[(size_t)t * k + l] = idx;
         topk_weights[(size_t)t * k + l] = idx >= 0 ? e / denom * scale : 0.f;
     }

@@ -14,7 +14,7 @@
  * (byte j of a row = block j along K; bytes past K/128 are ignored). D is bf16 (the FP32 sum
  * rounded once to nearest even) or FP32, as d_type (MOE_BF16, MOE_F32 of moe_serving.h) says.
  *
- * Shapes: K a positive multiple of 128, at most 2^22; N any positive number; G (groups) in
+ * Shapes: K a positive multiple of 128, at most 2^22; N any number from 1 to 2^30; G (groups) in
  * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); fewer than 2^31 tiles
  * of 32 x 32 in D (MOE_ERR_SHAPE); B of any size.
  *
@@ -34,9 +34,9 @@ extern "C" {
 #endif
 
 /* Workspace bytes of a call whose A has up to `max_rows` rows in `groups` groups (dense: m
- * rows, 1 group; contiguous: m rows; masked: groups * max_m rows). Holds the row and tile
- * lists and a fixed area for the FP32 partial sums of products whose K is split over several
- * workgroups (added in a fixed order). Contents need no initialisation. 0 if unsupported. */
+ * rows, 1 group; contiguous: m rows; masked: groups * max_m rows): the row and tile lists. A
+ * workspace of moe_gemm_workspace_bytes for the same rows and groups serves as well. Contents
+ * need no initialisation. 0 if unsupported. */
 size_t moe_fp8_gemm_workspace_bytes(int32_t max_rows, int32_t groups);
 
 /* Dense: d [m][n] = A [m][k] . B [n][k]^T. m = 0 launches nothing. */

@@ -71,7 +71,7 @@ def test_fp8_gemm_refusals():
     for name in ("d", "a", "asf", "b", "bsf", "ws"):
         assert dense(**{name: None}) == moe.MOE_ERR_NULL, name
         assert dense(**{name: A + 4}) == moe.MOE_ERR_ALIGN, name
-    for bad in (dict(n=0), dict(n=-5), dict(k=0), dict(k=64), dict(k=200), dict(k=2 ** 23), dict(ty=2), dict(ty=-1),
+    for bad in (dict(n=0), dict(n=-5), dict(n=2 ** 30 + 1), dict(k=0), dict(k=64), dict(k=200), dict(k=2 ** 23), dict(ty=2), dict(ty=-1),
                 dict(m=2 ** 23, n=2 ** 30, k=128, wb=1 << 40)):
         assert dense(**bad) == moe.MOE_ERR_SHAPE, bad
     assert dense(m=-1) == moe.MOE_ERR_TOKENS
