@@ -7,11 +7,11 @@
 // With so few rows every product is a stream of packed weights, each fragment (16 columns x
 // 128 K, 1 KB) read once from memory straight into the registers of the one wave that
 // multiplies it (v_mfma_scale_f32_16x16x128_f8f6f4, the expert's tokens as rows). What counts is
-// bytes in flight: a wave loads one chunk of K steps ahead of the one it multiplies, about
-// 128 KB per CU in all. There is no routing pass: each workgroup of few_linear1 derives the
-// chosen experts from the T*k ids, as one bit mask of tokens per expert in LDS (bits are set by
-// integer atomics, whose order does not matter), and the first workgroup of each expert leaves
-// its (slot, weight) rows in the workspace for few_linear2.
+// bytes in flight: a wave loads one chunk of K steps ahead of the one it multiplies, 128 to
+// 256 KB per CU in all. There is no routing pass: each workgroup of few_linear1 derives the
+// chosen experts from the T*k ids (at most 64 of them: each wave for itself, in registers; more: as one
+// bit mask of tokens per expert in LDS, set by integer atomics, whose order does not matter), and the
+// first workgroup of each expert leaves its (slot, weight) rows in the workspace for few_linear2.
 //
 // few_linear1: a workgroup owns one 128-wide block of h of one chosen expert; wave w of 8 the
 // gate fragment w and the up fragment w, so the block's largest |h| of a row meets in LDS and
@@ -19,6 +19,16 @@
 // half of K (the sums meet in LDS). few_linear2: a workgroup owns 32 output columns; its 8 waves
 // share the (expert, 512 K) pieces, each adds w * (its partial products) per token into its own
 // FP32 tile in LDS, and the tiles are added in wave order.
+//
+// One or two tokens of 8 experts give few_linear1 fewer blocks than there are CUs, and a CU reads no more
+// than about 40 GB/s. Where h is at most 32 K elements a workgroup therefore takes half a block in four
+// parts of K and leaves h in FP32; every workgroup of few_linear2 requantises all of it into LDS, which
+// costs 1.7 us of the 7.7 saved (one token, top-8, H = 7168, I = 2048: 29.7 + 13.4 -> 22.0 + 15.1 us).
+//
+// Measured: 32 tokens, top-8 of 32 experts, H = 7168, I = 2048: 130 us for 749 MB of weights (85 us,
+// 5.9 TB/s, and 45 us); one token 37 us for 187 MB; 3 tokens of a 256 x 512 layer 9.8 us, two launches'
+// latency.
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -39,6 +49,8 @@ constexpr size_t kMaxXLds = 120 * 1024;
 constexpr int kRsrcWord3 = 0x00020000;   // raw buffer descriptor: byte offsets, no swizzle
 constexpr int kAllRecords = -1;
 constexpr int kNt = 2;                   // buffer loads: non-temporal
+// Most elements of h that few_linear2 requantises itself
+constexpr int kMaxH32 = 32 * 1024;
 
 // A row of a chosen expert: the token's first slot that names it, and its weights' sum
 struct FewRow {
@@ -65,11 +77,14 @@ __device__ inline float few_swiglu(float g, float u) {
     return g * u * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-__device__ inline v4i load_nt(const uint8_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
-}
-__device__ inline uint32_t load_nt_word(const uint8_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+// A buffer where something is left to read (left > 0), else one that loads read nothing from; both
+// uniform, and pinned to scalar registers (kept over blocks, a condition becomes a vector value, and the
+// loads become loops over its lanes)
+__device__ inline __amdgpu_buffer_rsrc_t rsrc_if(const uint8_t* p, int left) {
+    uint64_t base = (uint64_t)(uintptr_t)p;
+    int records = __builtin_amdgcn_readfirstlane(left > 0 ? kAllRecords : 0);
+    asm("" : "+s"(base), "+s"(records));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)base, 0, records, kRsrcWord3);
 }
 
 template <int OPS>
@@ -92,6 +107,7 @@ struct FewArgs {
     FewRow* rows;       // [T*k] the rows of the chosen experts, expert after expert
     FewSeg* segs;       // [min(E, T*k)] the chosen experts, ascending, with their rows
     int32_t* n_used;
+    float* h32;         // [T*k][I], where few_linear2 requantises
     uint16_t* y;
 };
 
@@ -123,39 +139,34 @@ __device__ inline void multiply(const Chunk<C, FM>& c, int ks, int nks, v4f (&c0
     step(std::integral_constant<int, 3>{});
 }
 
-// One wave's gate and up sums over K steps [k0, k1) for the expert's first 16 * FM tokens
-// (XLDS: x rows in LDS at xl, read right before their use, so that the registers hold weights only)
+// One wave's gate and up sums over K steps [k0, k1) for the expert's first 16 * FM tokens.
+// XLDS: x rows in LDS at xl, their scale bytes behind all T of them, read right before their use, so
+// that the registers hold weights only; the first weights are on their way when the workgroup's LDS
+// writes meet at a barrier here.
 template <int C, int FM, bool XLDS>
 __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, const uint8_t* bd, const uint8_t* bs, int k0,
                                     int k1, int lane, const uint8_t* xl, v4f (&ag)[FM], v4f (&au)[FM]) {
     const int g = lane >> 4, l = lane & 15;
-    const int xsfs = 4 * ((p.H + 511) / 512);
+    const uint32_t xsfs = 4 * (((uint32_t)p.H + 511) / 512);
+    const __amdgpu_buffer_rsrc_t rs_x = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, kAllRecords, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rs_xsf = __builtin_amdgcn_make_buffer_rsrc((void*)p.x_sf, 0, kAllRecords, kRsrcWord3);
     // (buffers with 32-bit offsets: at most 32 rows, and 64-bit addresses of each row would spill)
     uint32_t xa[FM], xs[FM];
     int sw[FM];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-        const int t = tok[min(f * 16 + l, cnt - 1)];     // rows past the last repeat it, unused
-        xa[f] = (uint32_t)t * (uint32_t)p.H + (XLDS ? 0 : 16 * g);
-        xs[f] = (uint32_t)t * (uint32_t)xsfs;
-        sw[f] = t & 7;
-    }
-    const __amdgpu_buffer_rsrc_t rs_x = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, kAllRecords, kRsrcWord3);
-    const __amdgpu_buffer_rsrc_t rs_xsf = __builtin_amdgcn_make_buffer_rsrc((void*)p.x_sf, 0, kAllRecords, kRsrcWord3);
     auto load = [&](Chunk<C, FM>& c, int ks) __attribute__((always_inline)) {
-        // steps past the last reload it (never multiplied)
+        // past the last step no weights are read, and x is read again (never multiplied)
         const int kb = min(ks, k1 - 1) >> 2;
-        const __amdgpu_buffer_rsrc_t rs_s =
-            __builtin_amdgcn_make_buffer_rsrc((void*)(bs + (size_t)kb * kBScaleBlockBytes), 0, kAllRecords, kRsrcWord3);
+        const __amdgpu_buffer_rsrc_t rs_s = rsrc_if(bs + (size_t)kb * kBScaleBlockBytes, k1 - ks);
         c.s0 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 0, kNt);
         c.s1 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 8 * 256, kNt);
+        if constexpr (!XLDS) {
 #pragma unroll
-        for (int f = 0; f < FM; ++f) c.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_xsf, xs[f], 4 * kb, 0);
+            for (int f = 0; f < FM; ++f) c.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_xsf, xs[f], 4 * kb, 0);
+        }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int kc = min(ks + i, k1 - 1);
-            const __amdgpu_buffer_rsrc_t rs_b =
-                __builtin_amdgcn_make_buffer_rsrc((void*)(bd + (size_t)kc * kBTileBytes), 0, kAllRecords, kRsrcWord3);
+            const __amdgpu_buffer_rsrc_t rs_b = rsrc_if(bd + (size_t)kc * kBTileBytes, k1 - ks - i);
             c.b0[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 0, kNt));
             c.b1[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 8 * kFragBytes, kNt));
             if constexpr (XLDS) continue;
@@ -170,19 +181,36 @@ __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, c
     auto rows = [&](Chunk<C, FM>& c, int ks) __attribute__((always_inline)) {
         if constexpr (XLDS) {
 #pragma unroll
-            for (int i = 0; i < C; ++i)
+            for (int f = 0; f < FM; ++f) {
+                c.sa[f] = *reinterpret_cast<const uint32_t*>(xl + xs[f] + min(ks, k1 - 1) / 4 * 4);
 #pragma unroll
-                for (int f = 0; f < FM; ++f) {
+                for (int i = 0; i < C; ++i) {
                     const uint8_t* x = xl + xa[f] + min(ks + i, k1 - 1) * 128;
                     const v4i lo = *reinterpret_cast<const v4i*>(x + ((g ^ sw[f]) << 4));
                     const v4i hi = *reinterpret_cast<const v4i*>(x + (((g + 4) ^ sw[f]) << 4));
                     c.a[f][i] = (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 }
+            }
         }
     };
-    if (k0 >= k1) return;
+    auto offsets = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            const uint32_t t = tok[min(f * 16 + l, cnt - 1)];     // rows past the last repeat it, unused
+            xa[f] = t * (uint32_t)p.H + (XLDS ? 0 : 16 * g);
+            xs[f] = t * xsfs + (XLDS ? (uint32_t)p.T * (uint32_t)p.H : 0);
+            sw[f] = t & 7;
+        }
+    };
     Chunk<C, FM> even, odd;
-    load(even, k0);
+    if constexpr (XLDS) {
+        load(even, k0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        offsets();
+    } else {
+        offsets();
+        load(even, k0);
+    }
     for (int ks = k0; ks < k1; ks += 2 * C) {
         load(odd, ks + C);
         rows(even, ks);
@@ -193,81 +221,156 @@ __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, c
     }
 }
 
-// FM: 16-row fragments an expert's tokens may need; KS: parts of K; C: K steps per chunk
-template <int FM, int KS, int C>
-__global__ __launch_bounds__(512 * KS, 4) void few_linear1(FewArgs p) {
-    constexpr int kThreads = 512 * KS;
-    __shared__ uint32_t mask[MOE_MAX_EXPERTS];
-    __shared__ int ids[kMaxT * MOE_MAX_TOPK];
+// The u-th chosen expert of at most 64 slots, its tokens (ascending) and their first slots, by each wave for
+// itself: lane s holds slot s, an expert's first slot stands for it, and its rank is the number of
+// smaller such. Also the number of chosen experts and the rows of those before this one.
+struct Chosen {
+    int expert, cnt, used, before;
+    uint64_t slots;            // the slots that stand for one of its tokens
+    uint64_t all;              // all slots that name it
+};
+__device__ inline Chosen choose64(const FewArgs& p, int lane, int u) {
+    const int S = p.T * p.k, t = lane / p.k;
+    const int id = lane < S ? p.idx[lane] : -1;
+    const int e = id >= 0 && id < p.E ? id : -1;
+    bool again = false, again_in_token = false;         // an earlier slot (of the token) names the same expert
+    for (int j = 0; j < S - 1; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        again = again || (j < lane && ej == e);
+        again_in_token = again_in_token || (j < lane && ej == e && j >= t * p.k);
+    }
+    const uint64_t first = __ballot(e >= 0 && !again);
+    int rank = 0;
+    for (uint64_t f = first; f != 0; f &= f - 1) rank += __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)f) - 1) < e;
+    Chosen c;
+    c.used = __popcll(first);
+    const uint64_t hit = __ballot(e >= 0 && !again && rank == u);
+    c.expert = hit ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)hit) - 1) : -1;
+    c.all = __ballot(e >= 0 && e == c.expert);
+    c.slots = __ballot(e >= 0 && e == c.expert && !again_in_token);
+    c.cnt = __popcll(c.slots);
+    c.before = __popcll(__ballot(e >= 0 && e < c.expert && !again_in_token));
+    return c;
+}
+
+// FM: 16-row fragments an expert's tokens may need; KS: parts of K; C: K steps per chunk; CW: column
+// waves (8: a whole block of h; 4: half of one, left in FP32 for few_linear2); S64: at most 64 slots
+template <int FM, int KS, int C, int CW, bool S64>
+__global__ __launch_bounds__(64 * CW * KS, 4) void few_linear1(FewArgs p) {
+    constexpr int kThreads = 64 * CW * KS;
+    static_assert(CW == 8 || (CW == 4 && FM == 1), "");
+    __shared__ uint32_t mask[S64 ? 1 : MOE_MAX_EXPERTS];
+    __shared__ int ids[S64 ? 1 : kMaxT * MOE_MAX_TOPK];
     __shared__ int tok[kMaxT], slot[kMaxT];        // the expert's tokens, ascending, and their first slots
-    extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];     // KS > 1: x, T * H bytes
+    extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];     // KS > 1: x and its scale bytes
     __shared__ uint32_t red[8][FM * 16];
     __shared__ __attribute__((aligned(16))) uint8_t codes[FM * 16][128];
-    __shared__ v4f part[KS > 1 ? 8 : 1][2 * FM][64];
+    __shared__ v4f part[KS > 1 ? KS - 1 : 1][KS > 1 ? CW : 1][2 * FM][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int cw = wave & 7, kp = wave >> 3;
+    const int cw = wave % CW, kp = wave / CW;
     const int g = lane >> 4, l = lane & 15;
-    const int NB = p.I / 128;
-    const int nb = blockIdx.x % NB, u = blockIdx.x / NB;      // the u-th chosen expert
+    const int NB = p.I / (16 * CW);
+    const int nb = blockIdx.x % NB, u = blockIdx.x / NB;      // columns of h, and the u-th chosen expert
 
-    // mask[e]: bit t set where token t names expert e
-    for (int e = tid; e < p.E; e += kThreads) mask[e] = 0;
-    __syncthreads();
-    for (int s = tid; s < p.T * p.k; s += kThreads) {
-        const int e = p.idx[s];
-        ids[s] = e;
-        if (e >= 0 && e < p.E) atomicOr(&mask[e], 1u << (s / p.k));
-    }
+    int expert, cnt;
+    const int xn = p.T * (p.H / 16), xsn = p.T * ((p.H + 511) / 512);     // 16-byte chunks of x, words of its scales
+    v4i x0{};                                      // the first chunk and word of each thread, under way early
+    uint32_t xs0 = 0;
     if constexpr (KS > 1) {
-        // x into LDS, 16-byte chunk c of a 128-byte step at chunk c ^ (token % 8)
-        for (int i = tid; i < p.T * (p.H / 16); i += kThreads) {
-            const int t = i / (p.H / 16), c = i - t * (p.H / 16);
-            *reinterpret_cast<v4i*>(xlds + (size_t)t * p.H + ((c ^ (t & 7)) << 4)) =
-                *reinterpret_cast<const v4i*>(p.x + (size_t)i * 16);
+        if (tid < xn) x0 = *reinterpret_cast<const v4i*>(p.x + (size_t)tid * 16);
+        if (tid < xsn) xs0 = *reinterpret_cast<const uint32_t*>(p.x_sf + (size_t)tid * 4);
+    }
+    Chosen ch{};
+    if constexpr (S64) {
+        ch = choose64(p, lane, u);
+        expert = ch.expert;
+        cnt = ch.cnt;
+        if (blockIdx.x == 0 && tid == 0) *p.n_used = ch.used;
+    } else {
+        // mask[e]: bit t set where token t names expert e
+        for (int e = tid; e < p.E; e += kThreads) mask[e] = 0;
+        __syncthreads();
+        for (int s = tid; s < p.T * p.k; s += kThreads) {
+            const int e = p.idx[s];
+            ids[s] = e;
+            if (e >= 0 && e < p.E) atomicOr(&mask[e], 1u << (s / p.k));
         }
     }
-    __syncthreads();
-    int expert = -1, used = 0, row_base = 0;       // rows of the experts before this one
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const uint32_t m = e0 + lane < p.E ? mask[e0 + lane] : 0u;
-        uint64_t b = __ballot(m != 0);
-        const int n = __popcll(b);
-        const int nth = used + __popcll(b & ((1ull << lane) - 1));    // this lane's expert is the nth chosen
-        if (expert < 0) {
-            const uint64_t hit = __ballot(m != 0 && nth == u);
-            if (nb == 0) {                             // uniform
-                int before = nth < u ? __popc(m) : 0;
-                for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
-                row_base += before;
+    // KS > 1: x into LDS, 16-byte chunk c of a 128-byte step at chunk c ^ (token % 8), then its scale bytes
+    auto x_store = [&](int i, const v4i& v) __attribute__((always_inline)) {
+        const int t = i / (p.H / 16), c = i - t * (p.H / 16);
+        *reinterpret_cast<v4i*>(xlds + (size_t)t * p.H + ((c ^ (t & 7)) << 4)) = v;
+    };
+    int row_base = 0;                              // rows of the experts before this one
+    if constexpr (S64) {
+        if (expert < 0) return;                    // fewer chosen experts than the grid allows for
+        row_base = ch.before;
+        if (wave == 0 && ((ch.slots >> lane) & 1)) {
+            const int i = __popcll(ch.slots & ((1ull << lane) - 1)), t = lane / p.k;
+            tok[i] = t;
+            slot[i] = lane;
+            if (nb == 0) {
+                float w = 0.f;
+                for (int j = lane; j < (t + 1) * p.k; ++j)
+                    if ((ch.all >> j) & 1) w += p.weights[j];
+                p.rows[row_base + i] = FewRow{lane, w};
             }
-            if (hit) expert = e0 + __ffsll((unsigned long long)hit) - 1;
         }
-        used += n;
-    }
-    expert = __builtin_amdgcn_readfirstlane(expert);
-    if (blockIdx.x == 0 && tid == 0) *p.n_used = used;
-    if (expert < 0) return;                        // fewer chosen experts than the grid allows for
-    const uint32_t m = mask[expert];
-    const int cnt = __popc(m);
-    if (tid < 32 && ((m >> tid) & 1u)) {
-        const int i = __popc(m & ((1u << tid) - 1));
-        int first = tid * p.k;
-        while (ids[first] != expert) ++first;            // the mask says that one is there
-        tok[i] = tid;
-        slot[i] = first;
-        if (nb == 0) {
-            float w = 0.f;
-            for (int j = first; j < (tid + 1) * p.k; ++j)
-                if (ids[j] == expert) w += p.weights[j];
-            p.rows[row_base + i] = FewRow{first, w};
+    } else {
+        __syncthreads();
+        expert = -1;
+        int used = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 64) {
+            const uint32_t m = e0 + lane < p.E ? mask[e0 + lane] : 0u;
+            uint64_t b = __ballot(m != 0);
+            const int n = __popcll(b);
+            const int nth = used + __popcll(b & ((1ull << lane) - 1));    // this lane's expert is the nth chosen
+            if (expert < 0) {
+                const uint64_t hit = __ballot(m != 0 && nth == u);
+                if (nb == 0) {                             // uniform
+                    int before = nth < u ? __popc(m) : 0;
+                    for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
+                    row_base += before;
+                }
+                if (hit) expert = e0 + __ffsll((unsigned long long)hit) - 1;
+            }
+            used += n;
+        }
+        expert = __builtin_amdgcn_readfirstlane(expert);
+        if (blockIdx.x == 0 && tid == 0) *p.n_used = used;
+        if (expert < 0) return;                        // fewer chosen experts than the grid allows for
+        const uint32_t m = mask[expert];
+        cnt = __builtin_amdgcn_readfirstlane(__popc(m));
+        if (tid < 32 && ((m >> tid) & 1u)) {
+            const int i = __popc(m & ((1u << tid) - 1));
+            int first = tid * p.k;
+            while (ids[first] != expert) ++first;            // the mask says that one is there
+            tok[i] = tid;
+            slot[i] = first;
+            if (nb == 0) {
+                float w = 0.f;
+                for (int j = first; j < (tid + 1) * p.k; ++j)
+                    if (ids[j] == expert) w += p.weights[j];
+                p.rows[row_base + i] = FewRow{first, w};
+            }
         }
     }
     if (nb == 0 && tid == 0) p.segs[u] = FewSeg{expert, row_base, cnt};
-    __syncthreads();
+    if constexpr (KS > 1) {
+        uint32_t* xs_lds = reinterpret_cast<uint32_t*>(xlds + (size_t)p.T * p.H);
+        if (tid < xn) x_store(tid, x0);
+        if (tid < xsn) xs_lds[tid] = xs0;
+        for (int i = tid + kThreads; i < xn; i += kThreads) x_store(i, *reinterpret_cast<const v4i*>(p.x + (size_t)i * 16));
+        for (int i = tid + kThreads; i < xsn; i += kThreads)
+            xs_lds[i] = *reinterpret_cast<const uint32_t*>(p.x_sf + (size_t)i * 4);
+    } else {
+        __syncthreads();
+    }
 
-    const uint8_t* bd = p.w1d + (size_t)expert * p.w1d_expert + (size_t)nb * p.w1d_ntile + cw * kFragBytes;
-    const uint8_t* bs = p.w1s + (size_t)expert * p.w1s_expert + (size_t)nb * p.w1s_ntile + cw * 256;
+    const int f0 = nb * CW % 8 + cw, blk = nb * CW / 8;        // fragment of the 128-column block, the block
+    const uint8_t* bd = p.w1d + (size_t)expert * p.w1d_expert + (size_t)blk * p.w1d_ntile + f0 * kFragBytes;
+    const uint8_t* bs = p.w1s + (size_t)expert * p.w1s_expert + (size_t)blk * p.w1s_ntile + f0 * 256;
     v4f ag[FM], au[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) ag[f] = au[f] = (v4f){0.f, 0.f, 0.f, 0.f};
@@ -285,18 +388,29 @@ __global__ __launch_bounds__(512 * KS, 4) void few_linear1(FewArgs p) {
         if (kp > 0) {
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
-                part[cw][2 * f][lane] = ag[f];
-                part[cw][2 * f + 1][lane] = au[f];
+                part[kp - 1][cw][2 * f][lane] = ag[f];
+                part[kp - 1][cw][2 * f + 1][lane] = au[f];
             }
         }
         __syncthreads();
         if (kp == 0) {
 #pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                ag[f] += part[cw][2 * f][lane];
-                au[f] += part[cw][2 * f + 1][lane];
-            }
+            for (int q = 0; q < KS - 1; ++q)
+#pragma unroll
+                for (int f = 0; f < FM; ++f) {
+                    ag[f] += part[q][cw][2 * f][lane];
+                    au[f] += part[q][cw][2 * f + 1][lane];
+                }
         }
+    }
+    if constexpr (CW == 4) {
+        // rows 4g + r, column 4l + cw of the half block
+        if (kp == 0)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * g + r < cnt)
+                    p.h32[(size_t)slot[4 * g + r] * p.I + nb * 64 + 4 * l + cw] = few_swiglu(ag[0][r], au[0][r]);
+        return;
     }
     // h of rows 16f + 4g + r, column 64*(cw/4) + 4*l + cw%4 of the block (the packed rows
     // are interleaved so); the largest |h| of a row over the block: DPP row, then the waves
@@ -348,8 +462,10 @@ __global__ __launch_bounds__(512 * KS, 4) void few_linear1(FewArgs p) {
 // Output columns per workgroup: two fragments
 constexpr int kFewCols = 32;
 
-template <int FM>
-__global__ __launch_bounds__(kFewThreads) void few_linear2(FewArgs p) {
+// H32: h comes in FP32 (at most kMaxH32 of it) and every workgroup requantises all of it into LDS while its
+// first weights arrive (the codes and scales also go to h8 and h_sf, one row per workgroup)
+template <int FM, bool H32>
+__global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
     constexpr int C = 4;
     // a token's row of a wave's tile: 36 floats, so that the 4 rows of a lane group fall into
     // different banks
@@ -360,10 +476,21 @@ __global__ __launch_bounds__(kFewThreads) void few_linear2(FewArgs p) {
     const int g = lane >> 4, l = lane & 15;
     // The experts and their rows in LDS: a dependent read from memory between the pieces would
     // wait for every weight load in flight (entries past the last are copied, not used)
-    __shared__ FewRow rows[kMaxT * MOE_MAX_TOPK];
-    __shared__ FewSeg segs[MOE_MAX_EXPERTS];
+    __shared__ FewRow rows[H32 ? 64 : kMaxT * MOE_MAX_TOPK];
+    __shared__ FewSeg segs[H32 ? 64 : MOE_MAX_EXPERTS];
     for (int i = tid; i < p.T * p.k; i += kFewThreads) rows[i] = p.rows[i];
     for (int i = tid; i < min(p.E, p.T * p.k); i += kFewThreads) segs[i] = p.segs[i];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[H32 ? kMaxH32 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[H32 ? kMaxH32 / 32 : 16];     // rows of 4 * ceil(I / 512)
+    v4f h[H32 ? kMaxH32 / 4 / kFewThreads : 1];
+    const int hn = p.T * p.k * p.I / 4;
+    if constexpr (H32) {
+#pragma unroll
+        for (int j = 0; j < kMaxH32 / 4 / kFewThreads; ++j) {
+            const int i = j * kFewThreads + tid;
+            if (j * kFewThreads < hn) h[j] = *reinterpret_cast<const v4f*>(p.h32 + 4 * (size_t)min(i, hn - 1));
+        }
+    }
     for (int i = lane; i < FM * 16 * kPitch; i += 64) (&tile[wave][0][0])[i] = 0.f;
     // each XCD (workgroup id mod 8) takes adjacent column tiles
     const int v = (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
@@ -371,55 +498,93 @@ __global__ __launch_bounds__(kFewThreads) void few_linear2(FewArgs p) {
     const int nks = p.I / 128, nkb = (nks + 3) / 4;
     const int items = __builtin_amdgcn_readfirstlane(*p.n_used) * nkb;
     const int first = (int)((long long)items * wave / kFewWaves), last = (int)((long long)items * (wave + 1) / kFewWaves);
-    const size_t hsfs = 4 * (size_t)nkb;
+    const uint32_t hsfs = 4 * (uint32_t)nkb;
     v4f c0[FM], c1[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) c0[f] = c1[f] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-    // where the loads stand: expert `lu` and its rows
-    int lu = -1;
+    // where the loads stand: piece `lit`, expert `lu` and its rows, 512 K number `lkb`; and the uses
+    int lit = first, lu = first / nkb, lkb = first - lu * nkb, ukb = lkb, uu = lu;
+    bool fresh = true;                             // the expert's addresses are not set yet
     int lcnt = 0;
-    const uint8_t *ha[FM], *hs[FM], *bd = nullptr, *bs = nullptr;
-    auto load = [&](Chunk<C, FM>& c, int it) __attribute__((always_inline)) {
-        it = min(it, last - 1);                    // past the last piece: reload it, never multiplied
-        const int u = it / nkb, kb = it - u * nkb;
-        if (u != lu) {
-            lu = u;
-            const FewSeg s = segs[u];
+    uint32_t ha[FM], hs[FM];
+    const uint8_t *bd = nullptr, *bs = nullptr;
+    auto load = [&](Chunk<C, FM>& c) __attribute__((always_inline)) {
+        const int left = last - lit;               // past the last piece nothing is read
+        const int kb = lkb;
+        if (fresh && left > 0) {
+            fresh = false;
+            const FewSeg s = segs[lu];
             const int e = __builtin_amdgcn_readfirstlane(s.expert);
             lcnt = __builtin_amdgcn_readfirstlane(s.count);
-            bd = p.w2d + (size_t)e * p.w2d_expert + (size_t)nt * p.w2d_ntile + frag * kFragBytes + lane * 16;
-            bs = p.w2s + (size_t)e * p.w2s_expert + (size_t)nt * p.w2s_ntile + frag * 256 + lane * 4;
+            bd = p.w2d + (size_t)e * p.w2d_expert + (size_t)nt * p.w2d_ntile + frag * kFragBytes;
+            bs = p.w2s + (size_t)e * p.w2s_expert + (size_t)nt * p.w2s_ntile + frag * 256;
+            if constexpr (!H32) {
 #pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                const int slot = rows[s.first + min(f * 16 + l, s.count - 1)].slot;
-                ha[f] = p.h8 + (size_t)slot * p.I + 16 * g;
-                hs[f] = p.h_sf + slot * hsfs;
+                for (int f = 0; f < FM; ++f) {
+                    const int slot = rows[s.first + min(f * 16 + l, s.count - 1)].slot;
+                    ha[f] = (uint32_t)slot * (uint32_t)p.I + 16 * g;
+                    hs[f] = (uint32_t)slot * hsfs;
+                }
             }
         }
-        c.s0 = load_nt_word(bs + (size_t)kb * kBScaleBlockBytes);
-        c.s1 = load_nt_word(bs + (size_t)kb * kBScaleBlockBytes + 256);
+        const __amdgpu_buffer_rsrc_t rs_s = rsrc_if(bs + (size_t)kb * kBScaleBlockBytes, left);
+        c.s0 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 0, kNt);
+        c.s1 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 256, kNt);
+        const __amdgpu_buffer_rsrc_t rs_h = rsrc_if(p.h8, left), rs_hsf = rsrc_if(p.h_sf, left);
+        if constexpr (!H32) {
 #pragma unroll
-        for (int f = 0; f < FM; ++f) c.sa[f] = *reinterpret_cast<const uint32_t*>(hs[f] + 4 * kb);
+            for (int f = 0; f < FM; ++f) c.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_hsf, hs[f], 4 * kb, 0);
+        }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int kc = min(4 * kb + i, nks - 1);
-            c.b0[i] = load_nt(bd + (size_t)kc * kBTileBytes);
-            c.b1[i] = load_nt(bd + (size_t)kc * kBTileBytes + kFragBytes);
+            const __amdgpu_buffer_rsrc_t rs_b = rsrc_if(bd + (size_t)kc * kBTileBytes, min(left, nks - 4 * kb - i));
+            c.b0[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 0, kNt));
+            c.b1[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, kFragBytes, kNt));
+            if constexpr (H32) continue;
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
                 if (f > 0 && lcnt <= 16) break;    // its rows are not used: whatever is there will do
-                const v4i lo = *reinterpret_cast<const v4i*>(ha[f] + kc * 128);
-                const v4i hi = *reinterpret_cast<const v4i*>(ha[f] + kc * 128 + 64);
+                const v4i lo = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_h, ha[f], kc * 128, 0));
+                const v4i hi = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_h, ha[f] + 64, kc * 128, 0));
                 c.a[f][i] = (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             }
         }
+        ++lit;
+        if (++lkb == nkb) {
+            lkb = 0;
+            ++lu;
+            fresh = true;
+        }
     };
-    // adds the products of the piece's expert to its tokens' sums once its last piece here is done
-    auto finish = [&](int it) __attribute__((always_inline)) {
-        const int u = it / nkb;
-        if (it + 1 < last && (it + 1) / nkb == u) return;
-        const FewSeg s = segs[u];
+    // H32: a piece's rows and their scales from LDS, right before their use
+    auto h_rows = [&](Chunk<C, FM>& c) __attribute__((always_inline)) {
+        if constexpr (H32) {
+            const int kb = ukb;
+            const FewSeg s = segs[uu];
+            const int slot = rows[s.first + min(l, s.count - 1)].slot;
+            c.sa[0] = *reinterpret_cast<const uint32_t*>(scales + (slot * nkb + kb) * 4);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const uint8_t* hc = codes + slot * p.I + min(4 * kb + i, nks - 1) * 128;
+                const v4i lo = *reinterpret_cast<const v4i*>(hc + ((g ^ (slot & 7)) << 4));
+                const v4i hi = *reinterpret_cast<const v4i*>(hc + (((g + 4) ^ (slot & 7)) << 4));
+                c.a[0][i] = (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            }
+        }
+    };
+    // multiplies a piece; adds the products of its expert to its tokens' sums once the last piece of it is done
+    auto use = [&](Chunk<C, FM>& c, int it) __attribute__((always_inline)) {
+        h_rows(c);
+        multiply<C, FM, 0>(c, ukb * 4, nks, c0, c1);
+        const FewSeg s = segs[uu];
+        const bool end = ++ukb == nkb;
+        if (end) {
+            ukb = 0;
+            ++uu;
+        }
+        if (!end && it + 1 < last) return;
 #pragma unroll
         for (int f = 0; f < FM; ++f)
 #pragma unroll
@@ -435,20 +600,60 @@ __global__ __launch_bounds__(kFewThreads) void few_linear2(FewArgs p) {
             }
     };
     __syncthreads();
+    Chunk<C, FM> even{}, odd{};
     if (first < last) {
-        Chunk<C, FM> even{}, odd{};
-        load(even, first);
-        for (int it = first; it < last; it += 2) {
-            load(odd, it + 1);
-            multiply<C, FM, 0>(even, (it % nkb) * 4, nks, c0, c1);
-            finish(it);
-            load(even, it + 2);
-            if (it + 1 < last) {
-                multiply<C, FM, 0>(odd, ((it + 1) % nkb) * 4, nks, c0, c1);
-                finish(it + 1);
+        load(even);
+        load(odd);
+    }
+    if constexpr (H32) {
+        // 4 values a thread, a 128-column block of a row on 32 lanes: its largest |h|, the scale byte, the
+        // codes; 16-byte chunk c of a block at chunk c ^ (row % 8)
+        const int down = 4 * kFewThreads / p.I, right = 4 * kFewThreads % p.I;
+        const int mine = (int)blockIdx.x, mine2 = mine + (int)gridDim.x;     // (at least 32 workgroups, at most 64 rows)
+        int row = 4 * tid / p.I, col = 4 * tid % p.I;
+#pragma unroll
+        for (int j = 0; j < kMaxH32 / 4 / kFewThreads; ++j) {
+            if (j * kFewThreads >= hn) continue;   // uniform
+            uint32_t a = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) a = max(a, __float_as_uint(fabsf(h[j][q])));
+            a = max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0xB1, 0xF, 0xF, false));
+            a = max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x4E, 0xF, 0xF, false));
+            a = max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x141, 0xF, 0xF, false));
+            a = max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x140, 0xF, 0xF, false));
+            a = max(a, (uint32_t)__shfl_xor((int)a, 16, 64));
+            const int byte = few_scale_byte(__uint_as_float(a));
+            const float mul = __uint_as_float((uint32_t)(254 - byte) << 23);
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(h[j][0] * mul, h[j][1] * mul, 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(h[j][2] * mul, h[j][3] * mul, w, true);
+            if (row < p.T * p.k) {
+                const int in = col & 127;
+                *reinterpret_cast<int*>(codes + row * p.I + (col - in) + ((((in >> 4) ^ row) & 7) << 4) + (in & 15)) = w;
+                if (in == 0) scales[row * 4 * nkb + (col >> 7)] = (uint8_t)byte;
+                if (row == mine || row == mine2) {
+                    *reinterpret_cast<int*>(p.h8 + row * p.I + col) = w;
+                    if (in == 0) p.h_sf[row * hsfs + (col >> 7)] = (uint8_t)byte;
+                }
+            }
+            row += down;
+            col += right;
+            if (col >= p.I) {
+                col -= p.I;
+                ++row;
             }
         }
+        // the LDS writes are done; the weights stay in flight
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
+    int it = first;
+    for (; it + 2 < last; it += 2) {
+        use(even, it);
+        load(even);
+        use(odd, it + 1);
+        load(odd);
+    }
+    if (it < last) use(even, it);
+    if (it + 1 < last) use(odd, it + 1);
     __syncthreads();
     // tile column 16*q + j: lane column j of fragment frag + q, row 128*(f/8) + 8*j + f%8 of the
     // 256-row tile; a thread stores the two adjacent columns of both fragments
@@ -480,7 +685,8 @@ FewLayout few_layout(const moe_shape_t& s) {
     L.rows = L.h_sf + align_up(slots * 4 * ((I + 511) / 512), 256);
     L.segs = L.rows + align_up(slots * sizeof(FewRow), 256);
     L.n_used = L.segs + align_up(slots * sizeof(FewSeg), 256);
-    L.total = L.n_used + 256;
+    L.h32 = L.n_used + 256;
+    L.total = L.h32 + align_up(std::min(slots * I, (size_t)kMaxH32) * sizeof(float), 256);
     return L;
 }
 
@@ -515,21 +721,27 @@ hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t
     p.rows = reinterpret_cast<FewRow*>(ws + W.rows);
     p.segs = reinterpret_cast<FewSeg*>(ws + W.segs);
     p.n_used = reinterpret_cast<int32_t*>(ws + W.n_used);
+    p.h32 = reinterpret_cast<float*>(ws + W.h32);
     p.y = y;
     // at most one expert per slot can be chosen
     const int max_used = s.num_experts < T * s.num_topk ? s.num_experts : T * s.num_topk;
     const unsigned g1 = (unsigned)max_used * (unsigned)(s.intermediate / 128), g2 = (unsigned)cdiv(s.hidden, 256) * 8u;
-    // With fewer workgroups than CUs, twice the waves in each, with x in LDS where it fits (the
-    // registers then hold weights only)
-    const size_t x_bytes = (size_t)T * s.hidden;
+    // With fewer workgroups than CUs, more waves in each, with x in LDS where it fits (the registers
+    // then hold weights only); where h is small, half blocks of it by twice the workgroups
+    const size_t x_bytes = (size_t)T * (s.hidden + 4 * cdiv(s.hidden, 512));
+    const int slots = T * s.num_topk;
     const bool split = g1 < 256 && T <= 16 && s.hidden >= 1024 && x_bytes <= kMaxXLds;
-    if (T <= 16) {
-        if (split) few_linear1<1, 2, 4><<<g1, 1024, x_bytes, stream>>>(p);
-        else few_linear1<1, 1, 2><<<g1, 512, 0, stream>>>(p);
-        few_linear2<1><<<g2, kFewThreads, 0, stream>>>(p);
+    if (T > 16) {
+        few_linear1<2, 1, 2, 8, false><<<g1, 512, 0, stream>>>(p);
+        few_linear2<2, false><<<g2, kFewThreads, 0, stream>>>(p);
+    } else if (split && slots <= 64 && (size_t)slots * s.intermediate <= kMaxH32) {
+        few_linear1<1, 4, 4, 4, true><<<2 * g1, 1024, x_bytes, stream>>>(p);
+        few_linear2<1, true><<<g2, kFewThreads, 0, stream>>>(p);
     } else {
-        few_linear1<2, 1, 2><<<g1, 512, 0, stream>>>(p);
-        few_linear2<2><<<g2, kFewThreads, 0, stream>>>(p);
+        if (split) few_linear1<1, 2, 4, 8, false><<<g1, 1024, x_bytes, stream>>>(p);
+        else if (slots <= 64) few_linear1<1, 1, 2, 8, true><<<g1, 512, 0, stream>>>(p);
+        else few_linear1<1, 1, 2, 8, false><<<g1, 512, 0, stream>>>(p);
+        few_linear2<1, false><<<g2, kFewThreads, 0, stream>>>(p);
     }
     return hipGetLastError();
 }

@@ -146,9 +146,9 @@ bool fp8_shape_ok(int G, int N, int K, int d_type) {
     return d_type == MOE_BF16 || d_type == MOE_F32;
 }
 
-// Whether the smallest tiles (32 x 32) of the product can be numbered
+// Whether tiles of 128 x 256, which exist for every output type, take a launch below 2^32 threads
 bool fp8_grid_ok(long long rows, int G, int N) {
-    return (rows / 32 + 2ll * G) * cdiv(N, 32) < (1ll << 31);
+    return (rows / 128 + G) * cdiv(N, kBN) < (1ll << 24);
 }
 
 GemmFp8Args fp8_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int N, int K, const uint8_t* b,
@@ -319,7 +319,7 @@ int moe_fp8_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     const GemmWs W = gemm_ws(m, 1);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
-    const Fp8Plan plan = fp8_plan(1, m, false, n, k, d_type == MOE_F32);
+    const Fp8Plan plan = fp8_plan(1, m, m, false, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
     GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
     g.dense_rows = m;
@@ -341,7 +341,7 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Fp8Plan plan = fp8_plan(groups, (double)m / groups, true, n, k, d_type == MOE_F32);
+    const Fp8Plan plan = fp8_plan(groups, (double)m / groups, m, true, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
     auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
     // one launch where one workgroup can hold all ids (8192 rows: 273 -> 248 us for the whole call)
@@ -368,13 +368,13 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (max_m < 0) return MOE_ERR_TOKENS;
     const long long rows = (long long)groups * max_m;
     if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
-    if (!fp8_grid_ok(rows + 64ll * groups, groups, n)) return MOE_ERR_SHAPE;
+    if (!fp8_grid_ok(rows, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws((int)rows, groups);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;
-    const Fp8Plan plan = fp8_plan(groups, rows_each, true, n, k, d_type == MOE_F32);
+    const Fp8Plan plan = fp8_plan(groups, rows_each, (int)rows, true, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
     if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
                            reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),

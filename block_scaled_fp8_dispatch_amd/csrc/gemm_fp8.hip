@@ -774,24 +774,28 @@ void launch_tiled(unsigned grid, const GemmFp8Args& a, hipStream_t stream) {
 struct Cost {
     Fp8Kernel kernel;
     int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
+    int threads;
     double fixed, step;
 };
-constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 6.0, 1.45},
-                          {Fp8Kernel::kTiled128, 128, 128, 256, 4.0, 0.83},
-                          {Fp8Kernel::kTiled64, 64, 64, 256, 4.9, 0.57},
-                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 10.0, 1.31},
-                          {Fp8Kernel::kSkinny64, 64, 64, 64, 4.0, 0.2275},
-                          {Fp8Kernel::kSkinny32, 64, 32, 32, 1.6, 0.10}};
-constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 8.0, 1.92},
-                         {Fp8Kernel::kSkinny64, 64, 64, 64, 4.2, 0.335},
-                         {Fp8Kernel::kSkinny32, 64, 32, 32, 2.0, 0.109}};
+constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 256, 6.0, 1.45},
+                          {Fp8Kernel::kTiled128, 128, 128, 256, 256, 4.0, 0.83},
+                          {Fp8Kernel::kTiled64, 64, 64, 256, 256, 4.9, 0.57},
+                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 256, 10.0, 1.31},
+                          {Fp8Kernel::kSkinny64, 64, 64, 64, 256, 4.0, 0.2275},
+                          {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 1.6, 0.10}};
+constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 256, 8.0, 1.92},
+                         {Fp8Kernel::kSkinny64, 64, 64, 64, 256, 4.2, 0.335},
+                         {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 2.0, 0.109}};
 
 template <size_t NK>
-Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, bool ragged, int N, int K) {
+Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, int max_rows, bool ragged, int N, int K) {
     Fp8Plan best{};
     double least = 0;
     const int steps = K / 128;
     for (const Cost& c : costs) {
+        // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
+        const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cdiv(N, c.bn);
+        if (c.kernel != Fp8Kernel::kTiled128 && grid * c.threads >= (1ull << 32)) continue;
         // groups of unknown length end in a tile that is half full on average
         const double mt = groups * (ragged ? rows / c.bm + 0.5 : std::ceil(rows / c.bm));
         const double tiles = std::ceil(mt) * std::ceil((double)N / c.bn);
@@ -814,9 +818,9 @@ Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, bool ragged, 
 
 }  // namespace
 
-Fp8Plan fp8_plan(int groups, double rows_per_group, bool ragged, int N, int K, bool out_f32) {
-    return out_f32 ? cheapest(kF32, groups, rows_per_group, ragged, N, K)
-                   : cheapest(kBf16, groups, rows_per_group, ragged, N, K);
+Fp8Plan fp8_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K, bool out_f32) {
+    return out_f32 ? cheapest(kF32, groups, rows_per_group, max_rows, ragged, N, K)
+                   : cheapest(kBf16, groups, rows_per_group, max_rows, ragged, N, K);
 }
 
 hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_t stream) {

@@ -173,7 +173,7 @@ hipError_t launch_router(const void* logits, int logits_type, int T, int E, int 
 
 // The forward of a few tokens (few.hip): workspace regions and launches
 struct FewLayout {
-    size_t h8, h_sf, rows, segs, n_used, total;
+    size_t h8, h_sf, rows, segs, n_used, h32, total;
 };
 FewLayout few_layout(const moe_shape_t& s);
 hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t* x, const uint8_t* x_sf,
@@ -202,14 +202,14 @@ struct GemmFp8Args {
     void* d;
     int out_f32;
 };
-// The kernel for groups of about rows_per_group rows (ragged: known on the device only), the
-// height of its row tiles, and whether one row tile per group reads B
+// The kernel for groups of about rows_per_group rows (ragged: known on the device only; at most max_rows
+// in all), the height of its row tiles, and whether one row tile per group reads B
 struct Fp8Plan {
     Fp8Kernel kernel;
     int block_m;
     bool stream;
 };
-Fp8Plan fp8_plan(int groups, double rows_per_group, bool ragged, int N, int K, bool out_f32);
+Fp8Plan fp8_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K, bool out_f32);
 hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_t stream);
 
 // Combine (combine.hip)

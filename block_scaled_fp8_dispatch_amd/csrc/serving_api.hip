@@ -7,6 +7,8 @@
 
 namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// 512 threads per 32 columns of the output have to stay below a launch's 2^32
+bool few_shape_ok(const moe_shape_t* s) { return moe::shape_ok(s) && s->hidden < (1 << 27); }
 }  // namespace
 
 using namespace moe;
@@ -34,7 +36,7 @@ int moe_topk_router(int32_t* topk_idx, float* topk_weights, const void* logits, 
 }
 
 size_t moe_few_workspace_bytes(const moe_shape_t* shape) {
-    if (!shape_ok(shape)) return 0;
+    if (!few_shape_ok(shape)) return 0;
     return few_layout(*shape).total;
 }
 
@@ -42,7 +44,7 @@ int moe_forward_few(uint16_t* y_bf16, const uint8_t* x_fp8, const uint8_t* x_sf,
                     const float* topk_weights, int32_t num_tokens, const moe_shape_t* shape, const void* packed,
                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!shape) return MOE_ERR_NULL;
-    if (!shape_ok(shape)) return MOE_ERR_SHAPE;
+    if (!few_shape_ok(shape)) return MOE_ERR_SHAPE;
     if (num_tokens < 0 || num_tokens > shape->max_tokens || num_tokens > MOE_FEW_MAX_TOKENS) return MOE_ERR_TOKENS;
     if (!y_bf16 || !x_fp8 || !x_sf || !topk_idx || !topk_weights || !packed || !workspace) return MOE_ERR_NULL;
     if (!aligned16(y_bf16) || !aligned16(x_fp8) || !aligned16(x_sf) || !aligned16(topk_idx) ||

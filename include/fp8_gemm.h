@@ -15,12 +15,13 @@
  * rounded once to nearest even) or FP32, as d_type (MOE_BF16, MOE_F32 of moe_serving.h) says.
  *
  * Shapes: K a positive multiple of 128, at most 2^22; N any number from 1 to 2^30; G (groups) in
- * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); fewer than 2^31 tiles
- * of 32 x 32 in D (MOE_ERR_SHAPE); B of any size.
+ * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); fewer than 2^24 tiles
+ * of 128 x 256 in D, counting one part tile per group (MOE_ERR_SHAPE); B of any size.
  *
  * Memory, errors and streams as in moe.h: device pointers, 16-byte aligned, owned by the
  * caller; host-detectable problems return a negative MOE_ERR_* status before any launch;
- * every call is asynchronous on `stream`. Calls that share a workspace must not overlap.
+ * every call is asynchronous on `stream`, and the buffers belong to the current device, as
+ * `stream` does. Calls that share a workspace must not overlap.
  * Results are deterministic.
  */
 #ifndef MOE_FP8_GEMM_H

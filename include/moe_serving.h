@@ -9,7 +9,7 @@
  * Formats, memory, errors and streams as in moe.h: device pointers, 16-byte aligned, owned by
  * the caller (the library allocates nothing); host-detectable problems return a negative
  * MOE_ERR_* status before any launch; every call is asynchronous on `stream` and may be
- * captured into a graph.
+ * captured into a graph. The buffers belong to the current device, and `stream` to it too.
  */
 #ifndef MOE_SERVING_H
 #define MOE_SERVING_H
@@ -49,7 +49,7 @@ int moe_topk_router(int32_t* topk_idx, float* topk_weights, const void* logits,
 
 /* Bytes of the workspace moe_forward_few needs for up to min(shape->max_tokens,
  * MOE_FEW_MAX_TOKENS) tokens; a moe_forward workspace of the same shape is always large
- * enough for it. 0 if the shape is unsupported. */
+ * enough for it. 0 if the shape is unsupported (as moe_forward's, and hidden below 2^27). */
 size_t moe_few_workspace_bytes(const moe_shape_t* shape);
 
 /* The forward for a few tokens: moe_forward's arguments, formats and packed weights, with

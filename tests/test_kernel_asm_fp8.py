@@ -87,12 +87,15 @@ def test_the_few_token_loops_spill_nothing(tmp_path):
                     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-S",
                     os.path.join(CSRC, "few.hip"), "-o", out], check=True, capture_output=True)
     asm = [line.strip() for line in open(out)]
-    label = {m.group(1): i for i, x in enumerate(asm) if (m := re.match(r"(\.LBB\d+_\d+):", x))}
-    checked = 0
-    for name, s in label.items():
-        back = [i for i, x in enumerate(asm) if i > s and x.startswith(("s_cbranch", "s_branch")) and x.split()[-1] == name]
-        body = asm[s:max(back) + 1] if back else []
-        if any(x.startswith("v_mfma") for x in body):
-            checked += 1
-            assert not [x for x in body if x.startswith("scratch_")], name
-    assert checked >= 5
+    loops, current = {}, None                    # instructions by the loop that the compiler's notes put their block in
+    for x in asm:
+        if re.match(r"(\.LBB\d+_\d+:|; %bb)", x):
+            current = None
+        if m := re.match(r"\.LBB(\d+_\d+):.*=>This", x) or re.search(r"in Loop: Header=BB(\d+_\d+)", x):
+            current = m.group(1)
+        if current:
+            loops.setdefault(current, []).append(x)
+    products = {k: v for k, v in loops.items() if any(x.startswith("v_mfma") for x in v)}
+    assert len(products) >= 9                    # five few_linear1 (one with two), three few_linear2
+    for name, body in products.items():
+        assert not [x for x in body if x.startswith("scratch_")], name

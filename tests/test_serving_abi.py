@@ -56,6 +56,8 @@ def test_few_sizes_and_refusals():
     assert call(T=-1) == moe.MOE_ERR_TOKENS
     assert call(T=4, shape=moe.make_shape(32, 7168, 2048, 8, 3)) == moe.MOE_ERR_TOKENS
     assert call(shape=moe.make_shape(32, 7000, 2048, 8, 64)) == moe.MOE_ERR_SHAPE
+    wide = moe.make_shape(4, 2 ** 27, 128, 3, 1)       # more columns than one launch covers
+    assert moe.moe_few_workspace_bytes(wide) == 0 and call(T=1, shape=wide, wsb=1 << 40) == moe.MOE_ERR_SHAPE
     assert call(T=0) == moe.MOE_OK
 
 
@@ -72,7 +74,7 @@ def test_fp8_gemm_refusals():
         assert dense(**{name: None}) == moe.MOE_ERR_NULL, name
         assert dense(**{name: A + 4}) == moe.MOE_ERR_ALIGN, name
     for bad in (dict(n=0), dict(n=-5), dict(n=2 ** 30 + 1), dict(k=0), dict(k=64), dict(k=200), dict(k=2 ** 23), dict(ty=2), dict(ty=-1),
-                dict(m=2 ** 23, n=2 ** 30, k=128, wb=1 << 40)):
+                dict(m=2 ** 23, n=2 ** 30, k=128, wb=1 << 40), dict(m=2 ** 15, n=2 ** 24, k=128, wb=1 << 40)):
         assert dense(**bad) == moe.MOE_ERR_SHAPE, bad
     assert dense(m=-1) == moe.MOE_ERR_TOKENS
     assert dense(m=2 ** 24, k=256) == moe.MOE_ERR_TOKENS
