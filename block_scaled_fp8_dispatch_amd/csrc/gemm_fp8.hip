@@ -81,10 +81,10 @@ __device__ inline void store_columns(T* dst, const T (&x)[n], int left) {
     }
 }
 
-// Workgroups go round-robin to the XCDs: tile id of this workgroup with each XCD (workgroup id
+// Workgroups go round-robin to the XCDs: tile id of workgroup `block` with each XCD (workgroup id
 // mod 8) owning a contiguous range of ids. -1: none left.
-__device__ inline int xcd_tile(int total) {
-    const int xcd = blockIdx.x & 7, li = blockIdx.x >> 3;
+__device__ inline int xcd_tile(int total, unsigned block) {
+    const int xcd = block & 7, li = block >> 3;
     const int per = total >> 3, rem = total & 7;
     if (li >= per + (xcd < rem ? 1 : 0)) return -1;
     return xcd * per + (xcd < rem ? xcd : rem) + li;
@@ -108,7 +108,7 @@ constexpr int kAllRecords = -1;
 //
 // With a workgroup's whole reading in flight at once it is bound by latency: 8.8 us (FP32, 128 x 32 x
 // 7168) and 7.9 us (33 x 7168 x 2048, 1.9 TB/s). Operands straight from memory to registers
-// instead were tried (14 and 12 us): a fragment read takes half a line of 16 rows at a time, and the
+// instead were tried and were slower: a fragment read takes half a line of 16 rows at a time, and the
 // chunks in flight do not fit the registers.
 template <int BM, int BN, int WAVES>
 struct SkinnyCfg {
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     int num_mt = dense ? (p.dense_rows + 63) / 64 : __builtin_amdgcn_readfirstlane(p.meta[0]);
     if (num_mt > p.max_tiles) num_mt = p.max_tiles;
     const int NT = (p.N + BN - 1) / BN;
-    const int v = xcd_tile(num_mt * SUB * NT);
+    const int v = xcd_tile(num_mt * SUB * NT, blockIdx.x);
     if (v < 0) return;
     // groups of 4 row tiles across all column tiles: their rows of A stay in the XCD's L2
     const int set = v / (kGroupM * SUB * NT), mt0 = set * kGroupM, gm = min(kGroupM, num_mt - mt0) * SUB;
@@ -336,51 +336,29 @@ struct Fp8Cfg {
     static_assert(BN % (16 * WAVES_N) == 0 && B_BYTES % 4096 == 0, "");
 };
 
+// Part `part` (of BM rows) of tile v. Tile ids walk groups of 4 row tiles (of args.block_m rows)
+// across all column tiles.
 // STREAM: B is read by one row tile only, through non-temporal loads. WIDE: N % 8 == 0, every row
 // and a lane's chunk aligned and a chunk wholly in or out, stored plainly.
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool STREAM, bool WIDE>
-__global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
-    // gfx950 buffer descriptors are a device-only type: the host pass sees an empty kernel
+__device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp8Args& args, uint8_t* smem, int num_mt, int v, int part) {
+    // gfx950 buffer descriptors are a device-only type: the host pass sees an empty function
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = Fp8Cfg<BM, BN, WAVES_M, WAVES_N>;
     constexpr int WM = C::WM, WN = C::WN, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
     constexpr int A_DMA = C::A_DMA, B_DMA = C::B_DMA, NSB = C::NSB;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     uint8_t* const bring = smem + DA * C::A_BYTES;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int g = lane >> 4, l = lane & 15;
-
-    // ---- tile ------------------------------------------------------------------------------
-    // Tile ids walk groups of 4 row tiles (of args.block_m rows) across all column tiles. The last
-    // round of 256 tiles, when it would be at most half full (256 x 256 tiles only), is left to
-    // the second launch (tail), whose workgroups take parts of BM rows of those tiles: 64 rows
-    // where that still is one round, else 128.
     const bool dense = args.dense_rows > 0;
-    const int bm = args.block_m;
-    int num_mt = dense ? (args.dense_rows + bm - 1) / bm : __builtin_amdgcn_readfirstlane(args.meta[0]);
-    if (num_mt > args.max_tiles) num_mt = args.max_tiles;
     const int NT = (args.N + BN - 1) / BN;
-    const int total = num_mt * NT;
-    const int rem = bm == 256 && BN == 256 ? total % kCus : 0;
-    const int main_total = rem <= kCus / 2 ? total - rem : total;
-    int v, part = 0;
-    if (!args.tail) {
-        v = xcd_tile(main_total);
-        if (v < 0) return;
-    } else {
-        if (BM != (rem <= kCus / 4 ? 64 : 128)) return;
-        const int u = xcd_tile((total - main_total) * (256 / BM));
-        if (u < 0) return;
-        v = main_total + u / (256 / BM);
-        part = u % (256 / BM);
-    }
     const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
     const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
     const int mt = mt0 + vin % gm, nt = vin / gm;
     const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
-    const int row0 = (dense ? mt * bm : __builtin_amdgcn_readfirstlane(args.tile_row0[mt])) + part * BM;
+    const int row0 = (dense ? mt * args.block_m : __builtin_amdgcn_readfirstlane(args.tile_row0[mt])) + part * BM;
     const int nks = args.K / kBK;
     // A and D row of tile row r, -1 on padding
     auto d_row = [&](int r) __attribute__((always_inline)) -> int {
@@ -393,7 +371,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
     };
 
     // padding comes last in a row tile: nothing but padding here
-    if (args.tail && __builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
+    if (part > 0 && __builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
 
     // ---- per-lane offsets --------------------------------------------------------------------
     // Load j of wave w fills LDS rows 8*(w*DMA + j) .. +7 of a tile; lane l lands at row + l/8,
@@ -609,6 +587,42 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 #endif
 }
 
+// The row tiles in use: their number lies on the device unless the product is dense
+__device__ inline int row_tiles(const GemmFp8Args& args, int bm) {
+    const int n = args.dense_rows > 0 ? (args.dense_rows + bm - 1) / bm : __builtin_amdgcn_readfirstlane(args.meta[0]);
+    return min(n, args.max_tiles);
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, bool STREAM, bool WIDE>
+__global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
+    using C = Fp8Cfg<BM, BN, WAVES_M, WAVES_N>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
+    const int num_mt = row_tiles(args, BM);
+    const int v = xcd_tile(num_mt * ((args.N + BN - 1) / BN), blockIdx.x);
+    if (v < 0) return;
+    tiled_part<BM, BN, WAVES_M, WAVES_N, STREAM, WIDE>(args, smem, num_mt, v, 0);
+}
+
+// 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where
+// those are no more than the CUs, else of 128 rows, so that more of them work, and each starts when a CU
+// is through with the rounds before (as launches of their own the parts wait for the last of these
+// workgroups: 8192 rows in 8 groups, 4096 x 7168: XXX us).
+template <bool WIDE>
+__global__ __launch_bounds__(256, 1) void gemm_fp8_rounds(GemmFp8Args args) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[160 * 1024];
+    const int num_mt = row_tiles(args, 256), total = num_mt * ((args.N + 255) / 256);
+    const int rem = total % kCus, full = rem <= kCus / 2 ? total - rem : total;
+    if ((int)blockIdx.x < full) {
+        tiled_part<256, 256, 2, 2, false, WIDE>(args, smem, num_mt, xcd_tile(full, blockIdx.x), 0);
+        return;
+    }
+    const int parts = rem <= kCus / 4 ? 4 : 2;
+    const int u = xcd_tile((total - full) * parts, blockIdx.x - full);
+    if (u < 0) return;
+    if (parts == 4) tiled_part<64, 256, 1, 4, false, WIDE>(args, smem, num_mt, full + u / 4, u % 4);
+    else tiled_part<128, 256, 2, 2, false, WIDE>(args, smem, num_mt, full + u / 2, u % 2);
+}
+
 // FP32 outputs with enough tiles: 128 x 256 of D per workgroup, 2 x 2 waves of 64 x 128, LDS rings of
 // three steps. Each step converts its operands to bf16 (exact) and feeds
 // v_mfma_f32_16x16x32_bf16. One barrier per step: behind it the loads of two steps ahead go into
@@ -630,7 +644,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
     int num_mt = dense ? (args.dense_rows + BM - 1) / BM : __builtin_amdgcn_readfirstlane(args.meta[0]);
     if (num_mt > args.max_tiles) num_mt = args.max_tiles;
     const int NT = (args.N + kBN - 1) / kBN;
-    const int v = xcd_tile(num_mt * NT);
+    const int v = xcd_tile(num_mt * NT, blockIdx.x);
     if (v < 0) return;
     const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
     const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
@@ -829,14 +843,10 @@ hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_
     const size_t grid = mt * (size_t)cdiv(a.N, kBN);
     switch (plan.kernel) {
         case Fp8Kernel::kTiled256: {
-            launch_tiled<256, 2, 2, false>((unsigned)grid, a, stream);
-            GemmFp8Args t = a;
-            t.tail = 1;
-            // the leftover tiles' number is known on the host for a dense product only
-            const size_t rem = grid % kCus;
-            const bool dense = a.dense_rows > 0;
-            if (!dense || (rem > 0 && rem <= kCus / 4)) launch_tiled<64, 1, 4, false>(kCus, t, stream);
-            if (!dense || (rem > kCus / 4 && rem <= kCus / 2)) launch_tiled<128, 2, 2, false>(kCus, t, stream);
+            // the parts are at most 256
+            const unsigned blocks = (unsigned)(a.dense_rows > 0 ? (grid % kCus == 0 || grid % kCus > kCus / 2 ? grid : grid - grid % kCus + kCus) : grid + kCus);
+            if (a.N % 8 == 0) gemm_fp8_rounds<true><<<blocks, 256, 0, stream>>>(a);
+            else gemm_fp8_rounds<false><<<blocks, 256, 0, stream>>>(a);
             break;
         }
         case Fp8Kernel::kTiled256x224:

@@ -198,7 +198,6 @@ struct GemmFp8Args {
     const int32_t* tile_expert;
     const int32_t* tile_row0;
     int max_tiles;
-    int tail;                  // the tiled kernels' second launch: the last tiles, in parts
     void* d;
     int out_f32;
 };

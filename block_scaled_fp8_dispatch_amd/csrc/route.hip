@@ -469,8 +469,8 @@ __global__ __launch_bounds__(1024) void gemm_layout_kernel(int G, int max_m,
 
 // Rows of the FP8 x FP8 contiguous GEMM grouped by their id in one launch: as the routing above,
 // but a row's place within its group does not matter (each row of D depends on its own row of A
-// only), so places are handed out by LDS atomics, one per wave where all its rows are of one
-// group. Full tiles first, then each group's last, partly filled one.
+// only), so places are handed out by LDS atomics, one per wave and group. Full tiles first, then
+// each group's last, partly filled one.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupPer = kGroupMaxRows / kGroupThreads;
 
@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_rows_kernel(const int32_t
                                                                    int32_t* __restrict__ meta,
                                                                    int32_t* __restrict__ tile_expert,
                                                                    int32_t* __restrict__ tile_row0) {
-    __shared__ int next[kMaxE];                          // rows of a group, then its next free place
+    __shared__ int next[kMaxE];                          // rows of a group so far
     __shared__ int row_of[kMaxE], foff[kMaxE + 1], pad_lo[kMaxE], pad_hi[kMaxE];
     __shared__ int warp_sums[16];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -492,38 +492,44 @@ __global__ __launch_bounds__(kGroupThreads) void group_rows_kernel(const int32_t
     }
     if (tid < G) next[tid] = 0;
     __syncthreads();
-    // takes one place of group e per lane that has one (e >= 0): the lane's place counted from next[e]
-    auto take = [&](int e) __attribute__((always_inline)) -> int {
-        const uint64_t have = __ballot(e >= 0);
-        if (have == 0) return 0;
-        const int e0 = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)have) - 1);
-        if (__ballot(e == e0) == have) {
-            int base = 0;
-            if (lane == 0) base = atomicAdd(&next[e0], __popcll(have));
-            return __builtin_amdgcn_readfirstlane(base) + __popcll(have & ((1ull << lane) - 1));
-        }
-        return e >= 0 ? atomicAdd(&next[e], 1) : 0;
-    };
+    // each row's place in its group: the lanes of a wave with the same group meet by ballots of its bits,
+    // and one lane adds for them (an atomic of each lane's own: 9.7 us against 8.4 for 8192 rows of 8 groups)
+    const int nbits = G > 1 ? 32 - __clz(G - 1) : 0;
+    int place[kGroupPer], from[kGroupPer];               // the first lane's sum, and which lane that is
+    const uint64_t below = (1ull << lane) - 1;
+    int rank[kGroupPer];
 #pragma unroll
     for (int i = 0; i < kGroupPer; ++i) {
-        if (i * kGroupThreads >= m) break;               // uniform
-        take(ev[i]);
+        if (i * kGroupThreads >= m) continue;            // uniform
+        uint64_t peers = __ballot(ev[i] >= 0);
+        for (int b = 0; b < nbits; ++b) {
+            const bool one = (ev[i] >> b) & 1;
+            const uint64_t ones = __ballot(one);
+            peers &= one ? ones : ~ones;
+        }
+        rank[i] = __popcll(peers & below);
+        from[i] = peers != 0 ? __ffsll((unsigned long long)peers) - 1 : lane;
+        place[i] = 0;
+        if (ev[i] >= 0 && lane == from[i]) place[i] = atomicAdd(&next[ev[i]], __popcll(peers));
+    }
+    // (the sums come back once all are under way)
+#pragma unroll
+    for (int i = 0; i < kGroupPer; ++i) {
+        if (i * kGroupThreads >= m) continue;
+        place[i] = __shfl(place[i], from[i], 64) + rank[i];
     }
     __syncthreads();
     const int c = tid < G ? next[tid] : 0;
     const int full = c / block_m, part = c % block_m != 0;
-    int n_full = 0, n_part = 0, n_rows = 0;
-    const int f0 = block_exclusive_scan_1024(full, warp_sums, &n_full);
-    __syncthreads();
-    const int p0 = block_exclusive_scan_1024(part, warp_sums, &n_part);
-    __syncthreads();
-    const int r0 = block_exclusive_scan_1024((full + part) * block_m, warp_sums, &n_rows);
+    int sums = 0;                                        // full tiles (at most 256 in all) and part tiles
+    const int before = block_exclusive_scan_1024(full << 16 | part, warp_sums, &sums);
+    const int f0 = before >> 16, p0 = before & 0xffff, n_full = sums >> 16, n_part = sums & 0xffff;
+    const int r0 = (f0 + p0) * block_m;
     if (tid < G) {
         foff[tid] = f0;
         pad_lo[tid] = r0 + c;
         pad_hi[tid] = r0 + (full + part) * block_m;
         row_of[tid] = r0;
-        next[tid] = r0;
     }
     if (tid == 0) {
         foff[G] = n_full;
@@ -549,9 +555,8 @@ __global__ __launch_bounds__(kGroupThreads) void group_rows_kernel(const int32_t
     }
 #pragma unroll
     for (int i = 0; i < kGroupPer; ++i) {
-        if (i * kGroupThreads >= m) break;               // uniform
-        const int place = take(ev[i]);
-        if (ev[i] >= 0) perm[place] = i * kGroupThreads + tid;
+        if (i * kGroupThreads >= m) continue;            // uniform
+        if (ev[i] >= 0) perm[row_of[ev[i]] + place[i]] = i * kGroupThreads + tid;
     }
 }
 

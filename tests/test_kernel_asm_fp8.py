@@ -14,14 +14,14 @@ pytestmark = pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not ava
 
 @pytest.fixture(scope="module")
 def kernels(tmp_path_factory):
-    """{name: lines} of every gemm_fp8_tiled instantiation."""
+    """{name: lines} of every instantiation of the tiled kernels."""
     out = str(tmp_path_factory.mktemp("asm") / "gemm_fp8.s")
     subprocess.run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
                     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-S",
                     os.path.join(CSRC, "gemm_fp8.hip"), "-o", out], check=True, capture_output=True)
     text = open(out).read()
     found = {m.group(1): [line.strip() for line in m.group(0).splitlines()]
-             for m in re.finditer(r"^(_ZN3moe\S*gemm_fp8_tiledI\S+):.*?^\.Lfunc_end", text, re.S | re.M)}
+             for m in re.finditer(r"^(_ZN3moe\S*gemm_fp8_(?:tiled|rounds)I\S+):.*?^\.Lfunc_end", text, re.S | re.M)}
     assert len(found) == 9
     return found
 
