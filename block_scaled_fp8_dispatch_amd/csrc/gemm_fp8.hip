@@ -101,47 +101,52 @@ constexpr int kAllRecords = -1;
 
 // Skinny kernel: few rows, or too few tiles for the tiled kernel. A workgroup owns a BM x BN tile
 // of D and its WAVES waves share K, wave w taking steps w, w + WAVES, ... and keeping sums of its
-// own. Each wave fills two LDS slots of its own (rows of A and B as the tiled kernel lays them
-// out), so there is no barrier before the end: it waits for the older slot, reads and multiplies
-// it, and refills it two of its steps ahead. The waves' sums meet in LDS, the upper half of the
-// waves onto the lower, then those in wave order.
+// own. Each wave fills LDS slots of its own (rows of A and B as the tiled kernel lays them
+// out), so there is no barrier before the end: it waits for its oldest slot, reads and multiplies
+// it, and refills it. The waves' sums meet in LDS, the upper half of the waves onto the lower, then
+// those in wave order.
 //
-// With a workgroup's whole reading in flight at once it is bound by latency: 8.8 us (FP32, 128 x 32 x
-// 7168) and 7.9 us (33 x 7168 x 2048, 1.9 TB/s). Operands straight from memory to registers
-// instead were tried and were slower: a fragment read takes half a line of 16 rows at a time, and the
-// chunks in flight do not fit the registers.
-template <int BM, int BN, int WAVES>
+// Bound by latency where tiles are few (128 x 32 x 7168, FP32: 5.7 us in 16 tiles of 16 x 16 with two slots
+// a wave; 32 x 32: 9.0), by weights in flight where they are many (4 x 7168 x 7168: 11.2 us, 4.6 TB/s,
+// in tiles of 16 x 32). Two workgroups or more on a CU with one slot a wave beat one with two (33 x 7168 x
+// 2048, 32 x 32: 7.5 us against 9.3). Operands straight from memory to registers instead were tried
+// and were slower: a fragment read takes half a line of 16 rows at a time, and the chunks in flight
+// do not fit the registers.
+constexpr int kSkinnyWaves = 8;
+
+template <int BM, int BN, int WAVES, int SLOTS>
 struct SkinnyCfg {
     static constexpr int FM = BM / 16, FN = BN / 16;
     static constexpr int SLOT = (BM + BN) * kBK;
     static constexpr int A_DMA = BM / 8, B_DMA = BN / 8, NS = FM + 1;
     static constexpr int PITCH = BN + 4;           // floats per row of a wave's sums
-    static constexpr int LDS_BYTES = 2 * WAVES * SLOT;
+    static constexpr int LDS_BYTES = SLOTS * WAVES * SLOT;
     static_assert(LDS_BYTES <= 160 * 1024 && BN <= 128, "");
     static_assert(WAVES / 2 * BM * PITCH * 4 <= LDS_BYTES, "the sums reuse the slots");
 };
 
-template <int BM, int BN, int WAVES, bool F32>
+template <int BM, int BN, int WAVES, int SLOTS, bool F32>
 __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    using C = SkinnyCfg<BM, BN, WAVES>;
+    using C = SkinnyCfg<BM, BN, WAVES, SLOTS>;
     constexpr int FM = C::FM, FN = C::FN, SUB = 64 / BM, PITCH = C::PITCH;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l = lane & 15;
     const bool dense = p.dense_rows > 0;
-    int num_mt = dense ? (p.dense_rows + 63) / 64 : __builtin_amdgcn_readfirstlane(p.meta[0]);
-    if (num_mt > p.max_tiles) num_mt = p.max_tiles;
+    // units of BM rows: of a dense product's rows, or of the 64-row tiles in the list
+    const int units = dense ? (p.dense_rows + BM - 1) / BM : min(__builtin_amdgcn_readfirstlane(p.meta[0]), p.max_tiles) * SUB;
     const int NT = (p.N + BN - 1) / BN;
-    const int v = xcd_tile(num_mt * SUB * NT, blockIdx.x);
+    const int v = xcd_tile(units * NT, blockIdx.x);
     if (v < 0) return;
     // groups of 4 row tiles across all column tiles: their rows of A stay in the XCD's L2
-    const int set = v / (kGroupM * SUB * NT), mt0 = set * kGroupM, gm = min(kGroupM, num_mt - mt0) * SUB;
-    const int vin = v - set * kGroupM * SUB * NT;
-    const int mt = mt0 + vin % gm / SUB, sub = vin % gm % SUB, nt = vin / gm;
+    constexpr int kSet = kGroupM * SUB;
+    const int set = v / (kSet * NT), u0 = set * kSet, gu = min(kSet, units - u0), vin = v - set * kSet * NT;
+    const int unit = u0 + vin % gu, nt = vin / gu;
+    const int mt = unit / SUB;
     const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(p.tile_expert[mt]);
-    const int row0 = (dense ? mt * 64 : __builtin_amdgcn_readfirstlane(p.tile_row0[mt])) + sub * BM;
+    const int row0 = dense ? unit * BM : __builtin_amdgcn_readfirstlane(p.tile_row0[mt]) + unit % SUB * BM;
     auto d_row = [&](int r) __attribute__((always_inline)) -> int {
         if (dense) return row0 + r < p.dense_rows ? row0 + r : -1;
         return p.perm[row0 + r];
@@ -153,7 +158,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     // padding comes last in a row tile: nothing but padding here
     if (__builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
 
-    uint8_t* const mine = smem + wave * 2 * C::SLOT;
+    uint8_t* const mine = smem + wave * SLOTS * C::SLOT;
     const int chunk = (lane & 7) ^ (lane >> 3);
     uint32_t a_off[C::A_DMA], b_off[C::B_DMA], sa_off[FM];
 #pragma unroll
@@ -170,7 +175,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(p.b_sf + ((size_t)group * ((p.N + 127) / 128) + nt * BN / 128) * p.sf_stride), 0, kAllRecords, kRsrcWord3);
 
-    uint32_t sa[2][FM], sb[2];
+    uint32_t sa[SLOTS][FM], sb[SLOTS];
     auto issue = [&](int ks, auto slot_c) __attribute__((always_inline)) {
         constexpr int S = decltype(slot_c)::value;
         uint8_t* dst = mine + S * C::SLOT;
@@ -197,19 +202,19 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
 #pragma unroll
         for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
     const int nks = p.K / kBK;
-    // step ks of this wave, in slot S: wait until only the younger slot's loads (if any) are in
+    // step ks of this wave, in slot S: wait until only the younger slots' loads (if any) are in
     // flight, multiply, refill
+    constexpr int W = C::NS + C::A_DMA + C::B_DMA;
+    auto wait = [&](auto younger_c) __attribute__((always_inline)) {
+        constexpr int V = decltype(younger_c)::value * W;
+        static_assert(V < 64, "vmcnt range");
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (V & 15) | (((V >> 4) & 3) << 14));
+        asm volatile("s_waitcnt vmcnt(%0)" :: "n"(V) : "memory");
+    };
     auto step = [&](int ks, auto slot_c) __attribute__((always_inline)) {
         constexpr int S = decltype(slot_c)::value;
-        constexpr int W = C::NS + C::A_DMA + C::B_DMA;
-        static_assert(W < 64, "vmcnt range");
-        if (ks + WAVES < nks) {
-            __builtin_amdgcn_s_waitcnt(0x0F70 | (W & 15) | (((W >> 4) & 3) << 14));
-            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(W) : "memory");
-        } else {
-            __builtin_amdgcn_s_waitcnt(0x0F70);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
+        if (SLOTS > 1 && ks + WAVES < nks) wait(IntC<SLOTS - 1>{});
+        else wait(IntC<0>{});
         const uint8_t* src = mine + S * C::SLOT;
         if constexpr (F32) {
             v8bf bv[FN][4];
@@ -244,17 +249,18 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
                                                                                  (int)sb[S]);
             }
         }
-        if (ks + 2 * WAVES < nks) {
+        if (ks + SLOTS * WAVES < nks) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the slot's reads are done
-            issue(ks + 2 * WAVES, slot_c);
+            issue(ks + SLOTS * WAVES, slot_c);
         }
     };
-    if (wave < nks) issue(wave, IntC<0>{});
-    if (wave + WAVES < nks) issue(wave + WAVES, IntC<1>{});
-    for (int ks = wave; ks < nks; ks += 2 * WAVES) {
-        step(ks, IntC<0>{});
-        if (ks + WAVES < nks) step(ks + WAVES, IntC<1>{});
-    }
+    static_assert(SLOTS <= 2, "");
+    auto each_slot = [&](int ks, auto&& f) __attribute__((always_inline)) {
+        if (ks < nks) f(ks, IntC<0>{});
+        if (SLOTS > 1 && ks + WAVES < nks) f(ks + WAVES, IntC<SLOTS - 1>{});
+    };
+    each_slot(wave, issue);
+    for (int ks = wave; ks < nks; ks += SLOTS * WAVES) each_slot(ks, step);
     __syncthreads();                               // the sums reuse the slots of all waves
     float* const sums = reinterpret_cast<float*>(smem);
     auto at = [&](int w, int r, int n) __attribute__((always_inline)) -> float& { return sums[(w * BM + r) * PITCH + n]; };
@@ -767,11 +773,12 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
 #endif
 }
 
-template <int BM, int BN, int WAVES>
-void launch_skinny(size_t tiles64, const GemmFp8Args& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)(tiles64 * (64 / BM) * (size_t)cdiv(a.N, BN));
-    if (a.out_f32) gemm_fp8_skinny<BM, BN, WAVES, true><<<grid, WAVES * 64, 0, stream>>>(a);
-    else gemm_fp8_skinny<BM, BN, WAVES, false><<<grid, WAVES * 64, 0, stream>>>(a);
+template <int BM, int BN, int SLOTS>
+void launch_skinny(const GemmFp8Args& a, hipStream_t stream) {
+    const size_t units = a.dense_rows > 0 ? cdiv(a.dense_rows, BM) : (size_t)a.max_tiles * (64 / BM);
+    const unsigned grid = (unsigned)(units * (size_t)cdiv(a.N, BN));
+    if (a.out_f32) gemm_fp8_skinny<BM, BN, kSkinnyWaves, SLOTS, true><<<grid, kSkinnyWaves * 64, 0, stream>>>(a);
+    else gemm_fp8_skinny<BM, BN, kSkinnyWaves, SLOTS, false><<<grid, kSkinnyWaves * 64, 0, stream>>>(a);
 }
 
 template <int BM, int WAVES_M, int WAVES_N, bool STREAM>
@@ -780,26 +787,33 @@ void launch_tiled(unsigned grid, const GemmFp8Args& a, hipStream_t stream) {
     else gemm_fp8_tiled<BM, kBN, WAVES_M, WAVES_N, STREAM, false><<<grid, 256, 0, stream>>>(a);
 }
 
-// Microseconds of a round of 256 workgroups of each kernel, as fixed + per-step (128 K) parts,
-// fitted to 16 products from 256 x 256 x 2048 to 4096 x 4096 x 7168 timed with every kernel (each
-// prediction within 15 % of its measurement; for instance 1000 x 1000 x 7168, bf16: 78, 43, 33, 22
-// and 33 us; 4096 x 4096 x 7168: 96, 107, 151, 272 and 467 us; 64 x 7168 x 7168: 71, 42, 33, 19 and
-// 18 us).
+// Microseconds of a product with each kernel. Tiled: rounds of 256 workgroups, each fixed + step per
+// 128 K, fitted to 16 products from 256 x 256 x 2048 to 4096 x 4096 x 7168 (for instance 4096 x 4096 x
+// 7168 by 256 and 128 rows: 96 and 151 us). Skinny: fixed + wave per step that a wave takes + for
+// every 256 workgroups tile + step per 128 K, fitted to 35 products (FP32: 23) from 1 x 256 x 512 to
+// 2 x 20000 x 7168, 2048 x 2048 x 18432 and 4096 x 4096 x 2048, each timed with every kernel, weights
+// from memory: what the model picks is 1 % slower than the best of the kernels on average, 10 % at most.
+// Tiles of 16 rows are for dense products: of a list's 64-row tiles with few rows 3 in 4 workgroups
+// would have none, and the others would share a quarter of the CUs.
 struct Cost {
     Fp8Kernel kernel;
     int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
     int threads;
-    double fixed, step;
+    double fixed, step, wave, tile;
 };
-constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 256, 6.0, 1.45},
-                          {Fp8Kernel::kTiled128, 128, 128, 256, 256, 4.0, 0.83},
-                          {Fp8Kernel::kTiled64, 64, 64, 256, 256, 4.9, 0.57},
-                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 256, 10.0, 1.31},
-                          {Fp8Kernel::kSkinny64, 64, 64, 64, 256, 4.0, 0.2275},
-                          {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 1.6, 0.10}};
-constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 256, 8.0, 1.92},
-                         {Fp8Kernel::kSkinny64, 64, 64, 64, 256, 4.2, 0.335},
-                         {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 2.0, 0.109}};
+constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 256, 6.0, 1.45, 0, 0},
+                          {Fp8Kernel::kTiled128, 128, 128, 256, 256, 4.0, 0.83, 0, 0},
+                          {Fp8Kernel::kTiled64, 64, 64, 256, 256, 4.9, 0.70, 0, 0},
+                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 256, 10.0, 1.31, 0, 0},
+                          {Fp8Kernel::kSkinny64, 64, 64, 64, 512, 2.26, 0.185, 2.05, 2.89},
+                          {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 1.89, 0.093, 0.95, 0.75},
+                          {Fp8Kernel::kSkinny16x32, 64, 16, 32, 512, 2.12, 0.064, 0.68, 0.40},
+                          {Fp8Kernel::kSkinny16, 64, 16, 16, 512, 2.05, 0.043, 0.42, 0.65}};
+constexpr Cost kF32[] = {{Fp8Kernel::kTiled128, 128, 128, 256, 256, 8.0, 1.92, 0, 0},
+                         {Fp8Kernel::kSkinny64, 64, 64, 64, 512, 2.78, 0.223, 1.81, 3.47},
+                         {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 2.07, 0.090, 0.89, 1.01},
+                         {Fp8Kernel::kSkinny16x32, 64, 16, 32, 512, 2.02, 0.056, 0.76, 0.52},
+                         {Fp8Kernel::kSkinny16, 64, 16, 16, 512, 2.01, 0.040, 0.51, 0.74}};
 
 template <size_t NK>
 Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, int max_rows, bool ragged, int N, int K) {
@@ -810,18 +824,24 @@ Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, int max_rows,
         // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
         const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cdiv(N, c.bn);
         if (c.kernel != Fp8Kernel::kTiled128 && grid * c.threads >= (1ull << 32)) continue;
+        if (ragged && c.bm < 32) continue;
         // groups of unknown length end in a tile that is half full on average
         const double mt = groups * (ragged ? rows / c.bm + 0.5 : std::ceil(rows / c.bm));
         const double tiles = std::ceil(mt) * std::ceil((double)N / c.bn);
-        double rounds = std::floor(tiles / kCus), t = 0;
-        const double rem = tiles - rounds * kCus;
-        if (rem > 0) {
-            // the second launch of the 256-row tiles: kBf16[2] and kBf16[1]
-            if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 4) t = kBf16[2].fixed + kBf16[2].step * steps;
-            else if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 2) t = kBf16[1].fixed + kBf16[1].step * steps;
-            else rounds += 1;
+        double t = 0;
+        if (c.wave > 0) {
+            t = c.fixed + c.wave * cdiv(steps, kSkinnyWaves) + tiles / kCus * (c.tile + c.step * steps);
+        } else {
+            double rounds = std::floor(tiles / kCus);
+            const double rem = tiles - rounds * kCus;
+            if (rem > 0) {
+                // the parts of the 256-row tiles' last round: kBf16[2] and kBf16[1]
+                if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 4) t = kBf16[2].fixed + kBf16[2].step * steps;
+                else if (c.kernel == Fp8Kernel::kTiled256 && rem <= kCus / 2) t = kBf16[1].fixed + kBf16[1].step * steps;
+                else rounds += 1;
+            }
+            t += rounds * (c.fixed + c.step * steps);
         }
-        t += rounds * (c.fixed + c.step * steps);
         if (best.block_m == 0 || t < least) {
             best = Fp8Plan{c.kernel, c.block_m, rows <= c.block_m};
             least = t;
@@ -860,8 +880,10 @@ hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_
             if (plan.stream) launch_tiled<64, 1, 4, true>((unsigned)grid, a, stream);
             else launch_tiled<64, 1, 4, false>((unsigned)grid, a, stream);
             break;
-        case Fp8Kernel::kSkinny64: launch_skinny<64, 64, 4>(mt, a, stream); break;
-        case Fp8Kernel::kSkinny32: launch_skinny<32, 32, 8>(mt, a, stream); break;
+        case Fp8Kernel::kSkinny64: launch_skinny<64, 64, 1>(a, stream); break;
+        case Fp8Kernel::kSkinny32: launch_skinny<32, 32, 1>(a, stream); break;
+        case Fp8Kernel::kSkinny16x32: launch_skinny<16, 32, 1>(a, stream); break;
+        case Fp8Kernel::kSkinny16: launch_skinny<16, 16, 2>(a, stream); break;
     }
     return hipGetLastError();
 }

@@ -181,7 +181,7 @@ hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t
                       hipStream_t stream);
 
 // FP8 x FP8 GEMM with 128-block scales (gemm_fp8.hip)
-enum class Fp8Kernel { kTiled256, kTiled256x224, kTiled128, kTiled64, kSkinny64, kSkinny32 };
+enum class Fp8Kernel { kTiled256, kTiled256x224, kTiled128, kTiled64, kSkinny64, kSkinny32, kSkinny16x32, kSkinny16 };
 struct GemmFp8Args {
     const uint8_t* a;          // e4m3 rows of K bytes
     const uint8_t* a_sf;       // rows of sf_stride UE8M0 bytes

@@ -149,3 +149,15 @@ def test_captured_groups_and_counts_change(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(d, want[i][0]) and torch.equal(d2, want[i][1]), i
+
+
+@pytest.mark.parametrize("ty", [moe.MOE_BF16, moe.MOE_F32])
+@pytest.mark.parametrize("M,N,K", [(1000, 2000, 2048), (513, 1031, 2176), (65, 4099, 1024), (300, 640, 1152), (17, 5000, 1280),
+                                   (97, 2311, 384), (33, 7168, 2048), (15, 31, 7168)])
+def test_few_or_small_tiles(M, N, K, ty):
+    """Products between the smallest and a round of large tiles, ragged both ways, whole K shares and not."""
+    print(f"[limits] dense {M} {N} {K} {ty}", flush=True)
+    p = Problem(M, N, K, 1, ty, seed=M)
+    d = p.dense()
+    p.check(d, np.unique(np.r_[0:min(M, 40), M // 2, M - 1 - np.arange(min(M, 20))]))
+    assert np.array_equal(p.dense(), d)
