@@ -17,7 +17,7 @@
 // router_wave_kernel (k > 16): one wave per token, lane l holding experts l, 64 + l, ...: k rounds
 // of the wave's largest key and the lowest expert that holds it.
 //
-// 32768 x 256 FP32 logits, top-8: 12.6 us (2.7 TB/s of logits; a copy of the kernel that only loads them
+// 32768 x 256 FP32 logits, top-8: 12.0 us (2.8 TB/s of logits; a copy of the kernel that only loads them
 // takes 7.2), bound by the vector instructions of the key sorts and of the rounds. 128 x 256: 5.2 us,
 // a launch and one chain of dependent rounds. One wave per token takes 22 us for the first.
 #include "moe_internal.h"
@@ -186,8 +186,9 @@ __device__ inline float lanes_sum(float v) {
     return v;
 }
 
-// 64/L tokens per wave, V experts per lane (E <= L * V), k <= 16.
-template <int L, int V, bool BF16>
+// 64/L tokens per wave, V experts per lane (E <= L * V), k <= 16. Q: experts of a lane that are
+// adjacent and loaded at once (4: FP32 logits, E % 4 == 0)
+template <int L, int V, bool BF16, int Q>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __restrict__ logits, int T, int E, int k,
                                                                 int over_all, float scale,
                                                                 int32_t* __restrict__ topk_idx,
@@ -206,7 +207,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     // offset register serves them all. What lies past a row's end is never looked at; past the
     // last row the loads return 0.
     constexpr int kBytes = BF16 ? 2 : 4;
-    const uint32_t offset = (uint32_t)(lane / L * E + l) * kBytes;
+    const uint32_t offset = (uint32_t)(lane / L * E + l * Q) * kBytes;
+    // expert i of a lane, less the lane's own part
+    auto base = [](int i) __attribute__((always_inline)) -> int { return i / Q * (Q * L) + i % Q; };
     float ahead[V];
     auto load = [&](uint32_t t0) __attribute__((always_inline)) {
         const size_t rest = (size_t)(tokens - t0) * E * kBytes;
@@ -214,8 +217,13 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
             (void*)(static_cast<const uint8_t*>(logits) + (size_t)t0 * E * kBytes), 0,
             (int)(uint32_t)(rest < 0xffffffffu ? rest : 0xffffffffu), 0x00020000);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if constexpr (BF16)
+        for (int i = 0; i < V; i += Q) {
+            if constexpr (Q == 4) {
+                typedef float v4f __attribute__((ext_vector_type(4)));
+                const v4f x = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, offset + i * L * kBytes, 0, 0));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ahead[i + q] = x[q];
+            } else if constexpr (BF16)
                 ahead[i] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, offset + i * L * kBytes, 0, 0) << 16);
             else
                 ahead[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, offset + i * L * kBytes, 0, 0));
@@ -231,13 +239,13 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
     for (int i = 0; i < V; ++i) x[i] = ahead[i];
     if (t0 + stride < tokens) load(t0 + stride);
     // whether x[i] may be chosen (false for a NaN)
-    auto valid = [&](int i) __attribute__((always_inline)) -> bool { return x[i] > -INFINITY && l < E - i * L; };
+    auto valid = [&](int i) __attribute__((always_inline)) -> bool { return x[i] > -INFINITY && l * Q < E - i / Q * (Q * L); };
     int h[LISTS][D];
     uint32_t low = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         low |= __float_as_uint(x[i]);
-        h[i / D][i % D] = valid(i) ? (int)(((uint32_t)signed_key(x[i]) & ~IDX) | (IDX - (uint32_t)(i * L + l))) : kNone;
+        h[i / D][i % D] = valid(i) ? (int)(((uint32_t)signed_key(x[i]) & ~IDX) | (IDX - (uint32_t)(base(i) + l * Q))) : kNone;
     }
     // every list in descending order
     auto order = [&](int& a, int& b) __attribute__((always_inline)) {
@@ -291,10 +299,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
                 m = lanes_max<L>(m);
                 int lowest = 0x7fffffff;           // expert among those that hold m
 #pragma unroll
-                for (int i = 0; i < V; ++i) lowest = min(lowest, key[i] == m ? i * L + l : 0x7fffffff);
+                for (int i = 0; i < V; ++i) lowest = min(lowest, key[i] == m ? base(i) + l * Q : 0x7fffffff);
                 lowest = -lanes_max<L>(-lowest);
 #pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = i * L + l == lowest ? kNone : key[i];
+                for (int i = 0; i < V; ++i) key[i] = base(i) + l * Q == lowest ? kNone : key[i];
                 if (l == j && m != kNone) idx = lowest;
             }
         }
@@ -329,12 +337,15 @@ void launch(const void* logits, int T, int E, int k, int over_all, float scale, 
         kernel<<<passes && g > kRouterGroups ? kRouterGroups : g, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
     };
     if (k <= 16) {
-        if (E <= 32) run(router_kernel<16, 2, BF16>, 4);
-        else if (E <= 64) run(router_kernel<16, 4, BF16>, 4);
-        else if (E <= 128) run(router_kernel<16, 8, BF16>, 4);
-        else if (E <= 256) run(router_kernel<16, 16, BF16>, 4);
-        else if (E <= 512) run(router_kernel<32, 16, BF16>, 2);
-        else run(router_kernel<64, 16, BF16>, 1);
+        // 32768 x 256 FP32, top-8: 13.8 us with single loads, 12.9 with fours (in a graph)
+        constexpr int Q = BF16 ? 1 : 4;
+        const bool quads = !BF16 && E % 4 == 0;
+        if (E <= 32) run(router_kernel<16, 2, BF16, 1>, 4);
+        else if (E <= 64) quads ? run(router_kernel<16, 4, BF16, Q>, 4) : run(router_kernel<16, 4, BF16, 1>, 4);
+        else if (E <= 128) quads ? run(router_kernel<16, 8, BF16, Q>, 4) : run(router_kernel<16, 8, BF16, 1>, 4);
+        else if (E <= 256) quads ? run(router_kernel<16, 16, BF16, Q>, 4) : run(router_kernel<16, 16, BF16, 1>, 4);
+        else if (E <= 512) quads ? run(router_kernel<32, 16, BF16, Q>, 2) : run(router_kernel<32, 16, BF16, 1>, 2);
+        else quads ? run(router_kernel<64, 16, BF16, Q>, 1) : run(router_kernel<64, 16, BF16, 1>, 1);
     } else {
         if (E <= 64) run(router_wave_kernel<1, BF16>, 1, false);
         else if (E <= 128) run(router_wave_kernel<2, BF16>, 1, false);

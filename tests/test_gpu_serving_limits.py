@@ -161,3 +161,39 @@ def test_few_or_small_tiles(M, N, K, ty):
     d = p.dense()
     p.check(d, np.unique(np.r_[0:min(M, 40), M // 2, M - 1 - np.arange(min(M, 20))]))
     assert np.array_equal(p.dense(), d)
+
+
+@pytest.mark.parametrize("E", [33, 36, 63, 64, 100, 127, 128, 201, 252, 256, 257, 384, 510, 512, 644, 1023, 1024])
+def test_router_rows_end_anywhere(E):
+    """Expert counts around the kernels' borders, multiples of 4 (loaded in fours) and not; the row behind
+    the last token would win every choice."""
+    T, k = 300, 8
+    x = torch.full((T + 1, E), 1e30, device="cuda")
+    x[:T] = torch.randn(T, E, device="cuda")
+    idx = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), -7.0, device="cuda")
+    moe.moe_topk_router(idx, w, x, moe.MOE_F32, T, E, k, moe.MOE_ROUTER_SOFTMAX_ALL)
+    torch.cuda.synchronize()
+    ref_idx, ref_w = oracle.topk_router(x[:T].double().cpu().numpy(), k, True)
+    assert np.array_equal(idx[:T].cpu().numpy(), ref_idx)
+    # |x| < 6: distances below 12; the rounding of test_gpu_router.py at D = 12
+    tol = (2 * (12 + 4) + E + 2) * 2.0 ** -24
+    assert (np.abs(w[:T].double().cpu().numpy() - ref_w) <= tol * ref_w + 2.0 ** -126).all()
+    assert (idx[T] == -7).all() and (w[T] == -7.0).all()
+
+
+@pytest.mark.parametrize("E", [30, 64, 250, 256])
+def test_router_passes(E):
+    """More tokens than one pass of the grid takes: as calls on parts that one pass takes."""
+    T, k, part = 100003, 8, 20000
+    x = torch.randn(T, E, device="cuda")
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -7.0, device="cuda")
+    moe.moe_topk_router(idx, w, x, moe.MOE_F32, T, E, k, moe.MOE_ROUTER_SOFTMAX_CHOSEN)
+    for a in range(0, T, part):
+        xs = x[a:a + part].clone()
+        n = xs.shape[0]
+        i2, w2 = torch.empty(n, k, dtype=torch.int32, device="cuda"), torch.empty(n, k, device="cuda")
+        moe.moe_topk_router(i2, w2, xs, moe.MOE_F32, n, E, k, moe.MOE_ROUTER_SOFTMAX_CHOSEN)
+        torch.cuda.synchronize()
+        assert torch.equal(idx[a:a + part], i2) and torch.equal(w[a:a + part], w2)
