@@ -18,7 +18,8 @@
 // the row is requantised there. With few workgroups a second set of 8 waves takes the upper
 // half of K (the sums meet in LDS). few_linear2: a workgroup owns 32 output columns; its 8 waves
 // share the (expert, 512 K) pieces, each adds w * (its partial products) per token into its own
-// FP32 tile in LDS, and the tiles are added in wave order.
+// FP32 tile in LDS, and the tiles are added in wave order. Narrow outputs take 16 columns and, up to 16
+// tokens, 16 waves a workgroup.
 //
 // One or two tokens of 8 experts give few_linear1 fewer blocks than there are CUs, and a CU reads no more
 // than about 40 GB/s. Where h is at most 32 K elements a workgroup therefore takes half a block in four
@@ -41,8 +42,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kMaxT = MOE_FEW_MAX_TOKENS;
 // Largest x kept in LDS (beside 31.5 KB of few_linear1's own)
 constexpr size_t kMaxXLds = 120 * 1024;
@@ -51,6 +50,10 @@ constexpr int kAllRecords = -1;
 constexpr int kNt = 2;                   // buffer loads: non-temporal
 // Most elements of h that few_linear2 requantises itself
 constexpr int kMaxH32 = 32 * 1024;
+// Most workgroups of 32 columns that become twice as many of 16 (5 tokens, top-2 of 8, 7168 x 4096: 59.6 us by
+// 224 of 32 columns, 65.9 by 448 of 16; 16 tokens, top-4 of 16, 4096 x 1024: 31.2 against 28.9; one, 2048 x
+// 2048: 15.9 against 14.0)
+constexpr int kNarrow = 128;
 
 // A row of a chosen expert: the token's first slot that names it, and its weights' sum
 struct FewRow {
@@ -119,7 +122,8 @@ struct Chunk {
     uint32_t s0, s1, sa[FM];
 };
 
-template <int C, int FM, int OPS0>
+// (NF: column sets, 1: b0 only)
+template <int C, int FM, int OPS0, int NF = 2>
 __device__ inline void multiply(const Chunk<C, FM>& c, int ks, int nks, v4f (&c0)[FM], v4f (&c1)[FM]) {
     auto step = [&](auto i) __attribute__((always_inline)) {
         constexpr int S = decltype(i)::value;
@@ -128,7 +132,7 @@ __device__ inline void multiply(const Chunk<C, FM>& c, int ks, int nks, v4f (&c0
 #pragma unroll
                 for (int f = 0; f < FM; ++f) {
                     c0[f] = mfma<OPS0 + S>(c.a[f][S], c.b0[S], c0[f], c.sa[f], c.s0);
-                    c1[f] = mfma<OPS0 + S>(c.a[f][S], c.b1[S], c1[f], c.sa[f], c.s1);
+                    if constexpr (NF == 2) c1[f] = mfma<OPS0 + S>(c.a[f][S], c.b1[S], c1[f], c.sa[f], c.s1);
                 }
             }
         }
@@ -222,30 +226,40 @@ __device__ inline void linear1_sums(const FewArgs& p, const int* tok, int cnt, c
 }
 
 // The u-th chosen expert of at most 64 slots, its tokens (ascending) and their first slots, by each wave for
-// itself: lane s holds slot s, an expert's first slot stands for it, and its rank is the number of
-// smaller such. Also the number of chosen experts and the rows of those before this one.
+// itself: lane s holds slot s; the lanes with the same expert meet by ballots of its bits, the first of
+// them stands for it, and the u-th smallest of those is found bit by bit. Also the number of chosen
+// experts and the rows of those before this one.
 struct Chosen {
     int expert, cnt, used, before;
     uint64_t slots;            // the slots that stand for one of its tokens
     uint64_t all;              // all slots that name it
 };
 __device__ inline Chosen choose64(const FewArgs& p, int lane, int u) {
-    const int S = p.T * p.k, t = lane / p.k;
-    const int id = lane < S ? p.idx[lane] : -1;
+    const int id = lane < p.T * p.k ? p.idx[lane] : -1;
     const int e = id >= 0 && id < p.E ? id : -1;
-    bool again = false, again_in_token = false;         // an earlier slot (of the token) names the same expert
-    for (int j = 0; j < S - 1; ++j) {
-        const int ej = __builtin_amdgcn_readlane(e, j);
-        again = again || (j < lane && ej == e);
-        again_in_token = again_in_token || (j < lane && ej == e && j >= t * p.k);
+    const int nbits = p.E > 1 ? 32 - __clz(p.E - 1) : 0;
+    const uint64_t have = __ballot(e >= 0);
+    uint64_t peers = have;
+    for (int b = 0; b < nbits; ++b) {
+        const bool one = (e >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        peers &= one ? ones : ~ones;
     }
-    const uint64_t first = __ballot(e >= 0 && !again);
-    int rank = 0;
-    for (uint64_t f = first; f != 0; f &= f - 1) rank += __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)f) - 1) < e;
+    // earlier slots (of the token: from its first slot on) that name the same expert
+    const uint64_t earlier = peers & ((1ull << lane) - 1);
+    const bool again_in_token = (earlier >> (lane - lane % p.k)) != 0;
+    const uint64_t first = __ballot(e >= 0 && earlier == 0);
     Chosen c;
     c.used = __popcll(first);
-    const uint64_t hit = __ballot(e >= 0 && !again && rank == u);
-    c.expert = hit ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)hit) - 1) : -1;
+    uint64_t at = first;
+    int rest = u;
+    for (int b = nbits - 1; b >= 0; --b) {
+        const uint64_t ones = __ballot((e >> b) & 1), zeros = at & ~ones;
+        const int n = __popcll(zeros);
+        at = rest < n ? zeros : at & ones;
+        rest -= rest < n ? 0 : n;
+    }
+    c.expert = u < c.used ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)at) - 1) : -1;
     c.all = __ballot(e >= 0 && e == c.expert);
     c.slots = __ballot(e >= 0 && e == c.expert && !again_in_token);
     c.cnt = __popcll(c.slots);
@@ -459,18 +473,16 @@ __global__ __launch_bounds__(64 * CW * KS, 4) void few_linear1(FewArgs p) {
     }
 }
 
-// Output columns per workgroup: two fragments
-constexpr int kFewCols = 32;
-
+// NF: fragments of 16 output columns per workgroup; WAVES share its pieces.
 // H32: h comes in FP32 (at most kMaxH32 of it) and every workgroup requantises all of it into LDS while its
 // first weights arrive (the codes and scales also go to h8 and h_sf, one row per workgroup)
-template <int FM, bool H32>
-__global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
-    constexpr int C = 4;
-    // a token's row of a wave's tile: 36 floats, so that the 4 rows of a lane group fall into
+template <int FM, bool H32, int NF, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, WAVES / 4) void few_linear2(FewArgs p) {
+    constexpr int C = 4, kThreads = WAVES * 64, kCols = 16 * NF;
+    // a token's row of a wave's tile: 4 floats more, so that the 4 rows of a lane group fall into
     // different banks
-    constexpr int kPitch = kFewCols + 4;
-    __shared__ float tile[kFewWaves][FM * 16][kPitch];
+    constexpr int kPitch = kCols + 4;
+    __shared__ float tile[WAVES][FM * 16][kPitch];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l = lane & 15;
@@ -478,26 +490,26 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
     // wait for every weight load in flight (entries past the last are copied, not used)
     __shared__ FewRow rows[H32 ? 64 : kMaxT * MOE_MAX_TOPK];
     __shared__ FewSeg segs[H32 ? 64 : MOE_MAX_EXPERTS];
-    for (int i = tid; i < p.T * p.k; i += kFewThreads) rows[i] = p.rows[i];
-    for (int i = tid; i < min(p.E, p.T * p.k); i += kFewThreads) segs[i] = p.segs[i];
+    for (int i = tid; i < p.T * p.k; i += kThreads) rows[i] = p.rows[i];
+    for (int i = tid; i < min(p.E, p.T * p.k); i += kThreads) segs[i] = p.segs[i];
     __shared__ __attribute__((aligned(16))) uint8_t codes[H32 ? kMaxH32 : 16];
     __shared__ __attribute__((aligned(16))) uint8_t scales[H32 ? kMaxH32 / 32 : 16];     // rows of 4 * ceil(I / 512)
-    v4f h[H32 ? kMaxH32 / 4 / kFewThreads : 1];
+    v4f h[H32 ? kMaxH32 / 4 / kThreads : 1];
     const int hn = p.T * p.k * p.I / 4;
     if constexpr (H32) {
 #pragma unroll
-        for (int j = 0; j < kMaxH32 / 4 / kFewThreads; ++j) {
-            const int i = j * kFewThreads + tid;
-            if (j * kFewThreads < hn) h[j] = *reinterpret_cast<const v4f*>(p.h32 + 4 * (size_t)min(i, hn - 1));
+        for (int j = 0; j < kMaxH32 / 4 / kThreads; ++j) {
+            const int i = j * kThreads + tid;
+            if (j * kThreads < hn) h[j] = *reinterpret_cast<const v4f*>(p.h32 + 4 * (size_t)min(i, hn - 1));
         }
     }
     for (int i = lane; i < FM * 16 * kPitch; i += 64) (&tile[wave][0][0])[i] = 0.f;
     // each XCD (workgroup id mod 8) takes adjacent column tiles
     const int v = (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
-    const int frag = (v & 7) * 2, nt = v >> 3;
+    const int frag = v % (16 / NF) * NF, nt = v / (16 / NF);
     const int nks = p.I / 128, nkb = (nks + 3) / 4;
     const int items = __builtin_amdgcn_readfirstlane(*p.n_used) * nkb;
-    const int first = (int)((long long)items * wave / kFewWaves), last = (int)((long long)items * (wave + 1) / kFewWaves);
+    const int first = (int)((long long)items * wave / WAVES), last = (int)((long long)items * (wave + 1) / WAVES);
     const uint32_t hsfs = 4 * (uint32_t)nkb;
     v4f c0[FM], c1[FM];
 #pragma unroll
@@ -530,7 +542,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
         }
         const __amdgpu_buffer_rsrc_t rs_s = rsrc_if(bs + (size_t)kb * kBScaleBlockBytes, left);
         c.s0 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 0, kNt);
-        c.s1 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 256, kNt);
+        if constexpr (NF == 2) c.s1 = __builtin_amdgcn_raw_buffer_load_b32(rs_s, lane * 4, 256, kNt);
         const __amdgpu_buffer_rsrc_t rs_h = rsrc_if(p.h8, left), rs_hsf = rsrc_if(p.h_sf, left);
         if constexpr (!H32) {
 #pragma unroll
@@ -541,7 +553,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
             const int kc = min(4 * kb + i, nks - 1);
             const __amdgpu_buffer_rsrc_t rs_b = rsrc_if(bd + (size_t)kc * kBTileBytes, min(left, nks - 4 * kb - i));
             c.b0[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, 0, kNt));
-            c.b1[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, kFragBytes, kNt));
+            if constexpr (NF == 2)
+                c.b1[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16, kFragBytes, kNt));
             if constexpr (H32) continue;
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
@@ -577,7 +590,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
     // multiplies a piece; adds the products of its expert to its tokens' sums once the last piece of it is done
     auto use = [&](Chunk<C, FM>& c, int it) __attribute__((always_inline)) {
         h_rows(c);
-        multiply<C, FM, 0>(c, ukb * 4, nks, c0, c1);
+        multiply<C, FM, 0, NF>(c, ukb * 4, nks, c0, c1);
         const FewSeg s = segs[uu];
         const bool end = ++ukb == nkb;
         if (end) {
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
                     const FewRow e = rows[s.first + row];
                     float* y = tile[wave][e.slot / p.k];
                     y[l] = __builtin_fmaf(e.weight, c0[f][r], y[l]);
-                    y[16 + l] = __builtin_fmaf(e.weight, c1[f][r], y[16 + l]);
+                    if constexpr (NF == 2) y[16 + l] = __builtin_fmaf(e.weight, c1[f][r], y[16 + l]);
                 }
                 c0[f][r] = c1[f][r] = 0.f;
             }
@@ -608,12 +621,12 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
     if constexpr (H32) {
         // 4 values a thread, a 128-column block of a row on 32 lanes: its largest |h|, the scale byte, the
         // codes; 16-byte chunk c of a block at chunk c ^ (row % 8)
-        const int down = 4 * kFewThreads / p.I, right = 4 * kFewThreads % p.I;
+        const int down = 4 * kThreads / p.I, right = 4 * kThreads % p.I;
         const int mine = (int)blockIdx.x, mine2 = mine + (int)gridDim.x;     // (at least 32 workgroups, at most 64 rows)
         int row = 4 * tid / p.I, col = 4 * tid % p.I;
 #pragma unroll
-        for (int j = 0; j < kMaxH32 / 4 / kFewThreads; ++j) {
-            if (j * kFewThreads >= hn) continue;   // uniform
+        for (int j = 0; j < kMaxH32 / 4 / kThreads; ++j) {
+            if (j * kThreads >= hn) continue;   // uniform
             uint32_t a = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) a = max(a, __float_as_uint(fabsf(h[j][q])));
@@ -656,20 +669,22 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_linear2(FewArgs p) {
     if (it + 1 < last) use(odd, it + 1);
     __syncthreads();
     // tile column 16*q + j: lane column j of fragment frag + q, row 128*(f/8) + 8*j + f%8 of the
-    // 256-row tile; a thread stores the two adjacent columns of both fragments
+    // 256-row tile; a thread stores the adjacent columns of both fragments
     const int col0 = nt * 256 + 128 * (frag >> 3) + (frag & 7);
-    for (int i = tid; i < p.T * 16; i += kFewThreads) {
+    for (int i = tid; i < p.T * 16; i += kThreads) {
         const int t = i >> 4, j = i & 15;
-        float a = tile[0][t][j], b = tile[0][t][16 + j];
+        float a = tile[0][t][j], b = NF == 2 ? tile[0][t][kCols - 16 + j] : 0.f;
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) {
+        for (int w = 1; w < WAVES; ++w) {
             a += tile[w][t][j];
-            b += tile[w][t][16 + j];
+            if constexpr (NF == 2) b += tile[w][t][16 + j];
         }
         const int col = col0 + 8 * j;
         if (col < p.H) {
             const uint32_t lo = __builtin_bit_cast(uint16_t, (__bf16)a), hi = __builtin_bit_cast(uint16_t, (__bf16)b);
-            *reinterpret_cast<uint32_t*>(p.y + (size_t)t * p.H + col) = lo | (hi << 16);
+            uint16_t* y = p.y + (size_t)t * p.H + col;
+            if constexpr (NF == 2) *reinterpret_cast<uint32_t*>(y) = lo | (hi << 16);
+            else *y = (uint16_t)lo;
         }
     }
 }
@@ -725,23 +740,36 @@ hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t
     p.y = y;
     // at most one expert per slot can be chosen
     const int max_used = s.num_experts < T * s.num_topk ? s.num_experts : T * s.num_topk;
-    const unsigned g1 = (unsigned)max_used * (unsigned)(s.intermediate / 128), g2 = (unsigned)cdiv(s.hidden, 256) * 8u;
+    const unsigned g1 = (unsigned)max_used * (unsigned)(s.intermediate / 128), tiles2 = (unsigned)cdiv(s.hidden, 256);
     // With fewer workgroups than CUs, more waves in each, with x in LDS where it fits (the registers
     // then hold weights only); where h is small, half blocks of it by twice the workgroups
     const size_t x_bytes = (size_t)T * (s.hidden + 4 * cdiv(s.hidden, 512));
     const int slots = T * s.num_topk;
     const bool split = g1 < 256 && T <= 16 && s.hidden >= 1024 && x_bytes <= kMaxXLds;
+    bool h32 = false;
     if (T > 16) {
         few_linear1<2, 1, 2, 8, false><<<g1, 512, 0, stream>>>(p);
-        few_linear2<2, false><<<g2, kFewThreads, 0, stream>>>(p);
     } else if (split && slots <= 64 && (size_t)slots * s.intermediate <= kMaxH32) {
         few_linear1<1, 4, 4, 4, true><<<2 * g1, 1024, x_bytes, stream>>>(p);
-        few_linear2<1, true><<<g2, kFewThreads, 0, stream>>>(p);
+        h32 = true;
+    } else if (split) {
+        few_linear1<1, 2, 4, 8, false><<<g1, 1024, x_bytes, stream>>>(p);
+    } else if (slots <= 64) {
+        few_linear1<1, 1, 2, 8, true><<<g1, 512, 0, stream>>>(p);
     } else {
-        if (split) few_linear1<1, 2, 4, 8, false><<<g1, 1024, x_bytes, stream>>>(p);
-        else if (slots <= 64) few_linear1<1, 1, 2, 8, true><<<g1, 512, 0, stream>>>(p);
-        else few_linear1<1, 1, 2, 8, false><<<g1, 512, 0, stream>>>(p);
-        few_linear2<1, false><<<g2, kFewThreads, 0, stream>>>(p);
+        few_linear1<1, 1, 2, 8, false><<<g1, 512, 0, stream>>>(p);
+    }
+    // narrow outputs: 16 columns a workgroup, and (16 tokens, where the registers allow it) twice the waves
+    const bool narrow = tiles2 * 8 <= (unsigned)kNarrow;
+    if (T > 16) {
+        if (narrow) few_linear2<2, false, 1, 8><<<tiles2 * 16, 512, 0, stream>>>(p);
+        else few_linear2<2, false, 2, 8><<<tiles2 * 8, 512, 0, stream>>>(p);
+    } else if (h32) {
+        if (narrow) few_linear2<1, true, 1, 16><<<tiles2 * 16, 1024, 0, stream>>>(p);
+        else few_linear2<1, true, 2, 8><<<tiles2 * 8, 512, 0, stream>>>(p);
+    } else {
+        if (narrow) few_linear2<1, false, 1, 16><<<tiles2 * 16, 1024, 0, stream>>>(p);
+        else few_linear2<1, false, 2, 8><<<tiles2 * 8, 512, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
