@@ -28,6 +28,7 @@
 // rounds of 256 x 256 tiles (4096 x 4096 x 7168: 90 to 102 us on different cards; a library product
 // with one scale per tensor reaches 2.66 at 4096 x 7168 x 18432). 64-row tiles that stream B once
 // (32 groups of about 32 rows, 4096 x 7168 each) run at 5.9 TB/s.
+#include <algorithm>
 #include <cmath>
 
 #include "moe_internal.h"
@@ -788,23 +789,23 @@ void launch_tiled(unsigned grid, const GemmFp8Args& a, hipStream_t stream) {
 }
 
 // Microseconds of a product with each kernel. Tiled: rounds of 256 workgroups, each fixed + step per
-// 128 K, fitted to 16 products from 256 x 256 x 2048 to 4096 x 4096 x 7168 (for instance 4096 x 4096 x
-// 7168 by 256 and 128 rows: 96 and 151 us). Skinny: fixed + wave per step that a wave takes + for
-// every 256 workgroups tile + step per 128 K, fitted to 35 products (FP32: 23) from 1 x 256 x 512 to
-// 2 x 20000 x 7168, 2048 x 2048 x 18432 and 4096 x 4096 x 2048, each timed with every kernel, weights
-// from memory: what the model picks is 1 % slower than the best of the kernels on average, 10 % at most.
-// Tiles of 16 rows are for dense products: of a list's 64-row tiles with few rows 3 in 4 workgroups
-// would have none, and the others would share a quarter of the CUs.
+// 128 K. Skinny: fixed + wave per step that a wave takes + for every 256 workgroups tile + step per
+// 128 K. Fitted to 35 products (FP32: 23) from 1 x 256 x 512 to 2 x 20000 x 7168, 2048 x 2048 x 18432
+// and 4096 x 4096 x 2048, each timed with every kernel, weights from memory, and the tiled ones to
+// 4096 x 4096 x 7168 (256 rows: 90 to 100 us) and 4096 x 7168 x 18432 (256 columns 453, 224 432) too:
+// what the model picks is 1 to 2 % slower than the best of the kernels on average, 10 % at most.
+// Of a list's 64-row tiles with few rows 3 in 4 workgroups of 16 rows have none and the others share a
+// quarter of the CUs, so that there all count (16 x 4096 x 4096 so: 13.6 us, without the empty ones 6.9).
 struct Cost {
     Fp8Kernel kernel;
     int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
     int threads;
     double fixed, step, wave, tile;
 };
-constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 256, 6.0, 1.45, 0, 0},
-                          {Fp8Kernel::kTiled128, 128, 128, 256, 256, 4.0, 0.83, 0, 0},
-                          {Fp8Kernel::kTiled64, 64, 64, 256, 256, 4.9, 0.70, 0, 0},
-                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 256, 10.0, 1.31, 0, 0},
+constexpr Cost kBf16[] = {{Fp8Kernel::kTiled256, 256, 256, 256, 256, 10.8, 1.50, 0, 0},
+                          {Fp8Kernel::kTiled128, 128, 128, 256, 256, 7.0, 0.80, 0, 0},
+                          {Fp8Kernel::kTiled64, 64, 64, 256, 256, 4.6, 0.72, 0, 0},
+                          {Fp8Kernel::kTiled256x224, 256, 256, 224, 256, 13.5, 1.38, 0, 0},
                           {Fp8Kernel::kSkinny64, 64, 64, 64, 512, 2.26, 0.185, 2.05, 2.89},
                           {Fp8Kernel::kSkinny32, 64, 32, 32, 512, 1.89, 0.093, 0.95, 0.75},
                           {Fp8Kernel::kSkinny16x32, 64, 16, 32, 512, 2.12, 0.064, 0.68, 0.40},
@@ -824,9 +825,9 @@ Fp8Plan cheapest(const Cost (&costs)[NK], int groups, double rows, int max_rows,
         // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
         const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cdiv(N, c.bn);
         if (c.kernel != Fp8Kernel::kTiled128 && grid * c.threads >= (1ull << 32)) continue;
-        if (ragged && c.bm < 32) continue;
         // groups of unknown length end in a tile that is half full on average
-        const double mt = groups * (ragged ? rows / c.bm + 0.5 : std::ceil(rows / c.bm));
+        double mt = groups * (ragged ? rows / c.bm + 0.5 : std::ceil(rows / c.bm));
+        if (ragged && c.bm < 32) mt = groups * std::max(1.0, rows / 64 + 0.5) * (64 / c.bm);
         const double tiles = std::ceil(mt) * std::ceil((double)N / c.bn);
         double t = 0;
         if (c.wave > 0) {
