@@ -197,3 +197,18 @@ def test_router_passes(E):
         moe.moe_topk_router(i2, w2, xs, moe.MOE_F32, n, E, k, moe.MOE_ROUTER_SOFTMAX_CHOSEN)
         torch.cuda.synchronize()
         assert torch.equal(idx[a:a + part], i2) and torch.equal(w[a:a + part], w2)
+
+
+@pytest.mark.parametrize("M,G", [(1024, 256), (1025, 256), (1024, 257), (257, 256), (1000, 3), (16385, 2), (4097, 5), (8193, 5)])
+def test_contiguous_grouping_borders(M, G):
+    """Row and group counts at which the grouping changes its kernel."""
+    K, N = 128, 40
+    p = Problem(M, N, K, G, moe.MOE_BF16, seed=M + G)
+    grp = np.random.default_rng(G).integers(-1, G, size=M).astype(np.int32)
+    grp[0] = G - 1
+    d = p.contiguous(grp)
+    for g in range(0, G, max(1, G // 20)):
+        p.check(d, np.nonzero(grp == g)[0], g)
+    p.check(d, np.nonzero(grp == G - 1)[0], G - 1)
+    assert (d[grp < 0] == POISON[moe.MOE_BF16]).all()
+    assert np.array_equal(p.contiguous(grp), d), "two calls gave different bytes"
