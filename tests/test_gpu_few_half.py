@@ -27,6 +27,9 @@ from test_gpu_few import FewRun, check  # noqa: E402
     (MoEConfig("half_64", T=16, E=9, k=4, H=1024, I=384), 4096),
     (MoEConfig("half_66", T=11, E=9, k=6, H=1024, I=128), 11),           # more slots than lanes
     (MoEConfig("half_i128", T=8, E=70, k=8, H=1024, I=128), 8),
+    (MoEConfig("wide_20", T=20, E=4, k=2, H=4352, I=256), 20),           # more than 128 workgroups of 32 columns
+    (MoEConfig("narrow_20", T=20, E=4, k=2, H=4096, I=384), 32),         # 128: of 16 columns
+    (MoEConfig("wide_66", T=11, E=9, k=6, H=4224, I=128), 11),
     (MoEConfig("half_shared", T=12, E=2, k=2, H=1664, I=768), 12),       # every token to both experts
 ], ids=lambda v: v.name if hasattr(v, "name") else str(v))
 def test_parity(cfg, max_tokens):
