@@ -187,7 +187,7 @@ __device__ inline float lanes_sum(float v) {
 }
 
 // 64/L tokens per wave, V experts per lane (E <= L * V), k <= 16. Q: experts of a lane that are
-// adjacent and loaded at once (4: FP32 logits, E % 4 == 0)
+// adjacent and loaded at once (4: E % 4 == 0)
 template <int L, int V, bool BF16, int Q>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __restrict__ logits, int T, int E, int k,
                                                                 int over_all, float scale,
@@ -218,7 +218,12 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
             (int)(uint32_t)(rest < 0xffffffffu ? rest : 0xffffffffu), 0x00020000);
 #pragma unroll
         for (int i = 0; i < V; i += Q) {
-            if constexpr (Q == 4) {
+            if constexpr (Q == 4 && BF16) {
+                typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+                const v2u x = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(rs, offset + i * L * kBytes, 0, 0));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ahead[i + q] = __uint_as_float(q % 2 ? x[q / 2] & 0xffff0000u : x[q / 2] << 16);
+            } else if constexpr (Q == 4) {
                 typedef float v4f __attribute__((ext_vector_type(4)));
                 const v4f x = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, offset + i * L * kBytes, 0, 0));
 #pragma unroll
@@ -337,15 +342,14 @@ void launch(const void* logits, int T, int E, int k, int over_all, float scale, 
         kernel<<<passes && g > kRouterGroups ? kRouterGroups : g, kRouterThreads, 0, stream>>>(logits, T, E, k, over_all, scale, idx, w);
     };
     if (k <= 16) {
-        // 32768 x 256 FP32, top-8: 13.8 us with single loads, 12.9 with fours (in a graph)
-        constexpr int Q = BF16 ? 1 : 4;
-        const bool quads = !BF16 && E % 4 == 0;
+        // 32768 x 256, top-8, in a graph: FP32 13.8 us with single loads, 12.9 with fours; bf16 10.1 and 9.3
+        const bool quads = E % 4 == 0;
         if (E <= 32) run(router_kernel<16, 2, BF16, 1>, 4);
-        else if (E <= 64) quads ? run(router_kernel<16, 4, BF16, Q>, 4) : run(router_kernel<16, 4, BF16, 1>, 4);
-        else if (E <= 128) quads ? run(router_kernel<16, 8, BF16, Q>, 4) : run(router_kernel<16, 8, BF16, 1>, 4);
-        else if (E <= 256) quads ? run(router_kernel<16, 16, BF16, Q>, 4) : run(router_kernel<16, 16, BF16, 1>, 4);
-        else if (E <= 512) quads ? run(router_kernel<32, 16, BF16, Q>, 2) : run(router_kernel<32, 16, BF16, 1>, 2);
-        else quads ? run(router_kernel<64, 16, BF16, Q>, 1) : run(router_kernel<64, 16, BF16, 1>, 1);
+        else if (E <= 64) quads ? run(router_kernel<16, 4, BF16, 4>, 4) : run(router_kernel<16, 4, BF16, 1>, 4);
+        else if (E <= 128) quads ? run(router_kernel<16, 8, BF16, 4>, 4) : run(router_kernel<16, 8, BF16, 1>, 4);
+        else if (E <= 256) quads ? run(router_kernel<16, 16, BF16, 4>, 4) : run(router_kernel<16, 16, BF16, 1>, 4);
+        else if (E <= 512) quads ? run(router_kernel<32, 16, BF16, 4>, 2) : run(router_kernel<32, 16, BF16, 1>, 2);
+        else quads ? run(router_kernel<64, 16, BF16, 4>, 1) : run(router_kernel<64, 16, BF16, 1>, 1);
     } else {
         if (E <= 64) run(router_wave_kernel<1, BF16>, 1, false);
         else if (E <= 128) run(router_wave_kernel<2, BF16>, 1, false);

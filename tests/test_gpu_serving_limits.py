@@ -163,16 +163,17 @@ def test_few_or_small_tiles(M, N, K, ty):
     assert np.array_equal(p.dense(), d)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("E", [33, 36, 63, 64, 100, 127, 128, 201, 252, 256, 257, 384, 510, 512, 644, 1023, 1024])
-def test_router_rows_end_anywhere(E):
+def test_router_rows_end_anywhere(E, dtype):
     """Expert counts around the kernels' borders, multiples of 4 (loaded in fours) and not; the row behind
     the last token would win every choice."""
     T, k = 300, 8
-    x = torch.full((T + 1, E), 1e30, device="cuda")
-    x[:T] = torch.randn(T, E, device="cuda")
+    x = torch.full((T + 1, E), 1e30, device="cuda", dtype=dtype)
+    x[:T] = torch.randn(T, E, device="cuda").to(dtype)
     idx = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
     w = torch.full((T + 1, k), -7.0, device="cuda")
-    moe.moe_topk_router(idx, w, x, moe.MOE_F32, T, E, k, moe.MOE_ROUTER_SOFTMAX_ALL)
+    moe.moe_topk_router(idx, w, x, moe.MOE_BF16 if dtype == torch.bfloat16 else moe.MOE_F32, T, E, k, moe.MOE_ROUTER_SOFTMAX_ALL)
     torch.cuda.synchronize()
     ref_idx, ref_w = oracle.topk_router(x[:T].double().cpu().numpy(), k, True)
     assert np.array_equal(idx[:T].cpu().numpy(), ref_idx)
