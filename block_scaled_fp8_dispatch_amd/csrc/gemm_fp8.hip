@@ -6,8 +6,10 @@
 // bits below it (measured on gfx950: 2^16 + 270 within 8 gives 2^16 + 264; across groups of 8 the
 // sum is FP32's), about 1.5e-5 of the result's norm on normal data: far below a bf16 output's
 // rounding (1.7e-3), but not FP32. FP32 outputs therefore go through v_mfma_f32_16x16x32_bf16,
-// at half its rate: an e4m3 value times its block's power of two is exact in bf16 (3 mantissa
-// bits of 7, the exponent range of FP32), and that instruction's sums are FP32's.
+// at half its rate, whose sums are FP32's: an e4m3 value times its block's power of two is exact
+// in bf16 (3 mantissa bits of 7, the exponent range of FP32) for scale bytes 3 to 246. Rows with a
+// byte outside, their own or their columns', are computed again from the codes alone, both
+// scales going to each block's sum (add_block).
 //
 // Tiled kernel (bf16 outputs). A workgroup of 4 waves owns a BM x 256 tile of D. Both operands
 // of a K step (BM x 128 and 256 x 128 bytes) go straight from memory into LDS rings
@@ -48,17 +50,48 @@ constexpr int kCus = 256;                 // compute units of an MI355X
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-// 2^(byte - 127) as the operand of the scaled conversions, which read its exponent field (byte
-// 255: NaN)
-__device__ inline float scale_f32(int byte) { return __uint_as_float(byte == 255 ? 0x7fc00000u : (uint32_t)byte << 23); }
+// 2^(byte - 127) as the operand of the scaled conversions, which read its exponent field
+__device__ inline float scale_f32(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// two words of e4m3 codes (8 values) times 2^(byte - 127), exact in bf16
+// The largest `byte - 3` (unsigned) of a row's scale bytes: above kBf16Holds where an e4m3 value times 2^(byte - 127)
+// need not be a bf16 number (448 * 2^119 is below bf16's largest, 2^-9 * 2^-124 its smallest). The loops keep it, at
+// two instructions a byte, and what it says is looked at once behind them (a branch in every step: 128 x 32 x 7168 6.0 us
+// instead of 5.5, 33 x 7168 x 2048 9.2 instead of 6.9).
+constexpr uint32_t kBf16Holds = 246 - 3;
+// (pinned: done before the byte's register is loaded again, else the byte is copied, which waits for that load)
+__device__ inline void keep_beyond(uint32_t& far, uint32_t byte) {
+    far = max(far, byte - 3u);
+    asm volatile("" : "+v"(far));
+}
+
+// two words of e4m3 codes (8 values) times 2^(byte - 127), exact in bf16 for bytes 3 to 246
 __device__ inline v8bf to_bf16(int w0, int w1, float scale) {
     const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
     const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
     const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
     const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
     return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// sum += the products of one K step for a fragment's rows and columns, from the codes unscaled (exact in bf16) and
+// both scales on the block's sum, so that nothing on the way leaves FP32's range unless the result does. row: the
+// scale bytes of the lane's rows 4g .. 4g+3, col: the columns'
+__device__ inline void add_block(v4f& sum, const v8i& a, const v8i& b, const uint32_t (&row)[4], uint32_t col) {
+    v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(a[2 * q], a[2 * q + 1], 1.0f), to_bf16(b[2 * q], b[2 * q + 1], 1.0f),
+                                                    x, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        sum[r] += row[r] == 255u || col == 255u ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(x[r], (int)(row[r] + col) - 254);
+}
+
+// A lane's codes of K step ks from memory, as a fragment read from LDS has them
+__device__ inline v8i load_block(__amdgpu_buffer_rsrc_t rs, uint32_t at, int ks) {
+    const v4i lo = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, at, ks * kBK, 0));
+    const v4i hi = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, at + 64, ks * kBK, 0));
+    return (v8i){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 }
 
 // Stores the first `left` of n adjacent columns of a row. A row may start at any element, so the
@@ -202,6 +235,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+    uint32_t far_a[FM] = {}, far_b = 0;            // F32: keep_beyond() of this wave's steps
     const int nks = p.K / kBK;
     // step ks of this wave, in slot S: wait until only the younger slots' loads (if any) are in
     // flight, multiply, refill
@@ -218,20 +252,22 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
         else wait(IntC<0>{});
         const uint8_t* src = mine + S * C::SLOT;
         if constexpr (F32) {
+            keep_beyond(far_b, sb[S]);
             v8bf bv[FN][4];
 #pragma unroll
             for (int n = 0; n < FN; ++n) {
                 const v8i w = read(src + (BM + n * 16) * kBK);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) bv[n][q] = to_bf16(w[2 * q], w[2 * q + 1], scale_f32((int)sb[S]));
+                for (int q = 0; q < 4; ++q) bv[n][q] = to_bf16(w[2 * q], w[2 * q + 1], scale_f32(sb[S]));
             }
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
+                keep_beyond(far_a[f], sa[S][f]);
                 const v8i w = read(src + f * 16 * kBK);
                 // the same 8 consecutive codes of a lane on both sides: any order of K will do
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const v8bf av = to_bf16(w[2 * q], w[2 * q + 1], scale_f32((int)sa[S][f]));
+                    const v8bf av = to_bf16(w[2 * q], w[2 * q + 1], scale_f32(sa[S][f]));
 #pragma unroll
                     for (int n = 0; n < FN; ++n)
                         acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[n][q], acc[f][n], 0, 0, 0);
@@ -262,6 +298,19 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
     };
     each_slot(wave, issue);
     for (int ks = wave; ks < nks; ks += SLOTS * WAVES) each_slot(ks, step);
+    // F32: the rows that need add_block in some wave's steps, and whether there are any
+    __shared__ uint8_t far_rows[F32 ? WAVES : 1][BM];
+    __shared__ int far_any[WAVES];
+    if constexpr (F32) {
+        bool any = false;
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            const bool far = max(far_a[f], far_b) > kBf16Holds;
+            far_rows[wave][f * 16 + l] = far;
+            any |= far;
+        }
+        far_any[wave] = __ballot(any) != 0;
+    }
     __syncthreads();                               // the sums reuse the slots of all waves
     float* const sums = reinterpret_cast<float*>(smem);
     auto at = [&](int w, int r, int n) __attribute__((always_inline)) -> float& { return sums[(w * BM + r) * PITCH + n]; };
@@ -283,14 +332,10 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
                 for (int r = 0; r < 4; ++r) at(wave, f * 16 + 4 * g + r, n * 16 + l) += acc[f][n][r];
     }
     __syncthreads();
-    // four adjacent columns per thread
-    for (int i = tid; i < BM * BN / 4; i += WAVES * 64) {
-        const int r = i / (BN / 4), c = i % (BN / 4) * 4, n = nt * BN + c;
-        const int row = d_row(r);
-        if (row < 0) continue;
-        v4f x = *reinterpret_cast<const v4f*>(&at(0, r, c));
-#pragma unroll
-        for (int w = 1; w < WAVES / 2; ++w) x += *reinterpret_cast<const v4f*>(&at(w, r, c));
+    // columns c .. c+3 of row r
+    auto store = [&](int r, int c, const v4f& x) __attribute__((always_inline)) {
+        const int row = d_row(r), n = nt * BN + c;
+        if (row < 0) return;
         const size_t to = (size_t)row * p.N + n;
         if constexpr (F32) {
             const float out[4] = {x.x, x.y, x.z, x.w};
@@ -300,6 +345,51 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp8_skinny(GemmFp8Args p) {
             const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x.z, x.w}), v2bf));
             const uint16_t out[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
             store_columns<4>(static_cast<uint16_t*>(p.d) + to, out, p.N - n);
+        }
+    };
+    // four adjacent columns per thread
+    for (int i = tid; i < BM * BN / 4; i += WAVES * 64) {
+        const int r = i / (BN / 4), c = i % (BN / 4) * 4;
+        v4f x = *reinterpret_cast<const v4f*>(&at(0, r, c));
+#pragma unroll
+        for (int w = 1; w < WAVES / 2; ++w) x += *reinterpret_cast<const v4f*>(&at(w, r, c));
+        store(r, c, x);
+    }
+    if constexpr (F32) {
+        int any = 0;                               // (looked up before the stores: 0.2 us more)
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) any |= far_any[w];
+        if (__builtin_amdgcn_readfirstlane(any) == 0) return;
+        // fragment after fragment, operands straight from memory; the waves share K as before. Each element is
+        // stored over by the thread that stored it.
+        for (int i = 0; i < FM * FN; ++i) {
+            const int f = i / FN, n = i % FN;
+            bool far = false;                      // row 16f + l
+            for (int w = 0; w < WAVES; ++w) far |= far_rows[w][f * 16 + l] != 0;
+            const uint64_t rows = __ballot(far);
+            if (rows == 0) continue;
+            const uint32_t a_at = a_row(f * 16 + l) * (uint32_t)p.K + 16 * g;
+            const uint32_t b_at = (uint32_t)(min(nt * BN + n * 16 + l, p.N - 1) - nt * BN) * (uint32_t)p.K + 16 * g;
+            v4f sum = {0.f, 0.f, 0.f, 0.f};
+            for (int ks = wave; ks < nks; ks += WAVES) {
+                uint32_t row[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    row[r] = __builtin_amdgcn_raw_buffer_load_b8(rs_asf, a_row(f * 16 + 4 * g + r) * (uint32_t)p.sf_stride, ks, 0);
+                add_block(sum, load_block(rs_a, a_at, ks), load_block(rs_b, b_at, ks), row,
+                          __builtin_amdgcn_raw_buffer_load_b8(rs_bsf, 0, ks, 0));
+            }
+            __syncthreads();                       // what lies in the slots has been read
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[(wave * 16 + 4 * g + r) * 20 + l] = sum[r];
+            __syncthreads();
+            for (int j = tid; j < BM * BN / 4; j += WAVES * 64) {
+                const int r = j / (BN / 4), c = j % (BN / 4) * 4;
+                if (r / 16 != f || c / 16 != n || !((rows >> (r % 16)) & 1)) continue;
+                v4f x = {0.f, 0.f, 0.f, 0.f};
+                for (int w = 0; w < WAVES; ++w) x += *reinterpret_cast<const v4f*>(&sums[(w * 16 + r % 16) * 20 + c % 16]);
+                store(r, c, x);
+            }
         }
     }
 #endif
@@ -717,6 +807,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
     for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+    uint32_t far_a[FM] = {}, far_b = 0;            // keep_beyond() of all steps
     // the scale bytes of a step are copied out of their set before the set is loaded again
     auto step = [&](int ks, auto set_c) __attribute__((always_inline)) {
         constexpr int S = decltype(set_c)::value;
@@ -725,8 +816,12 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(W) : "memory");
         float fa[FM];
 #pragma unroll
-        for (int f = 0; f < FM; ++f) fa[f] = scale_f32((int)sa[S][f]);
-        const float fb = scale_f32((int)sb[S]);
+        for (int f = 0; f < FM; ++f) {
+            fa[f] = scale_f32(sa[S][f]);
+            keep_beyond(far_a[f], sa[S][f]);
+        }
+        const float fb = scale_f32(sb[S]);
+        keep_beyond(far_b, sb[S]);
         issue(ks + 2, set_c);
         const uint8_t* src = smem + (ks % SLOTS) * (A_BYTES + B_BYTES);
         v8bf av[FM][4];
@@ -768,6 +863,44 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled_f32(GemmFp8Args args) {
             float out[FN];
 #pragma unroll
             for (int n = 0; n < FN; ++n) out[n] = acc[f][n][r];
+            store_columns<FN>(d + (size_t)row * args.N + col0, out, args.N - col0);
+        }
+    }
+    // rows that need add_block: all of K again, operands from memory, stored over by the lanes that stored them
+    uint64_t far[FM], any = 0;                     // bit l: row 16f + l
+#pragma unroll
+    for (int f = 0; f < FM; ++f) any |= far[f] = __ballot(max(far_a[f], far_b) > kBf16Holds);
+    if (any == 0) return;
+    static_assert(FM == 4, "");
+    for (int f = 0; f < FM; ++f) {
+        const uint64_t rows = f == 0 ? far[0] : f == 1 ? far[1] : f == 2 ? far[2] : far[3];
+        if (rows == 0) continue;
+        v4f sum[FN];
+        uint32_t b_at[FN], row_at[4];
+        const uint32_t a_at = a_row(wm * 64 + f * 16 + l) * (uint32_t)args.K + 16 * g;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row_at[r] = a_row(wm * 64 + f * 16 + 4 * g + r) * (uint32_t)args.sf_stride;
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+            sum[n] = (v4f){0.f, 0.f, 0.f, 0.f};
+            b_at[n] = (uint32_t)(min(col0 + n, args.N - 1) - nt * kBN) * (uint32_t)args.K + 16 * g;
+        }
+        for (int ks = 0; ks < nks; ++ks) {
+            uint32_t row[4];
+            const uint32_t col = __builtin_amdgcn_raw_buffer_load_b8(rs_bsf, 0, ks, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) row[r] = __builtin_amdgcn_raw_buffer_load_b8(rs_asf, row_at[r], ks, 0);
+            const v8i a = load_block(rs_a, a_at, ks);
+#pragma unroll
+            for (int n = 0; n < FN; ++n) add_block(sum[n], a, load_block(rs_b, b_at[n], ks), row, col);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = d_row(wm * 64 + f * 16 + 4 * g + r);
+            if (row < 0 || !((rows >> (4 * g + r)) & 1)) continue;
+            float out[FN];
+#pragma unroll
+            for (int n = 0; n < FN; ++n) out[n] = sum[n][r];
             store_columns<FN>(d + (size_t)row * args.N + col0, out, args.N - col0);
         }
     }

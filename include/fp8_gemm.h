@@ -14,6 +14,10 @@
  * (byte j of a row = block j along K; bytes past K/128 are ignored). D is bf16 (the FP32 sum
  * rounded once to nearest even) or FP32, as d_type (MOE_BF16, MOE_F32 of moe_serving.h) says.
  *
+ * Every scale byte from 0 to 254 counts as written (255: NaN). With FP32 outputs, rows for which
+ * one of A's or B's bytes lies outside 3 .. 246 are multiplied a second time in a slower way; their
+ * tiles take a few times as long. The other rows' bits do not depend on it.
+ *
  * Shapes: K a positive multiple of 128, at most 2^22; N any number from 1 to 2^30; G (groups) in
  * [1, MOE_MAX_EXPERTS]; the rows of A times K below 2^32 (MOE_ERR_TOKENS); fewer than 2^24 tiles
  * of 128 x 256 in D, counting one part tile per group (MOE_ERR_SHAPE); B of any size.
