@@ -24,6 +24,8 @@
 //           padding rows of perm set to -1, invalid-id total
 //   scatter one workgroup per chunk: the stable rank of each slot among the chunk's
 //           slots of the same expert (wave ballots), then perm / inv
+#include <algorithm>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -410,8 +412,10 @@ __global__ __launch_bounds__(256) void gather_kernel(const uint8_t* __restrict__
 // clamp(masked_m[g], 0, max_m) rows, ceil(c_g / BM) tiles), then writes perm for its share
 // of padded rows: A row g * max_m + i, or -1 on padding. Workgroup 0 also writes the tile
 // list and meta[0].
-// (one row a thread: 6144 rows of 12 groups 3.3 us; 16 rows a thread 5.0)
-constexpr int kLayoutRows = 1024;
+// One row a thread and pass, at most two workgroups per CU. In us by workgroups of 16384 rows, of 1024, and these:
+// 12 groups, 6144 rows of capacity 4.1, 3.1, 3.1; 256 groups of 512, few rows used 13.0, 3.6, 3.7; 32 of 131072,
+// few used 3.6, 12.2, 3.3; 1024 of 8192, few used 17.9, 32.0, 4.6, all used 43.4, 59.6, 44.6 (256 workgroups 58.2).
+constexpr int kLayoutGroups = 512;
 
 __device__ inline int upper_group(const int* off, int G, int v) {
     // largest g in [0, G) with off[g] <= v
@@ -447,12 +451,11 @@ __global__ __launch_bounds__(1024) void gemm_layout_kernel(int G, int max_m,
     }
     if (tid == 0) toff[G] = total;
     __syncthreads();
-    const int rows = total * block_m;
-    const int r0 = blockIdx.x * kLayoutRows;
-    for (int p = r0 + tid; p < rows && p < r0 + kLayoutRows; p += 1024) {
-        const int t = p / block_m;
+    const uint32_t rows = (uint32_t)total * block_m;
+    for (uint32_t p = blockIdx.x * 1024 + tid; p < rows; p += gridDim.x * 1024) {
+        const int t = (int)(p / (uint32_t)block_m);
         const int g = upper_group(toff, G, t);
-        const int i = p - toff[g] * block_m;
+        const int i = (int)p - toff[g] * block_m;
         perm[p] = i < cnt[g] ? g * max_m + i : -1;
     }
     if (blockIdx.x == 0) {
@@ -605,7 +608,7 @@ hipError_t launch_gemm_layout(int G, int max_m, const int32_t* masked_m, int blo
                               int pad_rows_cap, int32_t* perm, int32_t* tile_expert,
                               int32_t* tile_row0, int32_t* meta, hipStream_t stream) {
     if (G < 1 || G > MOE_MAX_EXPERTS) return hipErrorInvalidValue;
-    const int grid = pad_rows_cap > 0 ? cdiv(pad_rows_cap, kLayoutRows) : 1;
+    const int grid = pad_rows_cap > 0 ? std::min(cdiv(pad_rows_cap, 1024), kLayoutGroups) : 1;
     gemm_layout_kernel<<<grid, 1024, 0, stream>>>(G, max_m, masked_m, block_m, perm, tile_expert,
                                                   tile_row0, meta);
     return hipGetLastError();
