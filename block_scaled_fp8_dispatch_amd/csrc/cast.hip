@@ -73,12 +73,17 @@ __global__ __launch_bounds__(kCastThreads) void cast_fp8_kernel(const uint16_t* 
 
 hipError_t launch_cast_fp8(const uint16_t* x, int rows, int cols, uint8_t* q, uint8_t* sf,
                            hipStream_t stream) {
-    const int chunks = cdiv(cols, 512);
-    const size_t n_waves = (size_t)rows * chunks;
-    if (n_waves == 0) return hipSuccess;
-    const size_t blocks = (n_waves + kCastThreads / 64 - 1) / (kCastThreads / 64);
-    cast_fp8_kernel<<<(unsigned)blocks, kCastThreads, 0, stream>>>(x, cols, chunks, q, sf,
-                                                                  4 * chunks, n_waves);
+    const int chunks = cols / 512 + (cols % 512 != 0);
+    // in launches of at most 2^31 threads: from 2^32 on a launch wraps without an error
+    const int most = (1 << 25) / chunks;                 // (chunks < 2^23)
+    for (int row0 = 0; row0 < rows; row0 += most) {
+        const size_t n_waves = (size_t)(rows - row0 < most ? rows - row0 : most) * chunks;
+        const size_t blocks = (n_waves + kCastThreads / 64 - 1) / (kCastThreads / 64);
+        cast_fp8_kernel<<<(unsigned)blocks, kCastThreads, 0, stream>>>(x + (size_t)row0 * cols, cols, chunks,
+                                                                      q + (size_t)row0 * cols,
+                                                                      sf + (size_t)row0 * 4 * chunks, 4 * chunks, n_waves);
+        if (rows - row0 <= most) break;                  // (row0 + most may pass 2^31)
+    }
     return hipGetLastError();
 }
 
