@@ -46,12 +46,15 @@ __device__ inline int l2_row(int f, int lane, int nt) {
     return nt * 256 + 128 * (f >> 3) + 8 * (lane & 15) + (f & 7);
 }
 
+// Threads of one launch: from 2^32 on a launch wraps without an error. The kernels take the first index of theirs.
+constexpr size_t kPackThreads = size_t(1) << 31;
+
 // One thread per 16-byte chunk of packed data.
 __global__ __launch_bounds__(256) void pack_data_kernel(
-    const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, size_t n_chunks,
+    size_t first, const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, size_t n_chunks,
     int rows_per_expert, int src_row_bytes, int nks, int n_tiles, int l1_gate_up, int I) {
     // rows at or past rows_per_expert (the zero padding of a last partial tile) are zeros
-    const size_t idx = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+    const size_t idx = first + blockIdx.x * (size_t)blockDim.x + threadIdx.x;
     if (idx >= n_chunks) return;
     const int lane = (int)(idx & 63);
     const int f = (int)((idx >> 6) & 15);
@@ -72,9 +75,9 @@ __global__ __launch_bounds__(256) void pack_data_kernel(
 
 // One thread per 32-bit scale word.
 __global__ __launch_bounds__(256) void pack_scale_kernel(
-    const uint8_t* __restrict__ src_sf, uint32_t* __restrict__ dst, size_t n_words,
+    size_t first, const uint8_t* __restrict__ src_sf, uint32_t* __restrict__ dst, size_t n_words,
     int rows_per_expert, int sf_row_bytes, int nks, int nkb, int n_tiles, int l1_gate_up, int I) {
-    const size_t idx = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+    const size_t idx = first + blockIdx.x * (size_t)blockDim.x + threadIdx.x;
     if (idx >= n_words) return;
     const int lane = (int)(idx & 63);
     const int f = (int)((idx >> 6) & 15);
@@ -95,6 +98,15 @@ __global__ __launch_bounds__(256) void pack_scale_kernel(
         if (ks < nks) w |= (uint32_t)s[ks * 4 + (lane >> 4)] << (8 * b);
     }
     dst[idx] = w;
+}
+
+template <class... P, class... A>
+void launch_each(void (*kernel)(size_t, P...), size_t n, hipStream_t stream, A... args) {
+    constexpr unsigned T = 256;
+    for (size_t first = 0; first < n; first += kPackThreads) {
+        const size_t m = n - first < kPackThreads ? n - first : kPackThreads;
+        kernel<<<(unsigned)((m + T - 1) / T), T, 0, stream>>>(first, args...);
+    }
 }
 
 }  // namespace
@@ -127,24 +139,19 @@ hipError_t launch_pack(const moe_shape_t& s, const PackedLayout& L, const uint8_
     const int E = s.num_experts, H = s.hidden, I = s.intermediate;
     const int nks1 = H / 128, nkb1 = cdiv(H, 512), nb1 = I / 128;
     const int nks2 = I / 128, nkb2 = cdiv(I, 512), nt2 = cdiv(H, 256);
-    const int T = 256;
     {
         const size_t n = (size_t)E * nb1 * nks1 * 1024;
-        pack_data_kernel<<<(unsigned)((n + T - 1) / T), T, 0, stream>>>(
-            w1, packed + L.w1d, n, 2 * I, H / 2, nks1, nb1, 1, I);
+        launch_each(pack_data_kernel, n, stream, w1, packed + L.w1d, n, 2 * I, H / 2, nks1, nb1, 1, I);
         const size_t m = (size_t)E * nb1 * nkb1 * 1024;
-        pack_scale_kernel<<<(unsigned)((m + T - 1) / T), T, 0, stream>>>(
-            w1_sf, reinterpret_cast<uint32_t*>(packed + L.w1s), m, 2 * I, H / 32, nks1, nkb1, nb1,
-            1, I);
+        launch_each(pack_scale_kernel, m, stream, w1_sf, reinterpret_cast<uint32_t*>(packed + L.w1s), m, 2 * I, H / 32, nks1, nkb1, nb1,
+                    1, I);
     }
     {
         const size_t n = (size_t)E * nt2 * nks2 * 1024;
-        pack_data_kernel<<<(unsigned)((n + T - 1) / T), T, 0, stream>>>(
-            w2, packed + L.w2d, n, H, I / 2, nks2, nt2, 0, I);
+        launch_each(pack_data_kernel, n, stream, w2, packed + L.w2d, n, H, I / 2, nks2, nt2, 0, I);
         const size_t m = (size_t)E * nt2 * nkb2 * 1024;
-        pack_scale_kernel<<<(unsigned)((m + T - 1) / T), T, 0, stream>>>(
-            w2_sf, reinterpret_cast<uint32_t*>(packed + L.w2s), m, H, I / 32, nks2, nkb2, nt2, 0,
-            I);
+        launch_each(pack_scale_kernel, m, stream, w2_sf, reinterpret_cast<uint32_t*>(packed + L.w2s), m, H, I / 32, nks2, nkb2, nt2, 0,
+                    I);
     }
     return hipGetLastError();
 }
@@ -167,13 +174,10 @@ PackedBLayout packed_b_layout(int G, int N, int K) {
 hipError_t launch_pack_b(int G, int N, int K, const PackedBLayout& L, const uint8_t* b,
                          const uint8_t* b_sf, uint8_t* packed, hipStream_t stream) {
     const int nks = K / 128, nkb = cdiv(K, 512), nt = L.n_tiles;
-    const int T = 256;
     const size_t n = (size_t)G * nt * nks * 1024;
-    pack_data_kernel<<<(unsigned)((n + T - 1) / T), T, 0, stream>>>(b, packed + L.data, n, N, K / 2,
-                                                                     nks, nt, 0, 0);
+    launch_each(pack_data_kernel, n, stream, b, packed + L.data, n, N, K / 2, nks, nt, 0, 0);
     const size_t m = (size_t)G * nt * nkb * 1024;
-    pack_scale_kernel<<<(unsigned)((m + T - 1) / T), T, 0, stream>>>(
-        b_sf, reinterpret_cast<uint32_t*>(packed + L.scales), m, N, K / 32, nks, nkb, nt, 0, 0);
+    launch_each(pack_scale_kernel, m, stream, b_sf, reinterpret_cast<uint32_t*>(packed + L.scales), m, N, K / 32, nks, nkb, nt, 0, 0);
     return hipGetLastError();
 }
 
