@@ -4,8 +4,9 @@
 // sum over K stays in the FP32 accumulators. That instruction adds the products of 8
 // consecutive K after aligning them to the largest of the 8 and drops what lies more than 13
 // bits below it (measured on gfx950: 2^16 + 270 within 8 gives 2^16 + 264; across groups of 8 the
-// sum is FP32's), about 1.5e-5 of the result's norm on normal data: far below a bf16 output's
-// rounding (1.7e-3), but not FP32. FP32 outputs therefore go through v_mfma_f32_16x16x32_bf16,
+// sum is FP32's). That is about 1.5e-5 of the result's norm on normal data, 5e-5 on codes of every
+// magnitude alike, at most 2^-10 of the sum over the groups of max|a| max|b|: far below a bf16
+// output's rounding (1.7e-3) unless products cancel, but not FP32. FP32 outputs therefore go through v_mfma_f32_16x16x32_bf16,
 // at half its rate, whose sums are FP32's: an e4m3 value times its block's power of two is exact
 // in bf16 (3 mantissa bits of 7, the exponent range of FP32) for scale bytes 3 to 246. Rows with a
 // byte outside, their own or their columns', are computed again from the codes alone, both
@@ -28,7 +29,7 @@
 //
 // Bound by the matrix units at the clock that the power limit leaves: 2.4 to 2.7 PFLOP/s in full
 // rounds of 256 x 256 tiles (4096 x 4096 x 7168: 90 to 102 us on different cards; a library product
-// with one scale per tensor reaches 2.66 at 4096 x 7168 x 18432). 64-row tiles that stream B once
+// with one scale per tensor reaches 2.62 to 2.66 at 4096 x 7168 x 18432, these kernels 2.5). 64-row tiles that stream B once
 // (32 groups of about 32 rows, 4096 x 7168 each) run at 5.9 TB/s.
 #include <algorithm>
 #include <cmath>
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_tiled(GemmFp8Args args) {
 // 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where
 // those are no more than the CUs, else of 128 rows, so that more of them work, and each starts when a CU
 // is through with the rounds before (as launches of their own the parts wait for the last of these
-// workgroups: 8192 rows in 8 groups, 4096 x 7168: XXX us).
+// workgroups: 3 to 5 us of 260 more at 8192 rows in 8 groups, 4096 x 7168).
 template <bool WIDE>
 __global__ __launch_bounds__(256, 1) void gemm_fp8_rounds(GemmFp8Args args) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[160 * 1024];
@@ -724,7 +725,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp8_rounds(GemmFp8Args args) {
 // three steps. Each step converts its operands to bf16 (exact) and feeds
 // v_mfma_f32_16x16x32_bf16. One barrier per step: behind it the loads of two steps ahead go into
 // the slot that every wave has finished reading. Bound by the conversions (192 per wave and step
-// beside 128 MFMAs): 900 TFLOP/s at 4096 x 4096 x 7168; accumulators kept in place by asm and
+// beside 128 MFMAs): 224 us, 1.07 PFLOP/s at 4096 x 4096 x 7168, 124 us at 32768 x 256 x 7168; accumulators kept in place by asm and
 // conversions placed between the MFMAs by hand measured 6 % slower.
 constexpr int kF32Rows = 128;
 

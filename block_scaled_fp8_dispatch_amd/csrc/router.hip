@@ -17,8 +17,8 @@
 // router_wave_kernel (k > 16): one wave per token, lane l holding experts l, 64 + l, ...: k rounds
 // of the wave's largest key and the lowest expert that holds it.
 //
-// 32768 x 256 FP32 logits, top-8: 12.0 us (2.8 TB/s of logits; a copy of the kernel that only loads them
-// takes 7.2), bound by the vector instructions of the key sorts and of the rounds. 128 x 256: 5.2 us,
+// 32768 x 256 FP32 logits, top-8: 12.0 us a call among others (2.8 TB/s of logits; a copy of the kernel that only
+// loads them takes 7.2), 12.9 where calls follow one another in a graph, bound by the vector instructions of the key sorts and of the rounds. 128 x 256: 5.2 us,
 // a launch and one chain of dependent rounds. One wave per token takes 22 us for the first.
 #include <algorithm>
 

@@ -57,6 +57,9 @@ size_t moe_few_workspace_bytes(const moe_shape_t* shape);
  * Linear1 with SwiGLU and the FP8 requantisation, then Linear2 with the weighted sum over the
  * token's experts; the weights of the chosen experts are read once each, whatever their number
  * of tokens.
+ * Both products run on the FP8 matrix unit, as moe_forward's: FP32 sums of groups of 8 consecutive
+ * K, within which what lies more than 13 bits below the largest product is dropped (fp8_gemm.h
+ * gives the bound).
  * The result differs from moe_forward's by rounding only: the sum over a token's experts runs
  * in FP32 in ascending expert order (moe_forward rounds each slot's output to bf16 first), and
  * a token that names an expert in several slots has their weights added up. Slots whose id is
