@@ -13,7 +13,9 @@
  *   SwiGLU    -> h = silu(gate) * up, requantised to FP8 e4m3 with one UE8M0 scale per
  *                1x128 (the smallest power of two that brings the block amax to <= 448,
  *                elements rounded to nearest even)
- *   Linear2   -> FP8 h x FP4 W2 [H, I], FP32 accumulation
+ *   Linear2   -> FP8 h x FP4 W2 [H, I], FP32 accumulation (both on the FP8 matrix unit:
+ *                within each 8 consecutive K it drops what lies more than 13 bits below
+ *                the largest product)
  *   combine   -> y[t] = bf16( sum over slots j = 0..k-1 of topk_weights[t,j] * o[t,j] )
  *
  * Formats (chenxutan.com/d/1930 sections 4.1-4.2; zevenfang.github.io section 4):
