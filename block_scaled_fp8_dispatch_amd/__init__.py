@@ -16,7 +16,9 @@ from ._lib import (EXPORTED, LIB_PATH, MOE_ERR_ALIGN, MOE_ERR_HIP, MOE_ERR_NULL,
                    moe_cast_to_fp8, gemm_call_raw, MOE_BF16, MOE_F32, MOE_FEW_MAX_TOKENS,
                    MOE_ROUTER_SOFTMAX_ALL, MOE_ROUTER_SOFTMAX_CHOSEN, moe_topk_router,
                    moe_few_workspace_bytes, moe_forward_few, moe_fp8_gemm_workspace_bytes, moe_fp8_gemm,
-                   moe_m_grouped_fp8_gemm_contiguous, moe_m_grouped_fp8_gemm_masked)
+                   moe_m_grouped_fp8_gemm_contiguous, moe_m_grouped_fp8_gemm_masked, moe_rmsnorm_to_fp8,
+                   moe_cast_to_fp4, moe_cast_from_fp4, moe_fp4_gemm_workspace_bytes, moe_fp4_gemm,
+                   moe_m_grouped_fp4_gemm_contiguous, moe_m_grouped_fp4_gemm_masked)
 
 __all__ = ["EXPORTED", "LIB_PATH", "MOE_OK", "MOE_ERR_NULL", "MOE_ERR_SHAPE", "MOE_ERR_ALIGN",
            "MOE_ERR_WORKSPACE", "MOE_ERR_TOKENS", "MOE_ERR_HIP", "MOE_ERR_SCRATCH",
@@ -31,4 +33,6 @@ __all__ = ["EXPORTED", "LIB_PATH", "MOE_OK", "MOE_ERR_NULL", "MOE_ERR_SHAPE", "M
            "MOE_BF16", "MOE_F32", "MOE_FEW_MAX_TOKENS", "MOE_ROUTER_SOFTMAX_ALL",
            "MOE_ROUTER_SOFTMAX_CHOSEN", "moe_topk_router", "moe_few_workspace_bytes", "moe_forward_few",
            "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_m_grouped_fp8_gemm_contiguous",
-           "moe_m_grouped_fp8_gemm_masked"]
+           "moe_m_grouped_fp8_gemm_masked", "moe_rmsnorm_to_fp8", "moe_cast_to_fp4", "moe_cast_from_fp4",
+           "moe_fp4_gemm_workspace_bytes", "moe_fp4_gemm", "moe_m_grouped_fp4_gemm_contiguous",
+           "moe_m_grouped_fp4_gemm_masked"]

@@ -1,5 +1,5 @@
 """ctypes binding of libmoe.so (the C ABI declared in include/moe.h, include/moe_serving.h,
-include/fp8_fp4_gemm.h and include/fp8_gemm.h).
+include/fp8_fp4_gemm.h, include/fp8_gemm.h and include/fp4_gemm.h).
 
 Argument marshalling only: every function passes device pointers, sizes and a HIP
 stream to the library and raises MoEError on a non-zero status. Tensors are torch
@@ -39,7 +39,9 @@ EXPORTED = ("moe_packed_weights_bytes", "moe_prepare_weights", "moe_workspace_by
             "moe_m_grouped_fp8_fp4_gemm_masked", "moe_cast_to_fp8",
             "moe_topk_router", "moe_few_workspace_bytes", "moe_forward_few",
             "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_m_grouped_fp8_gemm_contiguous",
-            "moe_m_grouped_fp8_gemm_masked")
+            "moe_m_grouped_fp8_gemm_masked", "moe_rmsnorm_to_fp8", "moe_cast_to_fp4", "moe_cast_from_fp4",
+            "moe_fp4_gemm_workspace_bytes", "moe_fp4_gemm", "moe_m_grouped_fp4_gemm_contiguous",
+            "moe_m_grouped_fp4_gemm_masked")
 
 
 class MoEError(RuntimeError):
@@ -128,6 +130,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_m_grouped_fp8_gemm_contiguous.restype = ctypes.c_int
     lib.moe_m_grouped_fp8_gemm_masked.argtypes = [P, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, S, P]
     lib.moe_m_grouped_fp8_gemm_masked.restype = ctypes.c_int
+    lib.moe_rmsnorm_to_fp8.argtypes = [P, P, P, P, P, P, P, I32, I32, I32, F32, P]
+    lib.moe_rmsnorm_to_fp8.restype = ctypes.c_int
+    lib.moe_cast_to_fp4.argtypes = [P, I32, I32, I32, P, P, P]
+    lib.moe_cast_to_fp4.restype = ctypes.c_int
+    lib.moe_cast_from_fp4.argtypes = [P, P, I32, I32, P, I32, P]
+    lib.moe_cast_from_fp4.restype = ctypes.c_int
+    lib.moe_fp4_gemm_workspace_bytes.argtypes = [I32, I32]
+    lib.moe_fp4_gemm_workspace_bytes.restype = S
+    lib.moe_fp4_gemm.argtypes = [P, I32, P, P, I32, I32, I32, P, P, S, P]
+    lib.moe_fp4_gemm.restype = ctypes.c_int
+    lib.moe_m_grouped_fp4_gemm_contiguous.argtypes = [P, I32, P, P, P, I32, I32, I32, I32, P, P, S, P]
+    lib.moe_m_grouped_fp4_gemm_contiguous.restype = ctypes.c_int
+    lib.moe_m_grouped_fp4_gemm_masked.argtypes = [P, I32, P, P, P, I32, I32, I32, I32, I32, P, P, S, P]
+    lib.moe_m_grouped_fp4_gemm_masked.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -382,3 +398,54 @@ def moe_m_grouped_fp8_gemm_masked(d, d_type: int, a, a_sf, masked_m, groups: int
         _ptr(d), int(d_type), _ptr(a), _ptr(a_sf), _ptr(masked_m), int(groups), int(max_m), int(expected_m), int(n),
         int(k), _ptr(b), _ptr(b_sf), _ptr(workspace), _nbytes(workspace), _stream(stream)),
         "moe_m_grouped_fp8_gemm_masked")
+
+
+# ---------------------------------------------------------------------------
+# Norm with FP8 output (include/moe_serving.h)
+# ---------------------------------------------------------------------------
+
+
+def moe_rmsnorm_to_fp8(x_fp8, x_sf, normed, residual_out, x, residual, weight, weight_type: int, rows: int, cols: int,
+                       eps: float, stream=None) -> None:
+    """normed, residual_out and residual may be None."""
+    _check(load_library().moe_rmsnorm_to_fp8(_ptr(x_fp8), _ptr(x_sf), _ptr(normed), _ptr(residual_out), _ptr(x), _ptr(residual),
+                                             _ptr(weight), int(weight_type), int(rows), int(cols), float(eps),
+                                             _stream(stream)), "moe_rmsnorm_to_fp8")
+
+
+# ---------------------------------------------------------------------------
+# FP4 casts and FP4 x FP4 GEMMs (include/fp4_gemm.h)
+# ---------------------------------------------------------------------------
+
+
+def moe_cast_to_fp4(x, x_type: int, rows: int, cols: int, x_fp4, x_sf, stream=None) -> None:
+    _check(load_library().moe_cast_to_fp4(_ptr(x), int(x_type), int(rows), int(cols), _ptr(x_fp4), _ptr(x_sf),
+                                          _stream(stream)), "moe_cast_to_fp4")
+
+
+def moe_cast_from_fp4(x_fp4, x_sf, rows: int, cols: int, x, x_type: int, stream=None) -> None:
+    _check(load_library().moe_cast_from_fp4(_ptr(x_fp4), _ptr(x_sf), int(rows), int(cols), _ptr(x), int(x_type),
+                                            _stream(stream)), "moe_cast_from_fp4")
+
+
+def moe_fp4_gemm_workspace_bytes(max_rows: int, groups: int) -> int:
+    return load_library().moe_fp4_gemm_workspace_bytes(int(max_rows), int(groups))
+
+
+def moe_fp4_gemm(d, d_type: int, a, a_sf, m: int, n: int, k: int, packed_b, workspace, stream=None) -> None:
+    _check(load_library().moe_fp4_gemm(_ptr(d), int(d_type), _ptr(a), _ptr(a_sf), int(m), int(n), int(k), _ptr(packed_b),
+                                       _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_fp4_gemm")
+
+
+def moe_m_grouped_fp4_gemm_contiguous(d, d_type: int, a, a_sf, group_of_row, m: int, groups: int, n: int, k: int, packed_b,
+                                      workspace, stream=None) -> None:
+    _check(load_library().moe_m_grouped_fp4_gemm_contiguous(
+        _ptr(d), int(d_type), _ptr(a), _ptr(a_sf), _ptr(group_of_row), int(m), int(groups), int(n), int(k), _ptr(packed_b),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_m_grouped_fp4_gemm_contiguous")
+
+
+def moe_m_grouped_fp4_gemm_masked(d, d_type: int, a, a_sf, masked_m, groups: int, max_m: int, expected_m: int, n: int, k: int,
+                                  packed_b, workspace, stream=None) -> None:
+    _check(load_library().moe_m_grouped_fp4_gemm_masked(
+        _ptr(d), int(d_type), _ptr(a), _ptr(a_sf), _ptr(masked_m), int(groups), int(max_m), int(expected_m), int(n), int(k),
+        _ptr(packed_b), _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_m_grouped_fp4_gemm_masked")

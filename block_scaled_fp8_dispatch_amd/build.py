@@ -16,8 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["moe_api.hip", "gemm_api.hip", "serving_api.hip", "route.hip", "pack.hip", "gemm.hip", "gemm_fp8.hip", "few.hip",
-           "router.hip", "combine.hip", "cast.hip"]
+SOURCES = ["moe_api.hip", "gemm_api.hip", "serving_api.hip", "route.hip", "pack.hip", "gemm.hip", "gemm_fp8.hip", "gemm_fp4.hip",
+           "few.hip", "router.hip", "norm.hip", "combine.hip", "cast.hip", "cast_fp4.hip"]
 ARCH = "gfx950"
 
 

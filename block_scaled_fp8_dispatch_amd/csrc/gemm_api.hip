@@ -1,9 +1,10 @@
-// C ABI of the plain FP8 x FP4 GEMMs and the FP8 cast (include/fp8_fp4_gemm.h) and of the
-// FP8 x FP8 GEMMs (include/fp8_gemm.h): argument checks, workspace layout, and the launches. Host code only; the kernels are the grouped
+// C ABI of the plain FP8 x FP4 GEMMs and the FP8 cast (include/fp8_fp4_gemm.h), of the
+// FP8 x FP8 GEMMs (include/fp8_gemm.h) and of the FP4 x FP4 GEMMs and the FP4 casts (include/fp4_gemm.h): argument checks, workspace layout, and the launches. Host code only; the kernels are the grouped
 // GEMM of gemm.hip in its plain mode (dense: rows and tiles derived in the kernel, K split
 // over several workgroups when the output has few tiles), the routing kernels of route.hip
 // (contiguous layout: rows grouped by their group id, stable in row order, each group padded
 // to the row-tile size), the layout kernel of route.hip (masked layout), and cast.hip.
+#include "fp4_gemm.h"
 #include "fp8_fp4_gemm.h"
 #include "fp8_gemm.h"
 #include "moe_internal.h"
@@ -171,6 +172,58 @@ GemmFp8Args fp8_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf,
     g.d = d;
     g.out_f32 = d_type == MOE_F32;
     return g;
+}
+
+// Row and tile lists of a contiguous GEMM: one launch where one workgroup can hold all ids (FP8 x FP8, 8192 rows: 273 -> 248
+// us for the whole call)
+hipError_t group_rows(const int32_t* group_of_row, int m, int groups, int BM, uint8_t* ws, const GemmWs& W, hipStream_t stream) {
+    auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+    if (m <= kGroupMaxRows)
+        return launch_group_rows(group_of_row, m, groups, BM, i32(W.perm), i32(W.meta), i32(W.tile_expert), i32(W.tile_row0),
+                                 stream);
+    return launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets), i32(W.perm),
+                        i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream);
+}
+
+// FP4 x FP4: B packed as the FP8 x FP4 GEMMs', K and N bounded as the FP8 x FP8 ones'
+bool fp4_shape_ok(int G, int N, int K, int d_type) {
+    return gemm_shape_ok(G, N, K) && K <= kFp8MaxK && N <= kFp8MaxN && (d_type == MOE_BF16 || d_type == MOE_F32);
+}
+
+GemmFp4Args fp4_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int G, int N, int K, const void* packed_b,
+                     uint8_t* ws, const GemmWs& W, int block_m, int tiles_bound) {
+    const PackedBLayout L = packed_b_layout(G, N, K);
+    const uint8_t* pk = static_cast<const uint8_t*>(packed_b);
+    GemmFp4Args g{};
+    g.block_m = block_m;
+    g.a = a;
+    g.a_sf = a_sf;
+    g.b = pk + L.data;
+    g.b_sf = pk + L.scales;
+    g.b_group = L.d_group;
+    g.b_ntile = L.d_ntile;
+    g.bs_group = L.s_group;
+    g.bs_ntile = L.s_ntile;
+    g.K = K;
+    g.N = N;
+    g.dense_rows = 0;
+    g.perm = reinterpret_cast<const int32_t*>(ws + W.perm);
+    g.meta = reinterpret_cast<const int32_t*>(ws + W.meta);
+    g.tile_expert = reinterpret_cast<const int32_t*>(ws + W.tile_expert);
+    g.tile_row0 = reinterpret_cast<const int32_t*>(ws + W.tile_row0);
+    g.max_tiles = tiles_bound < W.max_tiles ? tiles_bound : W.max_tiles;
+    g.d = d;
+    g.out_f32 = d_type == MOE_F32;
+    return g;
+}
+
+// The FP4 casts' arguments
+int fp4_cast_check(const void* x, int x_type, int rows, int cols, const void* q, const void* sf) {
+    if (!x || !q || !sf) return MOE_ERR_NULL;
+    if (cols < 32 || cols % 32 != 0 || (x_type != MOE_BF16 && x_type != MOE_F32)) return MOE_ERR_SHAPE;
+    if (rows < 0) return MOE_ERR_TOKENS;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(sf)) return MOE_ERR_ALIGN;
+    return MOE_OK;
 }
 
 }  // namespace
@@ -343,15 +396,7 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Fp8Plan plan = fp8_plan(groups, (double)m / groups, m, true, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
-    auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-    // one launch where one workgroup can hold all ids (8192 rows: 273 -> 248 us for the whole call)
-    const hipError_t grouped =
-        m <= kGroupMaxRows
-            ? launch_group_rows(group_of_row, m, groups, BM, i32(W.perm), i32(W.meta), i32(W.tile_expert),
-                                i32(W.tile_row0), stream)
-            : launch_route(group_of_row, m, groups, BM, i32(W.blk), i32(W.meta), i32(W.counts), i32(W.offsets),
-                           i32(W.perm), i32(W.inv), i32(W.tile_expert), i32(W.tile_row0), W.max_tiles, stream);
-    if (grouped != hipSuccess) return MOE_ERR_HIP;
+    if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
     const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, cdiv(m, BM) + groups);
     return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -382,6 +427,83 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
         return MOE_ERR_HIP;
     const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, groups * cdiv(max_m, BM));
     return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_cast_to_fp4(const void* x, int32_t x_type, int32_t rows, int32_t cols, uint8_t* x_fp4, uint8_t* x_sf,
+                    hipStream_t stream) {
+    const int bad = fp4_cast_check(x, x_type, rows, cols, x_fp4, x_sf);
+    if (bad != MOE_OK || rows == 0) return bad;
+    return launch_cast_to_fp4(x, x_type, rows, cols, x_fp4, x_sf, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_cast_from_fp4(const uint8_t* x_fp4, const uint8_t* x_sf, int32_t rows, int32_t cols, void* x, int32_t x_type,
+                      hipStream_t stream) {
+    const int bad = fp4_cast_check(x, x_type, rows, cols, x_fp4, x_sf);
+    if (bad != MOE_OK || rows == 0) return bad;
+    return launch_cast_from_fp4(x_fp4, x_sf, rows, cols, x, x_type, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+size_t moe_fp4_gemm_workspace_bytes(int32_t max_rows, int32_t groups) { return moe_fp8_gemm_workspace_bytes(max_rows, groups); }
+
+int moe_fp4_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, int32_t m, int32_t n, int32_t k,
+                 const void* packed_b, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!d || !a || !a_sf || !packed_b || !workspace) return MOE_ERR_NULL;
+    if (!fp4_shape_ok(1, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(packed_b) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+    if (!rows_ok(m, 1, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(m, 1, n)) return MOE_ERR_SHAPE;
+    const GemmWs W = gemm_ws(m, 1);
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
+    if (m == 0) return MOE_OK;
+    const int BM = 64;
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, 1, n, k, packed_b, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
+    g.dense_rows = m;
+    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
+                                      const int32_t* group_of_row, int32_t m, int32_t groups, int32_t n, int32_t k,
+                                      const void* packed_b, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!d || !a || !a_sf || !group_of_row || !packed_b || !workspace) return MOE_ERR_NULL;
+    if (!fp4_shape_ok(groups, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(group_of_row) || !aligned16(packed_b) ||
+        !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (!rows_ok(m, groups, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(m, groups, n)) return MOE_ERR_SHAPE;
+    const GemmWs W = gemm_ws(m, groups);
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
+    if (m == 0) return MOE_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int BM = 64;
+    if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
+    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, groups, n, k, packed_b, ws, W, BM, cdiv(m, BM) + groups);
+    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, const int32_t* masked_m,
+                                  int32_t groups, int32_t max_m, int32_t expected_m, int32_t n, int32_t k,
+                                  const void* packed_b, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!d || !a || !a_sf || !masked_m || !packed_b || !workspace) return MOE_ERR_NULL;
+    if (!fp4_shape_ok(groups, n, k, d_type)) return MOE_ERR_SHAPE;
+    if (!aligned16(d) || !aligned16(a) || !aligned16(a_sf) || !aligned16(masked_m) || !aligned16(packed_b) ||
+        !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (max_m < 0) return MOE_ERR_TOKENS;
+    const long long rows = (long long)groups * max_m;
+    if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
+    if (!fp8_grid_ok(rows, groups, n)) return MOE_ERR_SHAPE;
+    const GemmWs W = gemm_ws((int)rows, groups);
+    if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
+    if (max_m == 0) return MOE_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int BM = 64;
+    if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
+                           reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
+                           reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
+        return MOE_ERR_HIP;
+    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, groups, n, k, packed_b, ws, W, BM, groups * cdiv(max_m, BM));
+    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

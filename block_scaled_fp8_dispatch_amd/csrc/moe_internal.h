@@ -211,6 +211,37 @@ struct Fp8Plan {
 Fp8Plan fp8_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K, bool out_f32);
 hipError_t launch_gemm_fp8(const Fp8Plan& plan, const GemmFp8Args& a, hipStream_t stream);
 
+// FP4 casts (cast_fp4.hip); x_type: MOE_BF16 or MOE_F32
+hipError_t launch_cast_to_fp4(const void* x, int x_type, int rows, int cols, uint8_t* q, uint8_t* sf, hipStream_t stream);
+hipError_t launch_cast_from_fp4(const uint8_t* q, const uint8_t* sf, int rows, int cols, void* x, int x_type,
+                                hipStream_t stream);
+
+// FP4 x FP4 GEMM with 32-block scales (gemm_fp4.hip)
+struct GemmFp4Args {
+    const uint8_t* a;          // E2M1 rows of K/2 bytes
+    const uint8_t* a_sf;       // rows of K/32 UE8M0 bytes
+    const uint8_t* b;          // packed B data and scales (PackedBLayout; bytes)
+    const uint8_t* b_sf;
+    size_t b_group, b_ntile, bs_group, bs_ntile;
+    int K, N;
+    // Row tiles of block_m rows: dense_rows > 0: rows 0 .. dense_rows-1; otherwise the lists of
+    // the routing (perm: A and D row of each padded row, -1 padding)
+    int block_m;
+    int dense_rows;
+    const int32_t* perm;
+    const int32_t* meta;
+    const int32_t* tile_expert;
+    const int32_t* tile_row0;
+    int max_tiles;
+    void* d;
+    int out_f32;
+};
+hipError_t launch_gemm_fp4(const GemmFp4Args& a, hipStream_t stream);
+
+// Root-mean-square norm with FP8 output (norm.hip)
+hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int weight_type, int rows, int cols,
+                          float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream);
+
 // Combine (combine.hip)
 hipError_t launch_combine(const uint16_t* stage, const int32_t* topk_idx, const float* topk_weights,
                           int T, int k, int E, int H, uint16_t* y, hipStream_t stream);

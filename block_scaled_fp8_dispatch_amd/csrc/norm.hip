@@ -1,0 +1,231 @@
+// Root-mean-square norm of bf16 rows, with the residual's addition in front and the FP8 cast behind (the cast:
+// chenxutan.com/d/1930 section 9.2, the activation as FP8 codes and scale factors before the MoE call; section 11.1, a
+// block's scale follows its largest magnitude):
+//
+//   h = x + residual;  r = 1 / sqrt(mean(h^2) + eps);  n = h * r * weight
+//
+// residual_out = bf16(h), normed = bf16(n); codes and scales are moe_cast_to_fp8's rule applied to n. Everything between is
+// FP32: n is not rounded to bf16 before the cast.
+//
+// A workgroup owns a row and keeps it in registers: 8 columns per lane and chunk, so that the 16 lanes of a DPP row hold one
+// 128-column block.
+#include "moe_internal.h"
+#include "moe_serving.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
+// sum over the workgroup, in every thread, in a fixed order
+__device__ inline float block_sum(float s, float* part) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+    __syncthreads();                                   // `part` may still be read from the sum before
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = part[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += part[w];
+    return s;
+}
+
+__device__ inline void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+
+__device__ inline uint4 pack8(const float (&f)[8]) {
+    typedef float v8f __attribute__((ext_vector_type(8)));
+    typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+    const v8f v = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+    return __builtin_bit_cast(uint4, __builtin_convertvector(v, v8bf));
+}
+
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* residual;      // or null
+    const void* weight;
+    uint8_t* q;
+    uint8_t* sf;
+    uint16_t* normed;              // or null
+    uint16_t* residual_out;        // or null
+    int cols, sf_stride;
+    float eps;
+};
+
+// h of the 8 columns at c of a row that starts at `at`
+__device__ inline void load_h(const NormArgs& p, size_t at, int c, float (&h)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(p.x + at + c), h);
+    if (p.residual) {
+        float r[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.residual + at + c), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] += r[j];
+    }
+}
+
+template <bool WF32>
+__device__ inline void load_w(const NormArgs& p, int c, float (&w)[8]) {
+    if constexpr (WF32) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + c);
+        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + c + 4);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + c), w);
+    }
+}
+
+// UE8M0 byte of a block whose largest magnitude has FP32 bit pattern `bits` (sign clear): 448 = 1.75 * 2^8
+__device__ inline uint32_t fp8_scale_byte(uint32_t bits) {
+    if (bits == 0) return 127u;
+    if (bits >= 0x7f800000u) return 255u;              // an infinity or a NaN in the block
+    const int b = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return b < 0 ? 0u : (uint32_t)b;
+}
+
+__device__ inline uint32_t max_of_16(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
+}
+
+// n of 8 columns -> normed, codes, and (every 16th lane) the block's scale byte. c < sf_stride * 128; past cols: zeros
+__device__ inline void store_n(const NormArgs& p, size_t row, int c, const float (&n)[8]) {
+    const bool active = c < p.cols;
+    const size_t at = row * p.cols + c;
+    if (active && p.normed) *reinterpret_cast<uint4*>(p.normed + at) = pack8(n);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(n[j]) & 0x7fffffffu);
+    const uint32_t byte = fp8_scale_byte(max_of_16(m));
+    // 2^-(byte - 127); NaN for a block of NaN, so that its codes are NaN too
+    const float mul = byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - byte) << 23);
+    if (active) {
+        int a = __builtin_amdgcn_cvt_pk_fp8_f32(n[0] * mul, n[1] * mul, 0, false);
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(n[2] * mul, n[3] * mul, a, true);
+        int b = __builtin_amdgcn_cvt_pk_fp8_f32(n[4] * mul, n[5] * mul, 0, false);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(n[6] * mul, n[7] * mul, b, true);
+        *reinterpret_cast<uint2*>(p.q + at) = make_uint2((uint32_t)a, (uint32_t)b);
+    }
+    if ((threadIdx.x & 15) == 0 && (c >> 7) < p.sf_stride) p.sf[row * p.sf_stride + (c >> 7)] = active ? (uint8_t)byte : (uint8_t)0;
+}
+
+// Squares leave FP32's range where |h| passes 2^64 or, with a tiny eps, where all of the row is below about 2^-63. Such rows
+// are scaled by a power of two before they are squared. `f`: that power, or 1
+__device__ inline float square_scale(float sum, float eps) {
+    if (!(sum <= 3.4028235e38f)) return 0x1p-80f;
+    return sum < 0x1p-100f && eps < 0x1p-80f ? 0x1p80f : 1.0f;
+}
+
+__device__ inline float inverse_root(float sum, float cols, float eps, float f) {
+    return 1.0f / __builtin_sqrtf(sum / cols + eps * f * f);
+}
+
+// CH chunks of 2048 columns held in registers (CH = 0: any number, read again from memory for each pass)
+template <int CH, bool WF32>
+__global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormArgs p, int row0) {
+    __shared__ float part[kWaves];
+    const size_t row = (size_t)row0 + blockIdx.x, at = row * p.cols;
+    const int t8 = threadIdx.x * 8;
+    const float cols = (float)p.cols;
+    if constexpr (CH > 0) {
+        float h[CH][8], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = k * (8 * kThreads) + t8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
+            if (c < p.cols) load_h(p, at, c, h[k]);
+        }
+        float f = 1.0f;
+        auto squares = [&]() __attribute__((always_inline)) {
+            float q = 0.f;
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q += (h[k][j] * f) * (h[k][j] * f);
+            return block_sum(q, part);
+        };
+        s = squares();
+        f = square_scale(s, p.eps);
+        if (f != 1.0f) s = squares();
+        const float r = inverse_root(s, cols, p.eps, f);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = k * (8 * kThreads) + t8;
+            float n[8] = {};
+            if (c < p.cols) {
+                if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + at + c) = pack8(h[k]);
+                float w[8];
+                load_w<WF32>(p, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) n[j] = (h[k][j] * f) * r * w[j];
+            }
+            store_n(p, row, c, n);
+        }
+    } else {
+        const int end = (p.cols + 511) / 512 * 512;     // whole waves
+        float f = 1.0f;
+        auto squares = [&]() {
+            float q = 0.f;
+            for (int c = t8; c < p.cols; c += 8 * kThreads) {
+                float h[8];
+                load_h(p, at, c, h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q += (h[j] * f) * (h[j] * f);
+            }
+            return block_sum(q, part);
+        };
+        float s = squares();
+        f = square_scale(s, p.eps);
+        if (f != 1.0f) s = squares();
+        const float r = inverse_root(s, cols, p.eps, f);
+        for (int c = t8; c < end; c += 8 * kThreads) {
+            float h[8], n[8] = {};
+            if (c < p.cols) {
+                load_h(p, at, c, h);
+                // (the lane has read these columns of both inputs: either may be residual_out)
+                if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + at + c) = pack8(h);
+                float w[8];
+                load_w<WF32>(p, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) n[j] = (h[j] * f) * r * w[j];
+            }
+            store_n(p, row, c, n);
+        }
+    }
+}
+
+template <int CH>
+void launch(const NormArgs& p, bool wf32, int row0, unsigned rows, hipStream_t stream) {
+    if (wf32) rmsnorm_kernel<CH, true><<<rows, kThreads, 0, stream>>>(p, row0);
+    else rmsnorm_kernel<CH, false><<<rows, kThreads, 0, stream>>>(p, row0);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int weight_type, int rows, int cols,
+                          float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
+    NormArgs p{x, residual, weight, q, sf, normed, residual_out, cols, 4 * cdiv(cols, 512), eps};
+    const bool wf32 = weight_type == MOE_F32;
+    constexpr int kMost = 1 << 23;                      // rows of a launch: at most 2^31 threads
+    for (int row0 = 0; row0 < rows; row0 += kMost) {
+        const unsigned n = (unsigned)(rows - row0 < kMost ? rows - row0 : kMost);
+        const int chunks = cdiv(cols, 8 * kThreads);
+        if (chunks <= 1) launch<1>(p, wf32, row0, n, stream);
+        else if (chunks <= 2) launch<2>(p, wf32, row0, n, stream);
+        else if (chunks <= 4) launch<4>(p, wf32, row0, n, stream);
+        else if (chunks <= 8) launch<8>(p, wf32, row0, n, stream);
+        else launch<0>(p, wf32, row0, n, stream);
+        if (rows - row0 <= kMost) break;                // (row0 + kMost may pass 2^31)
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

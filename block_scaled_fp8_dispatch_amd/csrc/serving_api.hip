@@ -1,4 +1,4 @@
-// C ABI of the router and of the few-token forward (include/moe_serving.h): argument checks
+// C ABI of the router, of the norm with FP8 output and of the few-token forward (include/moe_serving.h): argument checks
 // and launches. Host code only.
 #include <cmath>
 
@@ -31,6 +31,22 @@ int moe_topk_router(int32_t* topk_idx, float* topk_weights, const void* logits, 
     if (launch_router(logits, logits_type, num_tokens, num_experts, num_topk,
                       softmax_over == MOE_ROUTER_SOFTMAX_ALL, weight_scale, topk_idx, topk_weights,
                       stream) != hipSuccess)
+        return MOE_ERR_HIP;
+    return MOE_OK;
+}
+
+int moe_rmsnorm_to_fp8(uint8_t* x_fp8, uint8_t* x_sf, uint16_t* normed, uint16_t* residual_out, const uint16_t* x,
+                       const uint16_t* residual, const void* weight, int32_t weight_type, int32_t rows, int32_t cols, float eps,
+                       hipStream_t stream) {
+    if (!x_fp8 || !x_sf || !x || !weight) return MOE_ERR_NULL;
+    if (cols < 128 || cols % 128 != 0 || (weight_type != MOE_BF16 && weight_type != MOE_F32)) return MOE_ERR_SHAPE;
+    if (!std::isfinite(eps) || eps <= 0.0f) return MOE_ERR_SHAPE;
+    if (rows < 0) return MOE_ERR_TOKENS;
+    if (!aligned16(x_fp8) || !aligned16(x_sf) || !aligned16(normed) || !aligned16(residual_out) || !aligned16(x) ||
+        !aligned16(residual) || !aligned16(weight))
+        return MOE_ERR_ALIGN;
+    if (rows == 0) return MOE_OK;
+    if (launch_rmsnorm(x, residual, weight, weight_type, rows, cols, eps, x_fp8, x_sf, normed, residual_out, stream) != hipSuccess)
         return MOE_ERR_HIP;
     return MOE_OK;
 }

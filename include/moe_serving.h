@@ -5,6 +5,9 @@
  *                     (chenxutan.com/d/1930 section 9.2: top-k, then softmax over the chosen
  *                     logits)
  *   moe_forward_few   moe_forward for at most MOE_FEW_MAX_TOKENS tokens, in two kernels
+ *   moe_rmsnorm_to_fp8  the norm in front of the layer, with the residual's addition, straight
+ *                     into the x_fp8 / x_sf that the forward and the GEMMs read (section 9.2:
+ *                     the activation is cast before the MoE call)
  *
  * Formats, memory, errors and streams as in moe.h: device pointers, 16-byte aligned, owned by
  * the caller (the library allocates nothing); host-detectable problems return a negative
@@ -43,6 +46,26 @@ int moe_topk_router(int32_t* topk_idx, float* topk_weights, const void* logits,
                     int32_t logits_type, int32_t num_tokens, int32_t num_experts,
                     int32_t num_topk, int32_t softmax_over, float weight_scale,
                     hipStream_t stream);
+
+/* Root-mean-square norm with FP8 output. For each row, in FP32 from bf16 inputs:
+ *   h = x + residual (x alone without one);  r = 1 / sqrt(mean(h^2) + eps);  n = h * r * weight
+ *   x_fp8         u8  [rows, cols] out, x_sf u8 [rows, 4*ceil(cols/512)] out: n as
+ *                 moe_cast_to_fp8 writes it (n is not rounded to bf16 before); a block of n that
+ *                 holds an infinity or a NaN gets the scale byte 255 and NaN codes
+ *   normed        bf16 [rows, cols] out: n, or NULL
+ *   residual_out  bf16 [rows, cols] out: h, or NULL. It may be x or residual itself; outputs
+ *                 and inputs overlap in no other way
+ *   x, residual   bf16 [rows, cols]; residual may be NULL
+ *   weight        [cols] of weight_type (MOE_BF16 or MOE_F32)
+ * Rows whose squares leave FP32's range are scaled before they are squared: every finite row
+ * gets its norm. An infinity in a row makes its other columns 0 and its own block NaN, a NaN
+ * makes the whole row NaN; other rows do not change. cols is a positive multiple of 128 and eps
+ * finite and above 0, else MOE_ERR_SHAPE (also for an unknown weight_type); rows < 0 is
+ * MOE_ERR_TOKENS; rows = 0 launches nothing. Results do not depend on scheduling. */
+int moe_rmsnorm_to_fp8(uint8_t* x_fp8, uint8_t* x_sf, uint16_t* normed, uint16_t* residual_out,
+                       const uint16_t* x, const uint16_t* residual, const void* weight,
+                       int32_t weight_type, int32_t rows, int32_t cols, float eps,
+                       hipStream_t stream);
 
 /* Most tokens of one moe_forward_few call. */
 #define MOE_FEW_MAX_TOKENS 32
