@@ -190,11 +190,12 @@ bool fp4_shape_ok(int G, int N, int K, int d_type) {
     return gemm_shape_ok(G, N, K) && K <= kFp8MaxK && N <= kFp8MaxN && (d_type == MOE_BF16 || d_type == MOE_F32);
 }
 
-GemmFp4Args fp4_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int G, int N, int K, const void* packed_b,
+GemmFp4Args fp4_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int rows, int G, int N, int K, const void* packed_b,
                      uint8_t* ws, const GemmWs& W, int block_m, int tiles_bound) {
     const PackedBLayout L = packed_b_layout(G, N, K);
     const uint8_t* pk = static_cast<const uint8_t*>(packed_b);
     GemmFp4Args g{};
+    g.rows = (uint32_t)rows;
     g.block_m = block_m;
     g.a = a;
     g.a_sf = a_sf;
@@ -455,10 +456,11 @@ int moe_fp4_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     const GemmWs W = gemm_ws(m, 1);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
-    const int BM = 64;
-    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, 1, n, k, packed_b, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
+    const Fp4Plan plan = fp4_plan(1, m, m, false, n, k);
+    const int BM = plan.block_m;
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, 1, n, k, packed_b, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
     g.dense_rows = m;
-    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
@@ -475,10 +477,11 @@ int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = 64;
+    const Fp4Plan plan = fp4_plan(groups, (double)m / groups, m, true, n, k);
+    const int BM = plan.block_m;
     if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
-    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, groups, n, k, packed_b, ws, W, BM, cdiv(m, BM) + groups);
-    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, ws, W, BM, cdiv(m, BM) + groups);
+    return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf, const int32_t* masked_m,
@@ -497,13 +500,15 @@ int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int BM = 64;
+    const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;
+    const Fp4Plan plan = fp4_plan(groups, rows_each, (int)rows, true, n, k);
+    const int BM = plan.block_m;
     if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
                            reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
                            reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
         return MOE_ERR_HIP;
-    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, groups, n, k, packed_b, ws, W, BM, groups * cdiv(max_m, BM));
-    return launch_gemm_fp4(g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, (int)rows, groups, n, k, packed_b, ws, W, BM, groups * cdiv(max_m, BM));
+    return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

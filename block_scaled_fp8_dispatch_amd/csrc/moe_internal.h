@@ -224,6 +224,7 @@ struct GemmFp4Args {
     const uint8_t* b_sf;
     size_t b_group, b_ntile, bs_group, bs_ntile;
     int K, N;
+    uint32_t rows;             // of A: nothing is read past them
     // Row tiles of block_m rows: dense_rows > 0: rows 0 .. dense_rows-1; otherwise the lists of
     // the routing (perm: A and D row of each padded row, -1 padding)
     int block_m;
@@ -236,7 +237,15 @@ struct GemmFp4Args {
     void* d;
     int out_f32;
 };
-hipError_t launch_gemm_fp4(const GemmFp4Args& a, hipStream_t stream);
+enum class Fp4Kernel { kTiled256, kTiled128, kSkinny64 };
+// The kernel for groups of about rows_per_group rows (ragged: known on the device only; at most max_rows in all) and the
+// height of its row tiles
+struct Fp4Plan {
+    Fp4Kernel kernel;
+    int block_m;
+};
+Fp4Plan fp4_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K);
+hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_t stream);
 
 // Root-mean-square norm with FP8 output (norm.hip)
 hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int weight_type, int rows, int cols,
