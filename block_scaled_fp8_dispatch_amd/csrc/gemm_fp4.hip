@@ -7,10 +7,13 @@
 // B is packed (pack.hip): a 16-column x 128-K fragment is one 1 KB read in lane order, its scales one 32-bit word per lane
 // and four K steps. A is read as it is: a lane's 16 bytes of a K step, and its scale byte.
 //
-// Skinny kernel. A workgroup owns a tile of BM rows x FN fragments and its 8 waves share K, wave w taking the pairs of K
-// steps w, w + 8, ... with sums of its own, which meet in LDS at the end. Operands go from memory straight into the
-// registers of the wave that multiplies them: 16 bytes a lane are a whole operand, and the two steps of a pair use whole
-// 128-byte lines of A's rows.
+// Skinny kernel. Operands go from memory straight into the registers of the wave that multiplies them: 16 bytes a lane are a
+// whole operand, and the two K steps of a pair use whole 128-byte lines of A's rows. A workgroup owns a tile of BM rows x FN
+// fragments of columns, and its WAVES waves share K, taking a pair in turn and keeping sums of their own, which meet in LDS at
+// the end. A wave keeps DEPTH pairs in flight.
+#include <algorithm>
+#include <cmath>
+
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -38,27 +41,30 @@ __device__ inline int xcd_tile(int total, unsigned block) {
     return xcd * per + (xcd < rem ? xcd : rem) + li;
 }
 
-constexpr int kSkinnyWaves = 8;
+template <int N>
+struct IntC {
+    static constexpr int value = N;
+};
 
-template <int FM, int FN, bool F32>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp4_skinny(GemmFp4Args p) {
+// NT: B through non-temporal loads (one row tile reads it)
+template <int FM, int FN, int WAVES, int DEPTH, bool F32, bool NT>
+__global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 16 * FM, SUB = 64 / BM, WAVES = kSkinnyWaves, PITCH = 16 * FN + 4;
-    __shared__ __attribute__((aligned(16))) float sums[WAVES / 2 * BM * PITCH];
+    constexpr int BM = 16 * FM, SUB = 64 / BM, kBAux = NT ? 2 : 0;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l = lane & 15;
     const bool dense = p.dense_rows > 0;
     // units of BM rows: of a dense product's rows, or of the 64-row tiles in the list
     const int units = dense ? (p.dense_rows + BM - 1) / BM : min(__builtin_amdgcn_readfirstlane(p.meta[0]), p.max_tiles) * SUB;
-    // column units of FN fragments; a 128-column half tile is 8 fragments, whose columns interleave
-    const int NT = (p.N + 127) / 128 * (8 / FN);
-    const int v = xcd_tile(units * NT, blockIdx.x);
+    // column units of FN fragments; the 8 fragments of 128 columns interleave their columns
+    const int units_n = (p.N + 127) / 128 * (8 / FN);
+    const int v = xcd_tile(units * units_n, blockIdx.x);
     if (v < 0) return;
     // groups of 4 row tiles across all column units: their rows of A stay in the XCD's L2
     constexpr int kSet = kGroupM * SUB;
-    const int set = v / (kSet * NT), u0 = set * kSet, gu = min(kSet, units - u0), vin = v - set * kSet * NT;
-    const int unit = u0 + vin % gu, nt = vin / gu;
+    const int set = v / (kSet * units_n), u0 = set * kSet, gu = min(kSet, units - u0), vin = v - set * kSet * units_n;
+    const int unit = u0 + vin % gu;
     const int mt = unit / SUB;
     const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(p.tile_expert[mt]);
     const int row0 = dense ? unit * BM : __builtin_amdgcn_readfirstlane(p.tile_row0[mt]) + unit % SUB * BM;
@@ -68,94 +74,126 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp4_skinny(GemmFp4Args
     };
     // padding comes last in a row tile: nothing but padding here
     if (__builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
+    const int f0 = vin / gu * FN, tile = f0 >> 4, frag = f0 & 15;   // fragments frag .. frag + FN-1 of a 256-column tile
+    const int nks = p.K / kBK;
 
-    const int f0 = nt * FN, tile = f0 >> 4, frag = f0 & 15;      // fragments frag .. frag + FN - 1 of a 256-column tile
     uint32_t a_off[FM], sa_off[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         const int d = d_row(f * 16 + l);
         const uint32_t row = d < 0 ? 0u : (uint32_t)d;           // padding rows read row 0 and are never stored
         a_off[f] = row * (uint32_t)(p.K / 2) + 16u * g;
-        sa_off[f] = row * (uint32_t)(p.K / 32) + (uint32_t)g;
+        sa_off[f] = row * (uint32_t)(p.K / 32);
     }
     const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, (int)(p.rows * (uint32_t)(p.K / 2)), kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)p.a_sf, 0, (int)(p.rows * (uint32_t)(p.K / 32)), kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.b + (size_t)group * p.b_group + (size_t)tile * p.b_ntile + frag * kFragBytes), 0, kAllRecords, kRsrcWord3);
+        (void*)(p.b + (size_t)group * p.b_group + (size_t)tile * p.b_ntile), 0, nks * kBTileBytes, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_bsf = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.b_sf + (size_t)group * p.bs_group + (size_t)tile * p.bs_ntile + frag * 256), 0, kAllRecords, kRsrcWord3);
+        (void*)(p.b_sf + (size_t)group * p.bs_group + (size_t)tile * p.bs_ntile), 0, (nks + 3) / 4 * kBScaleBlockBytes, kRsrcWord3);
+    const uint32_t b_off = frag * kFragBytes + lane * 16, sb_off = frag * 256 + lane * 4;
 
     v4f acc[FM][FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int n = 0; n < FN; ++n) acc[f][n] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const int nks = p.K / kBK;
-    for (int k0 = 2 * wave; k0 < nks; k0 += 2 * WAVES) {
-        // step 2 of the last pair may lie past K: its loads repeat the first's and it is not multiplied
-        const bool both = k0 + 1 < nks;
+    struct Stage {
         v4i a[2][FM], b[2][FN];
-        uint32_t sa[2][FM], sb[2][FN];
+        uint32_t sa[FM], sb[FN];
+    } st[DEPTH];
+    // A's scales: lane 16g + i loads the four bytes of row i for the pair's step g % 2, takes the other step's from the lane 16
+    // away, and picks byte g of both
+    const uint32_t sel = (uint32_t)g | (uint32_t)(g + 4) << 8 | 0x0c0c0000u;
+    // Pair `i` of this wave. The second step of the last pair may lie past K: its loads repeat the first's, and its scales are 0
+    // on both sides (B's as packed), 2^-254, by which its products vanish
+    auto load = [&](Stage& s, int i) __attribute__((always_inline)) {
+        const int ks = 2 * (i * WAVES + wave);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int ks = s && both ? k0 + 1 : k0;
+        for (int h = 0; h < 2; ++h) {
+            const int at = min(ks + h, nks - 1);
 #pragma unroll
-            for (int n = 0; n < FN; ++n) {
-                b[s][n] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, lane * 16 + n * kFragBytes, ks * kBTileBytes, 0));
-                sb[s][n] = __builtin_amdgcn_raw_buffer_load_b8(rs_bsf, lane * 4 + n * 256, (ks >> 2) * kBScaleBlockBytes + (ks & 3), 0);
-            }
+            for (int n = 0; n < FN; ++n)
+                s.b[h][n] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_b, b_off + n * kFragBytes, at * kBTileBytes, kBAux));
 #pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                a[s][f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_a, a_off[f], ks * (kBK / 2), 0));
-                sa[s][f] = __builtin_amdgcn_raw_buffer_load_b8(rs_asf, sa_off[f], ks * 4, 0);
-            }
+            for (int f = 0; f < FM; ++f)
+                s.a[h][f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_a, a_off[f], at * (kBK / 2), 0));
         }
-        auto multiply = [&](int s) __attribute__((always_inline)) {
+        const uint32_t at = 4u * (uint32_t)min(ks + (g & 1), nks - 1);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) s.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[f] + at, 0, 0);
+        // both steps' bytes of a fragment lie together
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+            s.sb[n] = __builtin_amdgcn_raw_buffer_load_b16(rs_bsf, sb_off + n * 256, (ks >> 2) * kBScaleBlockBytes + (ks & 3), kBAux);
+    };
+    auto multiply = [&](const Stage& s, int i) __attribute__((always_inline)) {
+        const uint32_t keep = 2 * (i * WAVES + wave) + 1 < nks ? ~0u : 0xffu;
+        uint32_t sa[FM];
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            const auto q = __builtin_amdgcn_permlane16_swap(s.sa[f], s.sa[f], false, false);
+            sa[f] = __builtin_amdgcn_perm(q[1], q[0], sel) & keep;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
-                const v8i x = {a[s][f].x, a[s][f].y, a[s][f].z, a[s][f].w, 0, 0, 0, 0};
+                const v8i x = {s.a[h][f].x, s.a[h][f].y, s.a[h][f].z, s.a[h][f].w, 0, 0, 0, 0};
 #pragma unroll
                 for (int n = 0; n < FN; ++n) {
-                    const v8i y = {b[s][n].x, b[s][n].y, b[s][n].z, b[s][n].w, 0, 0, 0, 0};
-                    acc[f][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[f][n], kFp4, kFp4, 0, (int)sa[s][f], 0, (int)sb[s][n]);
+                    const v8i y = {s.b[h][n].x, s.b[h][n].y, s.b[h][n].z, s.b[h][n].w, 0, 0, 0, 0};
+                    acc[f][n] = h == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[f][n], kFp4, kFp4, 0, (int)sa[f], 0, (int)s.sb[n])
+                                       : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[f][n], kFp4, kFp4, 1, (int)sa[f], 1, (int)s.sb[n]);
                 }
             }
+    };
+    // n pairs of this wave: DEPTH in flight, then each multiplied and its registers loaded again while there are more
+    const int pairs = (nks + 1) >> 1, n = (pairs - wave + WAVES - 1) / WAVES;
+    if (n < DEPTH) {
+#pragma unroll
+        for (int i = 0; i < DEPTH - 1; ++i)
+            if (i < n) load(st[i], i);
+#pragma unroll
+        for (int i = 0; i < DEPTH - 1; ++i)
+            if (i < n) multiply(st[i], i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) load(st[i], i);
+        int i = 0;
+        // the last DEPTH pairs, the first of them in stage S
+        auto rest = [&](auto first) __attribute__((always_inline)) {
+            constexpr int S = decltype(first)::value;
+#pragma unroll
+            for (int j = 0; j < DEPTH; ++j) multiply(st[(S + j) % DEPTH], i + j);
         };
-        multiply(0);
-        if (both) multiply(1);
-    }
-    // sums at column 16 * fragment + lane column, row of the tile
-    auto at = [&](int w, int r, int n) __attribute__((always_inline)) -> float& { return sums[(w * BM + r) * PITCH + n]; };
-    if (wave >= WAVES / 2) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) at(wave - WAVES / 2, f * 16 + 4 * g + r, n * 16 + l) = acc[f][n][r];
-    }
-    __syncthreads();
-    if (wave < WAVES / 2) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) at(wave, f * 16 + 4 * g + r, n * 16 + l) += acc[f][n][r];
-    }
-    __syncthreads();
-    // lane column j of fragment f is column 128 * (f / 8) + 8j + f % 8 of its tile: FN adjacent columns of D per thread
-    for (int i = tid; i < BM * 16; i += WAVES * 64) {
-        const int r = i >> 4, j = i & 15;
-        const int row = d_row(r), col = tile * kBN + 128 * (frag >> 3) + 8 * j + (frag & 7);
-        if (row < 0 || col >= p.N) continue;                     // (N is a multiple of 16: all FN columns or none)
-        float x[FN];
-#pragma unroll
-        for (int n = 0; n < FN; ++n) {
-            x[n] = at(0, r, n * 16 + j);
-#pragma unroll
-            for (int w = 1; w < WAVES / 2; ++w) x[n] += at(w, r, n * 16 + j);
+        auto turn = [&](auto stage) __attribute__((always_inline)) -> bool {
+            constexpr int S = decltype(stage)::value;
+            if (i + DEPTH >= n) {
+                rest(stage);
+                return true;
+            }
+            multiply(st[S], i);
+            load(st[S], i + DEPTH);
+            ++i;
+            return false;
+        };
+        for (;;) {
+            if (turn(IntC<0>{})) break;
+            if constexpr (DEPTH > 1)
+                if (turn(IntC<1 % DEPTH>{})) break;
+            if constexpr (DEPTH > 2)
+                if (turn(IntC<2 % DEPTH>{})) break;
+            if constexpr (DEPTH > 3)
+                if (turn(IntC<3 % DEPTH>{})) break;
         }
+    }
+
+    // Row of the tile and column of D of a lane's sums: rows 16f + 4g + r, columns col .. col + FN-1 (lane column j of fragment
+    // f is column 128 * (f / 8) + 8j + f % 8 of its tile; all FN or none: N is a multiple of 16)
+    auto store = [&](int r, int col, const float (&x)[FN]) __attribute__((always_inline)) {
+        const int row = d_row(r);
+        if (row < 0 || col >= p.N) return;
         const size_t to = (size_t)row * p.N + col;
         if constexpr (F32) {
             float* d = static_cast<float*>(p.d) + to;
@@ -165,13 +203,50 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp4_skinny(GemmFp4Args
                 for (int n = 0; n < FN; ++n) d[n] = x[n];
         } else {
             uint16_t* d = static_cast<uint16_t*>(p.d) + to;
-            const v2bf lo = __builtin_convertvector(((v2f){x[0], x[FN > 1 ? 1 : 0]}), v2bf);
-            const uint32_t w0 = __builtin_bit_cast(uint32_t, lo);
+            const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x[0], x[FN > 1 ? 1 : 0]}), v2bf));
             if constexpr (FN == 1) *d = (uint16_t)w0;
             else if constexpr (FN == 2) *reinterpret_cast<uint32_t*>(d) = w0;
-            else
-                *reinterpret_cast<uint2*>(d) = make_uint2(w0, __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x[2], x[3]}), v2bf)));
+            else *reinterpret_cast<uint2*>(d) = make_uint2(w0, __builtin_bit_cast(uint32_t, __builtin_convertvector(((v2f){x[2], x[3]}), v2bf)));
         }
+    };
+    const int col0 = tile * kBN + 128 * (frag >> 3) + (frag & 7);
+    // the waves' sums as the lanes hold them, then thread t of a fragment row adds lane t / 4's row t % 4 over the waves
+    constexpr int HALF = WAVES * FM * FN > 64 ? WAVES / 2 : WAVES;    // of the waves at a time: at most 64 KB
+    __shared__ __attribute__((aligned(16))) float sums[HALF * FM * FN * 256];
+    auto at = [&](int w, int f, int n) __attribute__((always_inline)) -> float* { return sums + ((w * FM + f) * FN + n) * 256; };
+    if (HALF < WAVES) {
+        if (wave >= HALF) {
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+#pragma unroll
+                for (int n = 0; n < FN; ++n) *reinterpret_cast<v4f*>(at(wave - HALF, f, n) + lane * 4) = acc[f][n];
+        }
+        __syncthreads();
+        if (wave < HALF) {
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+#pragma unroll
+                for (int n = 0; n < FN; ++n) acc[f][n] += *reinterpret_cast<const v4f*>(at(wave, f, n) + lane * 4);
+        }
+        __syncthreads();
+    }
+    if (wave < HALF) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int n = 0; n < FN; ++n) *reinterpret_cast<v4f*>(at(wave, f, n) + lane * 4) = acc[f][n];
+    }
+    __syncthreads();
+    for (int i = tid; i < FM * 256; i += WAVES * 64) {
+        const int f = i >> 8, t = i & 255;
+        float x[FN];
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+            x[n] = at(0, f, n)[t];
+#pragma unroll
+            for (int w = 1; w < HALF; ++w) x[n] += at(w, f, n)[t];
+        }
+        store(f * 16 + 4 * (t >> 6) + (t & 3), col0 + 8 * ((t >> 2) & 15), x);
     }
 #endif
 }
@@ -194,11 +269,6 @@ __device__ inline void mfma_scaled(v4f& acc, const v4i& a, const v4i& b, uint32_
         asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
                      : "+a"(acc) : "v"(a), "v"(b), "v"(sa), "v"(sb));
 }
-
-template <int N>
-struct IntC {
-    static constexpr int value = N;
-};
 
 #define MOE_LPTR(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -229,29 +299,48 @@ struct Fp4Cfg {
     static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
     static constexpr int FM = WM / 16, FN = WN / 16;
     static constexpr int A_BYTES = BM * kARow;
-    // ring slots: 160 KB with 256 rows, 160 with 128, 128 with 64
-    static constexpr int DB = BM == 256 ? 2 : 3, DA = DB + 1;
+    // ring slots: 160 KB with 256 rows and with 128, 80 with 64 (two workgroups per CU)
+    static constexpr int DA = BM == 256 ? 3 : BM == 128 ? 4 : 2, DB = BM == 128 ? 3 : 2;
     static constexpr int LDS_BYTES = DA * A_BYTES + DB * kBStep;
     static constexpr int A_DMA = A_BYTES / 1024 / 4, B_DMA = kBStep / 1024 / 4;   // 1 KB loads per wave and step
-    static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024, "");
+    static constexpr int NS = FM + FN;                                             // scale loads per wave and two steps
+    static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024 && DA >= 2 && DB >= 2, "");
+
+    // A wave's loads go out in the order X(k), Y(k), X(k+1), ...; X(k): the next block's scale words if k is even, then B of step
+    // k+DB; Y(k): A of step k+DA. How many of them may be in flight at the second barrier of step k (`odd`: k's), when A and B of
+    // step k+1 and, in odd steps, the scale words have to be there: those behind the last one needed.
+    static constexpr int in_flight(bool odd) {
+        int n = 0;
+        for (int d = 0;; ++d) {                        // X(k-d), then Y(k-d-1)
+            const bool even = odd == (d % 2 != 0);
+            if (DB <= d + 1) return n;                 // B of step k-d+DB
+            n += B_DMA;
+            if (even && odd && d == 1) return n;       // the scale words of X(k-1)
+            if (even) n += NS;
+            if (DA <= d + 2) return n;                 // A of step k-d-1+DA
+            n += A_DMA;
+        }
+    }
 };
 
 // Part `part` (of BM rows) of tile v. Tile ids walk groups of 4 row tiles (of args.block_m rows) across all column tiles.
-template <int BM, int WAVES_M, int WAVES_N, bool F32>
+// NT: B through non-temporal loads (one row tile reads it).
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
 __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, int num_mt, int v, int part) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty function
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
     constexpr int WM = C::WM, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB, A_DMA = C::A_DMA, B_DMA = C::B_DMA;
+    constexpr int kBAux = NT ? 2 : 0;
     uint8_t* const bring = smem + DA * C::A_BYTES;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int g = lane >> 4, l = lane & 15;
     const bool dense = args.dense_rows > 0;
-    const int NT = (args.N + kBN - 1) / kBN;
-    const int grp = v / (kGroupM * NT), mt0 = grp * kGroupM;
-    const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * NT;
+    const int tiles_n = (args.N + kBN - 1) / kBN;
+    const int grp = v / (kGroupM * tiles_n), mt0 = grp * kGroupM;
+    const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * tiles_n;
     const int mt = mt0 + vin % gm, nt = vin / gm;
     const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
     const int row0 = (dense ? mt * args.block_m : __builtin_amdgcn_readfirstlane(args.tile_row0[mt])) + part * BM;
@@ -301,13 +390,13 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
         const int i = wave * B_DMA + j;       // fragment i % 16 of the step's half i / 16
         const int kc = min(2 * ks + (i >> 4), nks - 1);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, MOE_LPTR(bring + (ks % DB) * kBStep + i * 1024), 16, lane * 16,
-                                                 kc * kBTileBytes + (i & 15) * kFragBytes, 0, 0);
+                                                 kc * kBTileBytes + (i & 15) * kFragBytes, 0, kBAux);
     };
     // scale words of a block of two steps: A's as loaded, and by byte of the K step in the block as the products take them
     uint32_t raw[FM], sa[2][FM], sb[2][FN];
     auto load_scale = [&](int kb, int i, int set) __attribute__((always_inline)) {
         if (i < FM) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[i] - (kb == last_kb ? past_sf : 0u), kb * 16, 0);
-        else sb[set][i - FM] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, lane * 4 + (wn * FN + i - FM) * 256, kb * kBScaleBlockBytes, 0);
+        else sb[set][i - FM] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, lane * 4 + (wn * FN + i - FM) * 256, kb * kBScaleBlockBytes, kBAux);
     };
     // (bytes of K steps past the last: 0)
     auto scale_words = [&](int kb, int f) __attribute__((always_inline)) -> uint32_t {
@@ -337,43 +426,34 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
         }
     asm volatile("s_nop 7" ::: "memory");   // accumulator writes -> first MFMA
 
-    // A step's window of loads starts behind its barrier and ends before the next step's: B of DB steps ahead, A of DA, and
-    // after even steps the next block's scale words, which have landed at the next step's barrier (DB = 2: behind B, which
-    // has to land there as well; DB = 3: in front, so that B need not)
-    constexpr int NS = FM + FN, TILE_OPS = A_DMA + B_DMA;
-    constexpr bool kScalesFirst = DB > 2;
+    // Loads of a step: B of DB steps ahead (on even steps behind the next block's scale words) from its first barrier on, which
+    // every wave passes with B of this step in registers; A of DA steps ahead from its second barrier on, which every wave
+    // passes with A of this step read
+    constexpr int NS = C::NS;
     constexpr int ROW = 2 * FN;             // MFMAs per fragment row
-    constexpr int SPACE = (FM - 1) * ROW / (NS + TILE_OPS) > 3 ? 3 : (FM - 1) * ROW / (NS + TILE_OPS);   // MFMAs per load
-    static_assert(SPACE >= 1, "a step's loads fit between its barriers");
-    auto issue = [&](int kp, bool scales, int set, int op) __attribute__((always_inline)) {
+    constexpr int X_ROOM = (FM - 2) * ROW, X_SPACE = X_ROOM / (NS + B_DMA) > 3 ? 3 : X_ROOM / (NS + B_DMA);   // MFMAs per load
+    constexpr int Y_SPACE = ROW / A_DMA;
+    static_assert(X_SPACE >= 1 && Y_SPACE >= 1, "a step's loads fit between its barriers");
+    auto issue_x = [&](int ks, bool scales, int set, int op) __attribute__((always_inline)) {
         const int ns = scales ? NS : 0;
-        const int s0 = kScalesFirst ? 0 : B_DMA;
-        if (op >= s0 && op < s0 + ns) {
-            load_scale(min((kp >> 1) + 1, last_kb), op - s0, set);
-            return;
-        }
-        if (op >= s0 + ns) op -= ns;
-        if (op < B_DMA) load_b(kp + DB, op);
-        else if (op < TILE_OPS) load_a(kp + DA, op - B_DMA);
+        if (op < ns) load_scale(min((ks >> 1) + 1, last_kb), op, set);
+        else if (op < ns + B_DMA) load_b(ks + DB, op - ns);
     };
     // the loads that the steps before step 0 would have issued
 #pragma unroll
     for (int i = 0; i < NS; ++i) load_scale(0, i, 0);
 #pragma unroll
-    for (int j = 0; j < A_DMA; ++j) load_a(0, j);
+    for (int k = DA > DB ? -DA : -DB; k < 0; ++k) {
 #pragma unroll
-    for (int s = 0; s < DB - 1; ++s) {
+        for (int j = 0; j < B_DMA; ++j)
+            if (k + DB >= 0) load_b(k + DB, j);
 #pragma unroll
-        for (int j = 0; j < B_DMA; ++j) load_b(s, j);
-#pragma unroll
-        for (int j = 0; j < A_DMA; ++j) load_a(s + 1, j);
+        for (int j = 0; j < A_DMA; ++j)
+            if (k + DA >= 0) load_a(k + DA, j);
     }
-    // of the step before step 0 only what goes out in its last row; step 0 issues the rest
-    constexpr int EARLY = (ROW + SPACE - 1) / SPACE < TILE_OPS ? (ROW + SPACE - 1) / SPACE : TILE_OPS;
-#pragma unroll
-    for (int op = 0; op < EARLY; ++op) issue(-1, false, 0, op);
     // everything after A and B of step 0
-    constexpr int WAIT0 = EARLY + A_DMA + (DB - 2) * TILE_OPS;
+    constexpr int WAIT0 = DA > DB ? (DB - 1) * B_DMA + DB * A_DMA : (DB - 1) * (B_DMA + A_DMA);
+    static_assert(DA == DB || DA == DB + 1, "order of the first loads");
     static_assert(WAIT0 < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt(0x0F70 | (WAIT0 & 15) | (((WAIT0 >> 4) & 3) << 14));
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(WAIT0) : "memory");
@@ -390,16 +470,18 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(sa[0][f]));
     asm volatile("s_nop 1" ::: "memory");   // scale words -> first MFMA
 
-    // One step: 256 of K, FM rows of 2 x FN MFMAs. Its barrier stands before the last row: this wave's loads of step ks+1 have
-    // landed, its LDS reads of step ks are done. Behind it each B fragment's registers take the next step's right after their
-    // last use, and the step's window of loads begins.
+    // One step: 256 of K, FM rows of 2 x FN MFMAs. Its first barrier stands behind the first row, where every wave holds B of the
+    // step in registers. At the second, before the last row, this wave's loads of step ks+1 have landed and its LDS reads of A
+    // are done; behind it each B fragment's registers take the next step's right after their last use.
     auto step = [&](int ks, auto odd_c, auto set_c) __attribute__((always_inline)) {
         constexpr int ODD = decltype(odd_c)::value, SET = decltype(set_c)::value;
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
+            if (fm == 1) asm volatile("s_barrier" ::: "memory");
             if (fm == FM - 1) {
                 // in flight may be what was issued behind B of step ks+1 and (odd steps) the scale words
-                constexpr int WN_ = DB == 2 ? A_DMA : ODD ? TILE_OPS : A_DMA + TILE_OPS;
+                constexpr int WN_ = C::in_flight(ODD);
+                static_assert(WN_ < 64, "vmcnt range");
                 __builtin_amdgcn_s_waitcnt(0x0070 | (WN_ & 15) | (((WN_ >> 4) & 3) << 14));
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
                 if constexpr (ODD) {
@@ -425,9 +507,9 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                             sa[SET ^ 1][t / (ROW / FM)] = scale_words((ks >> 1) + 1, t / (ROW / FM));
                             asm volatile("" : "+v"(sa[SET ^ 1][t / (ROW / FM)]));
                         }
-                        if (t % SPACE == 0) issue(ks, !ODD, SET ^ 1, t / SPACE);
-                    } else if ((ROW + fm * ROW + t) % SPACE == 0) {
-                        issue(ks - 1, ODD, SET ^ 1, (ROW + fm * ROW + t) / SPACE);
+                        if (t % Y_SPACE == 0 && t / Y_SPACE < A_DMA) load_a(ks + DA, t / Y_SPACE);
+                    } else if (fm > 0 && ((fm - 1) * ROW + t) % X_SPACE == 0) {
+                        issue_x(ks, !ODD, SET ^ 1, ((fm - 1) * ROW + t) / X_SPACE);
                     }
                     __builtin_amdgcn_sched_barrier(0x7);
                 }
@@ -494,14 +576,14 @@ __device__ inline int row_tiles(const GemmFp4Args& args, int bm) {
     return min(n, args.max_tiles);
 }
 
-template <int BM, int WAVES_M, int WAVES_N, bool F32>
-__global__ __launch_bounds__(256, 1) void gemm_fp4_tiled(GemmFp4Args args) {
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
+__global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void gemm_fp4_tiled(GemmFp4Args args) {
     using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     const int num_mt = row_tiles(args, BM);
     const int v = xcd_tile(num_mt * ((args.N + kBN - 1) / kBN), blockIdx.x);
     if (v < 0) return;
-    tiled_part<BM, WAVES_M, WAVES_N, F32>(args, smem, num_mt, v, 0);
+    tiled_part<BM, WAVES_M, WAVES_N, F32, NT>(args, smem, num_mt, v, 0);
 }
 
 // 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where those are no more than
@@ -512,28 +594,104 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rounds(GemmFp4Args args) {
     const int num_mt = row_tiles(args, 256), total = num_mt * ((args.N + kBN - 1) / kBN);
     const int rem = total % kCus, full = rem <= kCus / 2 ? total - rem : total;
     if ((int)blockIdx.x < full) {
-        tiled_part<256, 2, 2, F32>(args, smem, num_mt, xcd_tile(full, blockIdx.x), 0);
+        tiled_part<256, 2, 2, F32, false>(args, smem, num_mt, xcd_tile(full, blockIdx.x), 0);
         return;
     }
     const int parts = rem <= kCus / 4 ? 4 : 2;
     const int u = xcd_tile((total - full) * parts, blockIdx.x - full);
     if (u < 0) return;
-    if (parts == 4) tiled_part<64, 1, 4, F32>(args, smem, num_mt, full + u / 4, u % 4);
-    else tiled_part<128, 2, 2, F32>(args, smem, num_mt, full + u / 2, u % 2);
+    if (parts == 4) tiled_part<64, 1, 4, F32, false>(args, smem, num_mt, full + u / 4, u % 4);
+    else tiled_part<128, 2, 2, F32, false>(args, smem, num_mt, full + u / 2, u % 2);
 }
 
-template <int FM, int FN>
-hipError_t launch_skinny(const GemmFp4Args& a, hipStream_t stream) {
-    const size_t units = a.dense_rows > 0 ? cdiv(a.dense_rows, 16 * FM) : (size_t)a.max_tiles * (4 / FM);
-    const size_t tiles = units * (size_t)(cdiv(a.N, 128) * (8 / FN));
-    if (tiles >= (size_t(1) << 32) / (kSkinnyWaves * 64)) return hipErrorInvalidConfiguration;   // a launch wraps there
-    const unsigned grid = (unsigned)tiles;
-    if (a.out_f32) gemm_fp4_skinny<FM, FN, true><<<grid, kSkinnyWaves * 64, 0, stream>>>(a);
-    else gemm_fp4_skinny<FM, FN, false><<<grid, kSkinnyWaves * 64, 0, stream>>>(a);
+template <int BM, int WAVES_M, int WAVES_N>
+hipError_t launch_tiled(unsigned grid, bool nt, const GemmFp4Args& a, hipStream_t stream) {
+    if (a.out_f32) {
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, true><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, false><<<grid, 256, 0, stream>>>(a);
+    } else {
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, true><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, false><<<grid, 256, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
+template <int FM, int FN, int WAVES, int DEPTH>
+hipError_t launch_skinny(bool nt, const GemmFp4Args& a, hipStream_t stream) {
+    const size_t units = a.dense_rows > 0 ? cdiv(a.dense_rows, 16 * FM) : (size_t)a.max_tiles * (4 / FM);
+    const size_t tiles = units * (size_t)(cdiv(a.N, 128) * (8 / FN));
+    constexpr int T = WAVES * 64;
+    if (tiles >= (size_t(1) << 32) / T) return hipErrorInvalidConfiguration;   // a launch wraps there
+    const unsigned grid = (unsigned)tiles;
+    if (a.out_f32) {
+        if (nt) gemm_fp4_skinny<FM, FN, WAVES, DEPTH, true, true><<<grid, T, 0, stream>>>(a);
+        else gemm_fp4_skinny<FM, FN, WAVES, DEPTH, true, false><<<grid, T, 0, stream>>>(a);
+    } else {
+        if (nt) gemm_fp4_skinny<FM, FN, WAVES, DEPTH, false, true><<<grid, T, 0, stream>>>(a);
+        else gemm_fp4_skinny<FM, FN, WAVES, DEPTH, false, false><<<grid, T, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+// Microseconds of a product with each kernel. Tiled: rounds of the workgroups that the CUs hold, each fixed + step per 128 K
+// (64 rows: two on a CU, a last round of one on a CU takes 0.63 of it). Skinny: fixed + wave per pair of K steps that a wave
+// takes + for every 256 workgroups tile + step per 128 K. Fitted to 73 products from 1 x 256 x 512 to 7698 x 2704 x 3200 and 18
+// groups of about 25 rows, each timed with every kernel, weights from memory: what the model picks is 2 % slower than the
+// best of the kernels on average, 44 % at most (982 x 576 x 3584).
+// A list's 64-row tiles with few rows leave most workgroups of 16 or 32 rows without any and the others to a part of the CUs,
+// so that there all count.
+struct Cost {
+    Fp4Kernel kernel;
+    int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
+    int waves;                 // sharing K; 0: tiled
+    double fixed, step, wave, tile;
+};
+constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 6.8, 0.60, 0, 0},
+                           {Fp4Kernel::kTiled128, 128, 128, 256, 0, 7.6, 0.53, 0, 0},
+                           {Fp4Kernel::kTiled64, 64, 64, 256, 0, 9.2, 0.68, 0, 0},
+                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 2.12, 0.173, 1.64, 3.13},
+                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 1.73, 0.099, 1.26, 1.94},
+                           {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 1.45, 0.115, 1.54, 1.89},
+                           {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.44, 0.062, 1.23, 0.89},
+                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.50, 0.047, 0.95, 0.65},
+                           {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 1.79, 0.037, 1.10, 0.69}};
+constexpr double kAlone64 = 0.63;
+
 }  // namespace
+
+Fp4Plan fp4_plan(int groups, double rows, int max_rows, bool ragged, int N, int K) {
+    Fp4Plan best{};
+    double least = 0;
+    const int steps = K / kBK;
+    for (const Cost& c : kCosts) {
+        const int cols = c.waves ? cdiv(N, 128) * (128 / c.bn) : cdiv(N, kBN);
+        // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
+        const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cols;
+        if (c.kernel != Fp4Kernel::kTiled128 && grid * (c.waves ? c.waves * 64 : 256) >= (1ull << 32)) continue;
+        // groups of unknown length end in a tile that is half full on average
+        double mt = groups * (!ragged ? std::ceil(rows / c.bm) : rows > c.bm ? rows / c.bm + 0.5 : 1.0);
+        if (ragged && c.bm < 64) mt = groups * std::max(1.0, rows / 64 + 0.5) * (64 / c.bm);
+        const double tiles = std::ceil(mt) * cols;
+        double t = 0;
+        if (c.waves) {
+            t = c.fixed + c.wave * cdiv(cdiv(steps, 2), c.waves) + tiles / kCus * (c.tile + c.step * steps);
+        } else {
+            const double round = c.fixed + c.step * steps, slots = c.kernel == Fp4Kernel::kTiled64 ? 2 * kCus : kCus;
+            const double rounds = std::floor(tiles / slots), rem = tiles - rounds * slots;
+            t = rounds * round;
+            // the parts of the 256-row tiles' last round: of 64 rows, kCosts[2], or 128, kCosts[1]
+            if (c.kernel == Fp4Kernel::kTiled256 && rem > 0 && rem <= kCus / 4) t += kCosts[2].fixed + kCosts[2].step * steps;
+            else if (c.kernel == Fp4Kernel::kTiled256 && rem > 0 && rem <= kCus / 2) t += kCosts[1].fixed + kCosts[1].step * steps;
+            else if (c.kernel == Fp4Kernel::kTiled64 && rem > 0 && rem <= kCus) t += kAlone64 * round;
+            else if (rem > 0) t += round;
+        }
+        if (best.block_m == 0 || t < least) {
+            best = Fp4Plan{c.kernel, c.block_m, rows <= c.block_m};
+            least = t;
+        }
+    }
+    return best;
+}
 
 hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_t stream) {
     const size_t mt = a.dense_rows > 0 ? cdiv(a.dense_rows, plan.block_m) : a.max_tiles;
@@ -547,19 +705,16 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
             else gemm_fp4_rounds<false><<<blocks, 256, 0, stream>>>(a);
             break;
         }
-        case Fp4Kernel::kTiled128:
-            if (a.out_f32) gemm_fp4_tiled<128, 2, 2, true><<<(unsigned)grid, 256, 0, stream>>>(a);
-            else gemm_fp4_tiled<128, 2, 2, false><<<(unsigned)grid, 256, 0, stream>>>(a);
-            break;
-        case Fp4Kernel::kSkinny64: return launch_skinny<4, 4>(a, stream);
+        case Fp4Kernel::kTiled128: return launch_tiled<128, 2, 2>((unsigned)grid, plan.stream, a, stream);
+        case Fp4Kernel::kTiled64: return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
+        case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny64x32: return launch_skinny<4, 2, 8, 1>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 2>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 2>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny16x32: return launch_skinny<1, 2, 8, 3>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny16: return launch_skinny<1, 1, 16, 2>(plan.stream, a, stream);
     }
     return hipGetLastError();
-}
-
-Fp4Plan fp4_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K) {
-    if (rows_per_group > 256) return {Fp4Kernel::kTiled256, 256};
-    if (rows_per_group > 64) return {Fp4Kernel::kTiled128, 128};
-    return {Fp4Kernel::kSkinny64, 64};
 }
 
 }  // namespace moe
