@@ -293,37 +293,46 @@ __device__ inline uint32_t transpose_bytes(uint32_t x, const ByteSelect& sel) {
 constexpr int kStep = 2 * kBK;
 constexpr int kARow = kStep / 2;
 constexpr int kBStep = 2 * kBTileBytes;
+// Bytes of a chunk (4 steps) of a row's scales
+constexpr int kChunkRow = 4 * kStep / 32;
 
 template <int BM, int WAVES_M, int WAVES_N>
 struct Fp4Cfg {
     static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
     static constexpr int FM = WM / 16, FN = WN / 16;
     static constexpr int A_BYTES = BM * kARow;
-    // ring slots: 160 KB with 256 rows and with 128, 80 with 64 (two workgroups per CU)
-    static constexpr int DA = BM == 256 ? 3 : BM == 128 ? 4 : 2, DB = BM == 128 ? 3 : 2;
-    static constexpr int LDS_BYTES = DA * A_BYTES + DB * kBStep;
+    // A's scale words through LDS, where there is room (64 rows: two workgroups share the CU's)
+    static constexpr bool STAGED = BM >= 128;
+    static constexpr int S_BYTES = STAGED ? BM * kChunkRow : 0;
+    // ring slots: 144 KB with 256 rows, 152 with 128, 80 with 64
+    static constexpr int DA = BM == 128 ? 3 : 2, DB = BM == 128 ? 3 : 2;
+    static constexpr int LDS_BYTES = DA * A_BYTES + DB * kBStep + 2 * S_BYTES;
     static constexpr int A_DMA = A_BYTES / 1024 / 4, B_DMA = kBStep / 1024 / 4;   // 1 KB loads per wave and step
-    static constexpr int NS = FM + FN;                                             // scale loads per wave and two steps
+    static constexpr int S_DMA = S_BYTES / 256 / 4;                                // 256-byte loads per wave and chunk
     static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024 && DA >= 2 && DB >= 2, "");
 
-    // A wave's loads go out in the order X(k), Y(k), X(k+1), ...; X(k): the next block's scale words if k is even, then B of step
-    // k+DB; Y(k): A of step k+DA. How many of them may be in flight at the second barrier of step k (`odd`: k's), when A and B of
-    // step k+1 and, in odd steps, the scale words have to be there: those behind the last one needed.
-    static constexpr int in_flight(bool odd) {
+    // A wave's loads go out in the order X(k), Y(k), X(k+1), ...; X(k): scale words, then B of step k+DB; Y(k): A of step k+DA.
+    // Scale words of X(k), u = k % 4: A's of the next chunk in steps 0, 1 and, with DB = 2, 2 (into LDS), or in even steps of the
+    // next block (into registers); B's of the next block in even steps
+    static constexpr int S_STEPS = DB == 2 ? 3 : 2;                                 // so that they are there in step 3
+    static constexpr int S_EACH = (S_DMA + S_STEPS - 1) / S_STEPS;
+    static constexpr int staged(int u) { return u >= S_STEPS ? 0 : u == S_STEPS - 1 ? S_DMA - u * S_EACH : S_EACH; }
+    static constexpr int scales(int u) { return staged(u) + (u % 2 ? 0 : FN + (STAGED ? 0 : FM)); }
+    // How many loads may be in flight at the second barrier of step k, when A and B of step k+1 and, in odd steps, the scale words
+    // of X(k-1) have to be there: those behind the last one needed.
+    static constexpr int in_flight(int u) {
         int n = 0;
         for (int d = 0;; ++d) {                        // X(k-d), then Y(k-d-1)
-            const bool even = odd == (d % 2 != 0);
             if (DB <= d + 1) return n;                 // B of step k-d+DB
             n += B_DMA;
-            if (even && odd && d == 1) return n;       // the scale words of X(k-1)
-            if (even) n += NS;
+            if (u % 2 && d == 1) return n;
+            n += scales((u - d + 8) % 4);
             if (DA <= d + 2) return n;                 // A of step k-d-1+DA
             n += A_DMA;
         }
     }
 };
 
-// Part `part` (of BM rows) of tile v. Tile ids walk groups of 4 row tiles (of args.block_m rows) across all column tiles.
 // NT: B through non-temporal loads (one row tile reads it).
 template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
 __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, int num_mt, int v, int part) {
@@ -333,6 +342,7 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     constexpr int WM = C::WM, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB, A_DMA = C::A_DMA, B_DMA = C::B_DMA;
     constexpr int kBAux = NT ? 2 : 0;
     uint8_t* const bring = smem + DA * C::A_BYTES;
+    uint8_t* const sring = bring + DB * kBStep;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
@@ -367,12 +377,24 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     // With an odd number of K steps the last step's second half lies past the rows. Its loads repeat the first half's, and its
     // products vanish by their scales: byte 0 on both sides, 2^-254 (A's by scale_words, B's as packed)
     const uint32_t past = (nks & 1) && chunk >= 4 ? 64u : 0u;
-    // (the words of a last block's missing K steps repeat the last one's)
-    const int last_kb = (nks - 1) >> 2;
-    const uint32_t past_sf = 4u * max(0, 4 * last_kb + g - (nks - 1));
-    uint32_t sa_off[FM];
+    // A's scale words (4 bytes, a K step's): lane 16g + i takes step g's of row i, per fragment and block of 4 K steps, in
+    // registers, or, staged, row r's 8 of a chunk lie in LDS as 8-row groups of 256 bytes: word 32 * (half ^ group % 2) + 4 *
+    // (r % 8) + step in its half, so that a fragment's words lie in different banks. Words of K steps past the last repeat it.
+    const int last_kb = (nks - 1) >> 2, last_kc = (nks - 1) >> 3;
+    constexpr int NSA = C::STAGED ? C::S_DMA : FM;
+    uint32_t sa_off[NSA], past_sf[2];
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)(args.K / 32) + 4u * g;
+    for (int h = 0; h < 2; ++h) {
+        const int step = C::STAGED ? 8 * last_kc + 4 * ((lane >> 5) ^ h) + (lane & 3) : 4 * last_kb + g;
+        past_sf[h] = 4u * max(0, step - (nks - 1));
+    }
+#pragma unroll
+    for (int f = 0; f < NSA; ++f) {
+        if constexpr (C::STAGED)
+            sa_off[f] = a_row(8 * (wave * NSA + f) + ((lane >> 2) & 7)) * (uint32_t)(args.K / 32) + 16u * ((lane >> 5) ^ (f & 1)) + 4u * (lane & 3);
+        else
+            sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)(args.K / 32) + 4u * g;
+    }
     const ByteSelect sel = byte_select(g);
     const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)args.a, 0, (int)(args.rows * (uint32_t)(args.K / 2)), kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)args.a_sf, 0, (int)(args.rows * (uint32_t)(args.K / 32)), kRsrcWord3);
@@ -394,9 +416,23 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     };
     // scale words of a block of two steps: A's as loaded, and by byte of the K step in the block as the products take them
     uint32_t raw[FM], sa[2][FM], sb[2][FN];
-    auto load_scale = [&](int kb, int i, int set) __attribute__((always_inline)) {
-        if (i < FM) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[i] - (kb == last_kb ? past_sf : 0u), kb * 16, 0);
-        else sb[set][i - FM] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, lane * 4 + (wn * FN + i - FM) * 256, kb * kBScaleBlockBytes, kBAux);
+    auto load_sa = [&](int kb, int f) __attribute__((always_inline)) {
+        raw[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[f] - (kb == last_kb ? past_sf[0] : 0u), kb * 16, 0);
+    };
+    auto load_sb = [&](int kb, int f, int set) __attribute__((always_inline)) {
+        sb[set][f] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, lane * 4 + (wn * FN + f) * 256, kb * kBScaleBlockBytes, kBAux);
+    };
+    auto stage_sa = [&](int kc, int j) __attribute__((always_inline)) {
+        const int c = min(kc, last_kc);       // chunks past the last reload it into a free slot
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_asf, MOE_LPTR(sring + (kc & 1) * C::S_BYTES + (wave * NSA + j) * 256), 4,
+                                                 sa_off[j] - (c == last_kc ? past_sf[j & 1] : 0u), c * kChunkRow, 0, 0);
+    };
+    uint32_t rd_sa[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        rd_sa[h] = (uint32_t)((wm * WM / 8 + (l >> 3)) * 256 + 128 * (h ^ (l >> 3)) + 16 * (l & 7) + 4 * g);
+    auto read_sa = [&](int kb, int f) __attribute__((always_inline)) {
+        raw[f] = *reinterpret_cast<const uint32_t*>(sring + ((kb >> 1) & 1) * C::S_BYTES + f * 512 + rd_sa[kb & 1]);
     };
     // (bytes of K steps past the last: 0)
     auto scale_words = [&](int kb, int f) __attribute__((always_inline)) -> uint32_t {
@@ -426,22 +462,41 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
         }
     asm volatile("s_nop 7" ::: "memory");   // accumulator writes -> first MFMA
 
-    // Loads of a step: B of DB steps ahead (on even steps behind the next block's scale words) from its first barrier on, which
-    // every wave passes with B of this step in registers; A of DA steps ahead from its second barrier on, which every wave
-    // passes with A of this step read
-    constexpr int NS = C::NS;
+    // Loads of a step: scale words and B of DB steps ahead from its first barrier on, which every wave passes with B of this step
+    // in registers; A of DA steps ahead from its second barrier on, which every wave passes with A of this step read
     constexpr int ROW = 2 * FN;             // MFMAs per fragment row
-    constexpr int X_ROOM = (FM - 2) * ROW, X_SPACE = X_ROOM / (NS + B_DMA) > 3 ? 3 : X_ROOM / (NS + B_DMA);   // MFMAs per load
+    constexpr int X_OPS = C::scales(0) + B_DMA, X_ROOM = (FM - 2) * ROW, X_SPACE = X_ROOM / X_OPS > 3 ? 3 : X_ROOM / X_OPS;   // MFMAs per load
     constexpr int Y_SPACE = ROW / A_DMA;
-    static_assert(X_SPACE >= 1 && Y_SPACE >= 1, "a step's loads fit between its barriers");
-    auto issue_x = [&](int ks, bool scales, int set, int op) __attribute__((always_inline)) {
-        const int ns = scales ? NS : 0;
-        if (op < ns) load_scale(min((ks >> 1) + 1, last_kb), op, set);
-        else if (op < ns + B_DMA) load_b(ks + DB, op - ns);
+    static_assert(X_SPACE >= 1 && Y_SPACE >= 1 && C::scales(2) <= C::scales(0), "a step's loads fit between its barriers");
+    auto issue_x = [&](int ks, int u, int set, int op) __attribute__((always_inline)) {
+        if (op < C::staged(u)) {
+            stage_sa((ks >> 2) + 1, u * C::S_EACH + op);
+            return;
+        }
+        op -= C::staged(u);
+        if (u % 2 == 0) {
+            const int kb = min((ks >> 1) + 1, last_kb);
+            if (!C::STAGED && op < FM) {
+                load_sa(kb, op);
+                return;
+            }
+            if (!C::STAGED) op -= FM;
+            if (op < FN) {
+                load_sb(kb, op, set);
+                return;
+            }
+            op -= FN;
+        }
+        if (op < B_DMA) load_b(ks + DB, op);
     };
     // the loads that the steps before step 0 would have issued
 #pragma unroll
-    for (int i = 0; i < NS; ++i) load_scale(0, i, 0);
+    for (int i = 0; i < NSA; ++i) {
+        if constexpr (C::STAGED) stage_sa(0, i);
+        else load_sa(0, i);
+    }
+#pragma unroll
+    for (int f = 0; f < FN; ++f) load_sb(0, f, 0);
 #pragma unroll
     for (int k = DA > DB ? -DA : -DB; k < 0; ++k) {
 #pragma unroll
@@ -458,7 +513,10 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     __builtin_amdgcn_s_waitcnt(0x0F70 | (WAIT0 & 15) | (((WAIT0 >> 4) & 3) << 14));
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(WAIT0) : "memory");
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa[0][f] = scale_words(0, f);
+    for (int f = 0; f < FM; ++f) {
+        if constexpr (C::STAGED) read_sa(0, f);
+        sa[0][f] = scale_words(0, f);
+    }
     Pair a_cur, a_nx;
     v4i bq[2][FN];
 #pragma unroll
@@ -473,21 +531,23 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     // One step: 256 of K, FM rows of 2 x FN MFMAs. Its first barrier stands behind the first row, where every wave holds B of the
     // step in registers. At the second, before the last row, this wave's loads of step ks+1 have landed and its LDS reads of A
     // are done; behind it each B fragment's registers take the next step's right after their last use.
-    auto step = [&](int ks, auto odd_c, auto set_c) __attribute__((always_inline)) {
-        constexpr int ODD = decltype(odd_c)::value, SET = decltype(set_c)::value;
+    auto step = [&](int ks, auto u_c) __attribute__((always_inline)) {
+        constexpr int U = decltype(u_c)::value, ODD = U & 1, SET = U >> 1;   // U: ks % 4
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
             if (fm == 1) asm volatile("s_barrier" ::: "memory");
             if (fm == FM - 1) {
                 // in flight may be what was issued behind B of step ks+1 and (odd steps) the scale words
-                constexpr int WN_ = C::in_flight(ODD);
+                constexpr int WN_ = C::in_flight(U);
                 static_assert(WN_ < 64, "vmcnt range");
                 __builtin_amdgcn_s_waitcnt(0x0070 | (WN_ & 15) | (((WN_ >> 4) & 3) << 14));
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
                 if constexpr (ODD) {
                     // the next block's scale words have landed: no wait of the compiler's own for them
+                    if constexpr (!C::STAGED) {
 #pragma unroll
-                    for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(raw[f]));
+                        for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(raw[f]));
+                    }
 #pragma unroll
                     for (int f = 0; f < FN; ++f) asm volatile("" : "+v"(sb[SET ^ 1][f]));
                 }
@@ -503,13 +563,16 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                     if (t == 0) a_nx = fm + 1 < FM ? read_a(ks, fm + 1) : read_a(ks + 1, 0);
                     if (fm == FM - 1) {
                         bq[h][fn] = read_b(ks + 1, h, fn);
-                        if (ODD && t % (ROW / FM) == 0) {
-                            sa[SET ^ 1][t / (ROW / FM)] = scale_words((ks >> 1) + 1, t / (ROW / FM));
-                            asm volatile("" : "+v"(sa[SET ^ 1][t / (ROW / FM)]));
+                        // the next block's words of A: read from LDS, half a row of products later put in order
+                        if (ODD && C::STAGED && t < FM) read_sa((ks >> 1) + 1, t);
+                        constexpr int LATE = ROW - FM;
+                        if (ODD && t >= LATE) {
+                            sa[SET ^ 1][t - LATE] = scale_words((ks >> 1) + 1, t - LATE);
+                            asm volatile("" : "+v"(sa[SET ^ 1][t - LATE]));
                         }
                         if (t % Y_SPACE == 0 && t / Y_SPACE < A_DMA) load_a(ks + DA, t / Y_SPACE);
                     } else if (fm > 0 && ((fm - 1) * ROW + t) % X_SPACE == 0) {
-                        issue_x(ks, !ODD, SET ^ 1, ((fm - 1) * ROW + t) / X_SPACE);
+                        issue_x(ks, U, SET ^ 1, ((fm - 1) * ROW + t) / X_SPACE);
                     }
                     __builtin_amdgcn_sched_barrier(0x7);
                 }
@@ -520,14 +583,14 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     // 4 steps per iteration: two blocks of scale words, one per set
     int ks0 = 0;
     for (; ks0 + 4 <= nst; ks0 += 4) {
-        step(ks0, IntC<0>{}, IntC<0>{});
-        step(ks0 + 1, IntC<1>{}, IntC<0>{});
-        step(ks0 + 2, IntC<0>{}, IntC<1>{});
-        step(ks0 + 3, IntC<1>{}, IntC<1>{});
+        step(ks0, IntC<0>{});
+        step(ks0 + 1, IntC<1>{});
+        step(ks0 + 2, IntC<2>{});
+        step(ks0 + 3, IntC<3>{});
     }
-    if (ks0 < nst) step(ks0, IntC<0>{}, IntC<0>{});
-    if (ks0 + 1 < nst) step(ks0 + 1, IntC<1>{}, IntC<0>{});
-    if (ks0 + 2 < nst) step(ks0 + 2, IntC<0>{}, IntC<1>{});
+    if (ks0 < nst) step(ks0, IntC<0>{});
+    if (ks0 + 1 < nst) step(ks0 + 1, IntC<1>{});
+    if (ks0 + 2 < nst) step(ks0 + 2, IntC<2>{});
     // the last steps' reloads must land before the workgroup's LDS is given back
     __builtin_amdgcn_s_waitcnt(0x0F70);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
