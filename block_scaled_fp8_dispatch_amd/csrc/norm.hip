@@ -15,22 +15,53 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+template <int N>
+struct IntC {
+    static constexpr int value = N;
+};
 
-// sum over the workgroup, in every thread, in a fixed order
+
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+// NT: past the caches
+template <bool NT, class V>
+__device__ inline V get(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+    else return *static_cast<const V*>(p);
+}
+template <bool NT, class V>
+__device__ inline void put(void* p, const V& v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+    else *static_cast<V*>(p) = v;
+}
+
+// The sum over the workgroup of T threads, in every thread, in a fixed order: within 16 lanes by DPP (neighbours, pairs, the
+// mirrored half row, the mirrored row), then the four 16-lane rows, then the waves
+template <int T>
 __device__ inline float block_sum(float s, float* part) {
+    auto add = [&](auto ctrl) __attribute__((always_inline)) {
+        s += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(s), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    add(IntC<0xB1>{});
+    add(IntC<0x4E>{});
+    add(IntC<0x141>{});
+    add(IntC<0x140>{});
+    const int b = (int)__float_as_uint(s);
+    s = (__uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 0)) + __uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 16))) +
+        (__uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 32)) + __uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 48)));
+    if constexpr (T > 64) {
+        __syncthreads();                               // `part` may still be read from the sum before
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+        __syncthreads();
+        s = part[0];
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
-    __syncthreads();                                   // `part` may still be read from the sum before
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-    __syncthreads();
-    s = part[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += part[w];
+        for (int w = 1; w < T / 64; ++w) s += part[w];
+    }
     return s;
 }
 
-__device__ inline void unpack8(const uint4& v, float (&f)[8]) {
+__device__ inline void unpack8(const v4u& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -39,11 +70,11 @@ __device__ inline void unpack8(const uint4& v, float (&f)[8]) {
     }
 }
 
-__device__ inline uint4 pack8(const float (&f)[8]) {
+__device__ inline v4u pack8(const float (&f)[8]) {
     typedef float v8f __attribute__((ext_vector_type(8)));
     typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
     const v8f v = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
-    return __builtin_bit_cast(uint4, __builtin_convertvector(v, v8bf));
+    return __builtin_bit_cast(v4u, __builtin_convertvector(v, v8bf));
 }
 
 struct NormArgs {
@@ -59,11 +90,12 @@ struct NormArgs {
 };
 
 // h of the 8 columns at c of a row that starts at `at`
+template <bool NT>
 __device__ inline void load_h(const NormArgs& p, size_t at, int c, float (&h)[8]) {
-    unpack8(*reinterpret_cast<const uint4*>(p.x + at + c), h);
+    unpack8(get<NT, v4u>(p.x + at + c), h);
     if (p.residual) {
         float r[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.residual + at + c), r);
+        unpack8(get<NT, v4u>(p.residual + at + c), r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] += r[j];
     }
@@ -76,7 +108,7 @@ __device__ inline void load_w(const NormArgs& p, int c, float (&w)[8]) {
         const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + c + 4);
         w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + c), w);
+        unpack8(get<false, v4u>(static_cast<const uint16_t*>(p.weight) + c), w);
     }
 }
 
@@ -96,10 +128,11 @@ __device__ inline uint32_t max_of_16(uint32_t m) {
 }
 
 // n of 8 columns -> normed, codes, and (every 16th lane) the block's scale byte. c < sf_stride * 128; past cols: zeros
+template <bool NT>
 __device__ inline void store_n(const NormArgs& p, size_t row, int c, const float (&n)[8]) {
     const bool active = c < p.cols;
     const size_t at = row * p.cols + c;
-    if (active && p.normed) *reinterpret_cast<uint4*>(p.normed + at) = pack8(n);
+    if (active && p.normed) put<NT>(p.normed + at, pack8(n));
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(n[j]) & 0x7fffffffu);
@@ -111,7 +144,7 @@ __device__ inline void store_n(const NormArgs& p, size_t row, int c, const float
         a = __builtin_amdgcn_cvt_pk_fp8_f32(n[2] * mul, n[3] * mul, a, true);
         int b = __builtin_amdgcn_cvt_pk_fp8_f32(n[4] * mul, n[5] * mul, 0, false);
         b = __builtin_amdgcn_cvt_pk_fp8_f32(n[6] * mul, n[7] * mul, b, true);
-        *reinterpret_cast<uint2*>(p.q + at) = make_uint2((uint32_t)a, (uint32_t)b);
+        put<NT>(p.q + at, (v2u){(uint32_t)a, (uint32_t)b});
     }
     if ((threadIdx.x & 15) == 0 && (c >> 7) < p.sf_stride) p.sf[row * p.sf_stride + (c >> 7)] = active ? (uint8_t)byte : (uint8_t)0;
 }
@@ -127,10 +160,10 @@ __device__ inline float inverse_root(float sum, float cols, float eps, float f) 
     return 1.0f / __builtin_sqrtf(sum / cols + eps * f * f);
 }
 
-// CH chunks of 2048 columns held in registers (CH = 0: any number, read again from memory for each pass)
-template <int CH, bool WF32>
-__global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormArgs p, int row0) {
-    __shared__ float part[kWaves];
+// T threads hold CH chunks of 8 * T columns in registers (CH = 0: any number, read again from memory for each pass)
+template <int T, int CH, bool WF32, bool NT>
+__global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
+    __shared__ float part[T / 64];
     const size_t row = (size_t)row0 + blockIdx.x, at = row * p.cols;
     const int t8 = threadIdx.x * 8;
     const float cols = (float)p.cols;
@@ -138,10 +171,10 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormArgs p, int row0)
         float h[CH][8], s = 0.f;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (8 * kThreads) + t8;
+            const int c = k * (8 * T) + t8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
-            if (c < p.cols) load_h(p, at, c, h[k]);
+            if (c < p.cols) load_h<NT>(p, at, c, h[k]);
         }
         float f = 1.0f;
         auto squares = [&]() __attribute__((always_inline)) {
@@ -150,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormArgs p, int row0)
             for (int k = 0; k < CH; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q += (h[k][j] * f) * (h[k][j] * f);
-            return block_sum(q, part);
+            return block_sum<T>(q, part);
         };
         s = squares();
         f = square_scale(s, p.eps);
@@ -158,54 +191,59 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormArgs p, int row0)
         const float r = inverse_root(s, cols, p.eps, f);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (8 * kThreads) + t8;
+            const int c = k * (8 * T) + t8;
             float n[8] = {};
             if (c < p.cols) {
-                if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + at + c) = pack8(h[k]);
+                if (p.residual_out) put<NT>(p.residual_out + at + c, pack8(h[k]));
                 float w[8];
                 load_w<WF32>(p, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[j] = (h[k][j] * f) * r * w[j];
             }
-            store_n(p, row, c, n);
+            store_n<NT>(p, row, c, n);
         }
     } else {
         const int end = (p.cols + 511) / 512 * 512;     // whole waves
         float f = 1.0f;
         auto squares = [&]() {
             float q = 0.f;
-            for (int c = t8; c < p.cols; c += 8 * kThreads) {
+            for (int c = t8; c < p.cols; c += 8 * T) {
                 float h[8];
-                load_h(p, at, c, h);
+                load_h<false>(p, at, c, h);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q += (h[j] * f) * (h[j] * f);
             }
-            return block_sum(q, part);
+            return block_sum<T>(q, part);
         };
         float s = squares();
         f = square_scale(s, p.eps);
         if (f != 1.0f) s = squares();
         const float r = inverse_root(s, cols, p.eps, f);
-        for (int c = t8; c < end; c += 8 * kThreads) {
+        for (int c = t8; c < end; c += 8 * T) {
             float h[8], n[8] = {};
             if (c < p.cols) {
-                load_h(p, at, c, h);
+                load_h<false>(p, at, c, h);
                 // (the lane has read these columns of both inputs: either may be residual_out)
-                if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + at + c) = pack8(h);
+                if (p.residual_out) put<false>(p.residual_out + at + c, pack8(h));
                 float w[8];
                 load_w<WF32>(p, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[j] = (h[j] * f) * r * w[j];
             }
-            store_n(p, row, c, n);
+            store_n<false>(p, row, c, n);
         }
     }
 }
 
-template <int CH>
-void launch(const NormArgs& p, bool wf32, int row0, unsigned rows, hipStream_t stream) {
-    if (wf32) rmsnorm_kernel<CH, true><<<rows, kThreads, 0, stream>>>(p, row0);
-    else rmsnorm_kernel<CH, false><<<rows, kThreads, 0, stream>>>(p, row0);
+template <int T, int CH>
+void launch(const NormArgs& p, bool wf32, bool nt, int row0, unsigned rows, hipStream_t stream) {
+    if (wf32) {
+        if (nt) rmsnorm_kernel<T, CH, true, true><<<rows, T, 0, stream>>>(p, row0);
+        else rmsnorm_kernel<T, CH, true, false><<<rows, T, 0, stream>>>(p, row0);
+    } else {
+        if (nt) rmsnorm_kernel<T, CH, false, true><<<rows, T, 0, stream>>>(p, row0);
+        else rmsnorm_kernel<T, CH, false, false><<<rows, T, 0, stream>>>(p, row0);
+    }
 }
 
 }  // namespace
@@ -214,15 +252,25 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
                           float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
     NormArgs p{x, residual, weight, q, sf, normed, residual_out, cols, 4 * cdiv(cols, 512), eps};
     const bool wf32 = weight_type == MOE_F32;
-    constexpr int kMost = 1 << 23;                      // rows of a launch: at most 2^31 threads
+    // (what the L2s do not hold anyway goes past them)
+    const bool nt = (size_t)rows * cols > (size_t(8) << 20);
+    // Threads per row: as many as it has chunks while there are fewer rows than fill the CUs (16 x 7168: 3.1 us with 1024
+    // threads, 3.5 with 512, 4.9 with 256), fewer, with more in flight each, where rows are many (8192 x 7168: 69, 76 and 75 us with
+    // 512, 256 and 1024; 3000 x 4096: 15.6 with 128, 17.0 with 512)
+    constexpr int kMany = 1024;
+    constexpr int kMost = 1 << 21;                      // rows of a launch: at most 2^31 threads
     for (int row0 = 0; row0 < rows; row0 += kMost) {
         const unsigned n = (unsigned)(rows - row0 < kMost ? rows - row0 : kMost);
-        const int chunks = cdiv(cols, 8 * kThreads);
-        if (chunks <= 1) launch<1>(p, wf32, row0, n, stream);
-        else if (chunks <= 2) launch<2>(p, wf32, row0, n, stream);
-        else if (chunks <= 4) launch<4>(p, wf32, row0, n, stream);
-        else if (chunks <= 8) launch<8>(p, wf32, row0, n, stream);
-        else launch<0>(p, wf32, row0, n, stream);
+        if (cols <= 512) launch<64, 1>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 1024) launch<128, 1>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 2048) launch<256, 1>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 4096 && rows >= kMany) launch<128, 4>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 4096) launch<512, 1>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 8192 && rows >= kMany) launch<512, 2>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 8192) launch<1024, 1>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 16384) launch<1024, 2>(p, wf32, nt, row0, n, stream);
+        else if (cols <= 24576) launch<1024, 3>(p, wf32, nt, row0, n, stream);
+        else launch<1024, 0>(p, wf32, nt, row0, n, stream);
         if (rows - row0 <= kMost) break;                // (row0 + kMost may pass 2^31)
     }
     return hipGetLastError();
