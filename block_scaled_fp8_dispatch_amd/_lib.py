@@ -156,9 +156,12 @@ def make_shape(num_experts: int, hidden: int, intermediate: int, num_topk: int,
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:                            # (a tensor first: 0.13 us each instead of 0.23 behind a test for int)
+        return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
 
 
 _current_stream = None

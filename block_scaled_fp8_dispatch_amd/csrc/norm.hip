@@ -9,6 +9,8 @@
 //
 // A workgroup owns a row and keeps it in registers: 8 columns per lane and chunk, so that the 16 lanes of a DPP row hold one
 // 128-column block.
+#include <algorithm>
+
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -36,10 +38,10 @@ __device__ inline void put(void* p, const V& v) {
     else *static_cast<V*>(p) = v;
 }
 
-// The sum over the workgroup of T threads, in every thread, in a fixed order: within 16 lanes by DPP (neighbours, pairs, the
-// mirrored half row, the mirrored row), then the four 16-lane rows, then the waves
-template <int T>
-__device__ inline float block_sum(float s, float* part) {
+constexpr int kMaxThreads = 1024;
+
+// The sum over 16 lanes, in each of them: neighbours, pairs, the mirrored half row, the mirrored row
+__device__ inline float sum_of_16(float s) {
     auto add = [&](auto ctrl) __attribute__((always_inline)) {
         s += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(s), decltype(ctrl)::value, 0xF, 0xF, false));
     };
@@ -47,18 +49,22 @@ __device__ inline float block_sum(float s, float* part) {
     add(IntC<0x4E>{});
     add(IntC<0x141>{});
     add(IntC<0x140>{});
-    const int b = (int)__float_as_uint(s);
+    return s;
+}
+
+// The sum over the workgroup, in every thread, in a fixed order: 16 lanes, the wave's four rows of 16, the waves (at most 16)
+__device__ inline float block_sum(float s, float* part) {
+    const int b = (int)__float_as_uint(sum_of_16(s));
     s = (__uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 0)) + __uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 16))) +
         (__uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 32)) + __uint_as_float((uint32_t)__builtin_amdgcn_readlane(b, 48)));
-    if constexpr (T > 64) {
-        __syncthreads();                               // `part` may still be read from the sum before
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-        __syncthreads();
-        s = part[0];
-#pragma unroll
-        for (int w = 1; w < T / 64; ++w) s += part[w];
-    }
-    return s;
+    const int waves = blockDim.x >> 6;
+    if (waves == 1) return s;
+    static_assert(kMaxThreads == 16 * 64, "");
+    __syncthreads();                                   // `part` may still be read from the sum before
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    const int w = threadIdx.x & 15;
+    return sum_of_16(w < waves ? part[w] : 0.f);
 }
 
 __device__ inline void unpack8(const v4u& v, float (&f)[8]) {
@@ -160,18 +166,18 @@ __device__ inline float inverse_root(float sum, float cols, float eps, float f) 
     return 1.0f / __builtin_sqrtf(sum / cols + eps * f * f);
 }
 
-// T threads hold CH chunks of 8 * T columns in registers (CH = 0: any number, read again from memory for each pass)
-template <int T, int CH, bool WF32, bool NT>
-__global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
-    __shared__ float part[T / 64];
+// The threads hold CH chunks of 8 columns each in registers (CH = 0: any number, read again from memory for each pass)
+template <int CH, bool WF32, bool NT>
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int row0) {
+    __shared__ float part[kMaxThreads / 64];
     const size_t row = (size_t)row0 + blockIdx.x, at = row * p.cols;
-    const int t8 = threadIdx.x * 8;
+    const int t8 = threadIdx.x * 8, span = blockDim.x * 8;
     const float cols = (float)p.cols;
     if constexpr (CH > 0) {
         float h[CH][8], s = 0.f;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (8 * T) + t8;
+            const int c = k * (span) + t8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
             if (c < p.cols) load_h<NT>(p, at, c, h[k]);
@@ -183,7 +189,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
             for (int k = 0; k < CH; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q += (h[k][j] * f) * (h[k][j] * f);
-            return block_sum<T>(q, part);
+            return block_sum(q, part);
         };
         s = squares();
         f = square_scale(s, p.eps);
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
         const float r = inverse_root(s, cols, p.eps, f);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (8 * T) + t8;
+            const int c = k * (span) + t8;
             float n[8] = {};
             if (c < p.cols) {
                 if (p.residual_out) put<NT>(p.residual_out + at + c, pack8(h[k]));
@@ -207,19 +213,19 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
         float f = 1.0f;
         auto squares = [&]() {
             float q = 0.f;
-            for (int c = t8; c < p.cols; c += 8 * T) {
+            for (int c = t8; c < p.cols; c += span) {
                 float h[8];
                 load_h<false>(p, at, c, h);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q += (h[j] * f) * (h[j] * f);
             }
-            return block_sum<T>(q, part);
+            return block_sum(q, part);
         };
         float s = squares();
         f = square_scale(s, p.eps);
         if (f != 1.0f) s = squares();
         const float r = inverse_root(s, cols, p.eps, f);
-        for (int c = t8; c < end; c += 8 * T) {
+        for (int c = t8; c < end; c += span) {
             float h[8], n[8] = {};
             if (c < p.cols) {
                 load_h<false>(p, at, c, h);
@@ -235,14 +241,16 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(NormArgs p, int row0) {
     }
 }
 
-template <int T, int CH>
+template <int CH>
 void launch(const NormArgs& p, bool wf32, bool nt, int row0, unsigned rows, hipStream_t stream) {
+    // as many waves as the row needs
+    const int threads = CH > 0 ? 64 * cdiv(p.cols, 512 * CH) : kMaxThreads;
     if (wf32) {
-        if (nt) rmsnorm_kernel<T, CH, true, true><<<rows, T, 0, stream>>>(p, row0);
-        else rmsnorm_kernel<T, CH, true, false><<<rows, T, 0, stream>>>(p, row0);
+        if (nt) rmsnorm_kernel<CH, true, true><<<rows, threads, 0, stream>>>(p, row0);
+        else rmsnorm_kernel<CH, true, false><<<rows, threads, 0, stream>>>(p, row0);
     } else {
-        if (nt) rmsnorm_kernel<T, CH, false, true><<<rows, T, 0, stream>>>(p, row0);
-        else rmsnorm_kernel<T, CH, false, false><<<rows, T, 0, stream>>>(p, row0);
+        if (nt) rmsnorm_kernel<CH, false, true><<<rows, threads, 0, stream>>>(p, row0);
+        else rmsnorm_kernel<CH, false, false><<<rows, threads, 0, stream>>>(p, row0);
     }
 }
 
@@ -254,23 +262,23 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
     const bool wf32 = weight_type == MOE_F32;
     // (what the L2s do not hold anyway goes past them)
     const bool nt = (size_t)rows * cols > (size_t(8) << 20);
-    // Threads per row: as many as it has chunks while there are fewer rows than fill the CUs (16 x 7168: 3.1 us with 1024
-    // threads, 3.5 with 512, 4.9 with 256), fewer, with more in flight each, where rows are many (8192 x 7168: 69, 76 and 75 us with
-    // 512, 256 and 1024; 3000 x 4096: 15.6 with 128, 17.0 with 512)
+    // Chunks per thread: one while there are fewer rows than fill the CUs, so that a row has as many waves as it can (16 x 7168:
+    // 3.1 us with one chunk, 3.6 with two, 4.9 with four), more, with more in flight each, where rows are many and wide (8192 x
+    // 7168: 75 us with one, 69 with two, 76 with four; 3000 x 4096: 17.3, 17.4 and 15.6; 3000 x 18432: 68 with three, 78 with
+    // four; 20000 x 1536: 37, 38 and 40)
     constexpr int kMany = 1024;
+    const int least = cdiv(cols, 8 * kMaxThreads);
+    const int ch = rows < kMany || cols <= 2048 ? least : cols <= 4096 ? 4 : cols <= 8192 ? 2 : std::max(3, least);
     constexpr int kMost = 1 << 21;                      // rows of a launch: at most 2^31 threads
     for (int row0 = 0; row0 < rows; row0 += kMost) {
         const unsigned n = (unsigned)(rows - row0 < kMost ? rows - row0 : kMost);
-        if (cols <= 512) launch<64, 1>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 1024) launch<128, 1>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 2048) launch<256, 1>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 4096 && rows >= kMany) launch<128, 4>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 4096) launch<512, 1>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 8192 && rows >= kMany) launch<512, 2>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 8192) launch<1024, 1>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 16384) launch<1024, 2>(p, wf32, nt, row0, n, stream);
-        else if (cols <= 24576) launch<1024, 3>(p, wf32, nt, row0, n, stream);
-        else launch<1024, 0>(p, wf32, nt, row0, n, stream);
+        switch (ch) {
+            case 1: launch<1>(p, wf32, nt, row0, n, stream); break;
+            case 2: launch<2>(p, wf32, nt, row0, n, stream); break;
+            case 3: launch<3>(p, wf32, nt, row0, n, stream); break;
+            case 4: launch<4>(p, wf32, nt, row0, n, stream); break;
+            default: launch<0>(p, wf32, nt, row0, n, stream);
+        }
         if (rows - row0 <= kMost) break;                // (row0 + kMost may pass 2^31)
     }
     return hipGetLastError();
