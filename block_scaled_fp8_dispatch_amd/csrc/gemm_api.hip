@@ -191,7 +191,7 @@ bool fp4_shape_ok(int G, int N, int K, int d_type) {
 }
 
 GemmFp4Args fp4_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int rows, int G, int N, int K, const void* packed_b,
-                     uint8_t* ws, const GemmWs& W, int block_m, int tiles_bound) {
+                     const GemmWs& W, int block_m, int tiles_bound) {
     const PackedBLayout L = packed_b_layout(G, N, K);
     const uint8_t* pk = static_cast<const uint8_t*>(packed_b);
     GemmFp4Args g{};
@@ -207,15 +207,18 @@ GemmFp4Args fp4_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf,
     g.bs_ntile = L.s_ntile;
     g.K = K;
     g.N = N;
-    g.dense_rows = 0;
-    g.perm = reinterpret_cast<const int32_t*>(ws + W.perm);
-    g.meta = reinterpret_cast<const int32_t*>(ws + W.meta);
-    g.tile_expert = reinterpret_cast<const int32_t*>(ws + W.tile_expert);
-    g.tile_row0 = reinterpret_cast<const int32_t*>(ws + W.tile_row0);
     g.max_tiles = tiles_bound < W.max_tiles ? tiles_bound : W.max_tiles;
     g.d = d;
     g.out_f32 = d_type == MOE_F32;
     return g;
+}
+
+// Row tiles from the lists in the workspace
+void fp4_lists(GemmFp4Args& g, const uint8_t* ws, const GemmWs& W) {
+    g.perm = reinterpret_cast<const int32_t*>(ws + W.perm);
+    g.meta = reinterpret_cast<const int32_t*>(ws + W.meta);
+    g.tile_expert = reinterpret_cast<const int32_t*>(ws + W.tile_expert);
+    g.tile_row0 = reinterpret_cast<const int32_t*>(ws + W.tile_row0);
 }
 
 // The FP4 casts' arguments
@@ -458,7 +461,7 @@ int moe_fp4_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     if (m == 0) return MOE_OK;
     const Fp4Plan plan = fp4_plan(1, m, m, false, n, k);
     const int BM = plan.block_m;
-    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, 1, n, k, packed_b, static_cast<uint8_t*>(workspace), W, BM, cdiv(m, BM));
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, 1, n, k, packed_b, W, BM, cdiv(m, BM));
     g.dense_rows = m;
     return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -480,7 +483,8 @@ int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     const Fp4Plan plan = fp4_plan(groups, (double)m / groups, m, true, n, k);
     const int BM = plan.block_m;
     if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
-    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, ws, W, BM, cdiv(m, BM) + groups);
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, W, BM, cdiv(m, BM) + groups);
+    fp4_lists(g, ws, W);
     return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -503,11 +507,19 @@ int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;
     const Fp4Plan plan = fp4_plan(groups, rows_each, (int)rows, true, n, k);
     const int BM = plan.block_m;
-    if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
-                           reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
-                           reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
-        return MOE_ERR_HIP;
-    const GemmFp4Args g = fp4_args(d, d_type, a, a_sf, (int)rows, groups, n, k, packed_b, ws, W, BM, groups * cdiv(max_m, BM));
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, (int)rows, groups, n, k, packed_b, W, BM, groups * cdiv(max_m, BM));
+    // one wave's load of the counts in the GEMM's prologue instead of a launch
+    if (groups <= kMaskedGroups) {
+        g.masked_m = masked_m;
+        g.groups = groups;
+        g.max_m = max_m;
+    } else {
+        if (launch_gemm_layout(groups, max_m, masked_m, BM, W.pad_rows, reinterpret_cast<int32_t*>(ws + W.perm),
+                               reinterpret_cast<int32_t*>(ws + W.tile_expert), reinterpret_cast<int32_t*>(ws + W.tile_row0),
+                               reinterpret_cast<int32_t*>(ws + W.meta), stream) != hipSuccess)
+            return MOE_ERR_HIP;
+        fp4_lists(g, ws, W);
+    }
     return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -46,6 +46,52 @@ struct IntC {
     static constexpr int value = N;
 };
 
+// Row tiles of p.block_m rows. Dense: rows 0 .. dense_rows-1. Masked with at most 64 groups: every wave derives them from the
+// counts, a group per lane. Otherwise the lists that a launch before has made.
+struct RowTiles {
+    int total;
+    int tiles, upto, count;    // masked: lane g's row tiles, those of groups 0 .. g, its rows
+};
+// A row tile: of group `group`, rows row0 .. row0+count-1 of A and D, or, with a list, perm[row0 + r] (-1: padding, which
+// comes last)
+struct RowTile {
+    int group, row0, count;
+};
+
+__device__ inline RowTiles row_tiles(const GemmFp4Args& p, int bm) {
+    RowTiles t{};
+    if (p.dense_rows > 0) {
+        t.total = (p.dense_rows + bm - 1) / bm;
+    } else if (p.masked_m) {
+        const int lane = threadIdx.x & 63;
+        t.count = lane < p.groups ? min(max(p.masked_m[lane], 0), p.max_m) : 0;
+        t.tiles = (t.count + bm - 1) / bm;
+        // inclusive sums: within 16 lanes, then the rows of 16 before
+        int x = t.tiles;
+        x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+        t.upto = x;
+        t.total = __builtin_amdgcn_readlane(x, 63);
+    } else {
+        t.total = min(__builtin_amdgcn_readfirstlane(p.meta[0]), p.max_tiles);
+    }
+    return t;
+}
+
+__device__ inline RowTile row_tile(const GemmFp4Args& p, const RowTiles& t, int bm, int mt) {
+    if (p.dense_rows > 0) return {0, mt * bm, p.dense_rows - mt * bm};
+    if (p.masked_m) {
+        const int g = __builtin_ctzll(__ballot(t.upto > mt));
+        const int first = (mt - __builtin_amdgcn_readlane(t.upto, g) + __builtin_amdgcn_readlane(t.tiles, g)) * bm;
+        return {g, g * p.max_m + first, __builtin_amdgcn_readlane(t.count, g) - first};
+    }
+    return {__builtin_amdgcn_readfirstlane(p.tile_expert[mt]), __builtin_amdgcn_readfirstlane(p.tile_row0[mt]), 0};
+}
+
 // NT: B through non-temporal loads (one row tile reads it)
 template <int FM, int FN, int WAVES, int DEPTH, bool F32, bool NT>
 __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
@@ -54,26 +100,29 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l = lane & 15;
-    const bool dense = p.dense_rows > 0;
-    // units of BM rows: of a dense product's rows, or of the 64-row tiles in the list
-    const int units = dense ? (p.dense_rows + BM - 1) / BM : min(__builtin_amdgcn_readfirstlane(p.meta[0]), p.max_tiles) * SUB;
+    // units of BM rows of the row tiles (dense: of BM rows themselves)
+    const bool dense = p.dense_rows > 0, list = p.perm != nullptr;
+    const int bm = dense ? BM : 64, sub = dense ? 1 : SUB;
+    const RowTiles rt = row_tiles(p, bm);
+    const int units = rt.total * sub;
     // column units of FN fragments; the 8 fragments of 128 columns interleave their columns
     const int units_n = (p.N + 127) / 128 * (8 / FN);
     const int v = xcd_tile(units * units_n, blockIdx.x);
     if (v < 0) return;
     // groups of 4 row tiles across all column units: their rows of A stay in the XCD's L2
-    constexpr int kSet = kGroupM * SUB;
-    const int set = v / (kSet * units_n), u0 = set * kSet, gu = min(kSet, units - u0), vin = v - set * kSet * units_n;
+    const int set_units = kGroupM * SUB;
+    const int set = v / (set_units * units_n), u0 = set * set_units, gu = min(set_units, units - u0), vin = v - set * set_units * units_n;
     const int unit = u0 + vin % gu;
-    const int mt = unit / SUB;
-    const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(p.tile_expert[mt]);
-    const int row0 = dense ? unit * BM : __builtin_amdgcn_readfirstlane(p.tile_row0[mt]) + unit % SUB * BM;
+    const RowTile at0 = row_tile(p, rt, bm, unit / sub);
+    const int group = at0.group, row0 = at0.row0 + unit % sub * BM, count = at0.count - unit % sub * BM;
+    // A and D row of row r of the unit, -1 on padding
     auto d_row = [&](int r) __attribute__((always_inline)) -> int {
-        if (dense) return row0 + r < p.dense_rows ? row0 + r : -1;
-        return p.perm[row0 + r];
+        if (list) return p.perm[row0 + r];
+        return r < count ? row0 + r : -1;
     };
     // padding comes last in a row tile: nothing but padding here
     if (__builtin_amdgcn_readfirstlane(d_row(0)) < 0) return;
+
     const int f0 = vin / gu * FN, tile = f0 >> 4, frag = f0 & 15;   // fragments frag .. frag + FN-1 of a 256-column tile
     const int nks = p.K / kBK;
 
@@ -335,7 +384,7 @@ struct Fp4Cfg {
 
 // NT: B through non-temporal loads (one row tile reads it).
 template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
-__device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, int num_mt, int v, int part) {
+__device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, const RowTiles& rt, int v, int part) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty function
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
@@ -347,18 +396,18 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int g = lane >> 4, l = lane & 15;
-    const bool dense = args.dense_rows > 0;
     const int tiles_n = (args.N + kBN - 1) / kBN;
     const int grp = v / (kGroupM * tiles_n), mt0 = grp * kGroupM;
-    const int gm = min(kGroupM, num_mt - mt0), vin = v - grp * kGroupM * tiles_n;
-    const int mt = mt0 + vin % gm, nt = vin / gm;
-    const int group = dense ? 0 : __builtin_amdgcn_readfirstlane(args.tile_expert[mt]);
-    const int row0 = (dense ? mt * args.block_m : __builtin_amdgcn_readfirstlane(args.tile_row0[mt])) + part * BM;
+    const int gm = min(kGroupM, rt.total - mt0), vin = v - grp * kGroupM * tiles_n;
+    const int nt = vin / gm;
+    const RowTile at0 = row_tile(args, rt, args.block_m, mt0 + vin % gm);
+    const int group = at0.group, row0 = at0.row0 + part * BM, count = at0.count - part * BM;
+    const bool list = args.perm != nullptr;
     const int nks = args.K / kBK, nst = (nks + 1) >> 1;   // K steps of 128 and steps of 256
-    // A and D row of tile row r, -1 on padding
+    // A and D row of row r, -1 on padding
     auto d_row = [&](int r) __attribute__((always_inline)) -> int {
-        if (dense) return row0 + r < args.dense_rows ? row0 + r : -1;
-        return args.perm[row0 + r];
+        if (list) return args.perm[row0 + r];
+        return r < count ? row0 + r : -1;
     };
     auto a_row = [&](int r) __attribute__((always_inline)) -> uint32_t {
         const int d = d_row(r);
@@ -605,53 +654,70 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     const int fw = wn * FN;
     const int col0 = nt * kBN + 128 * (fw >> 3) + 8 * l + (fw & 7);
     if (col0 >= args.N) return;
-    // tiles of 256 rows store past the caches: all CUs store at once there (4096 x 7168 x 18432 249 -> 244 us, 8192^3 258 -> 250)
+    // bf16 of tiles of 256 rows goes past the caches: all CUs store at once there (4096 x 7168 x 18432 249 -> 244 us, 8192^3 258 ->
+    // 250); FP32's 16-byte stores leave half a line each, which the caches put together (8192^3 past them: 361 us)
     auto put = [&](auto* to, const auto& x) __attribute__((always_inline)) {
-        if constexpr (BM == 256) __builtin_nontemporal_store(x, to);
+        if constexpr (BM == 256 && !F32) __builtin_nontemporal_store(x, to);
         else *to = x;
     };
+    auto store = [&](int fm, int r, size_t to) __attribute__((always_inline)) {
+        if constexpr (F32) {
+            float* dst = static_cast<float*>(args.d) + to;
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
+            for (int q = 0; q < FN; q += 4)
+                put(reinterpret_cast<v4f*>(dst + q), (v4f){acc[fm][q][r], acc[fm][q + 1][r], acc[fm][q + 2][r], acc[fm][q + 3][r]});
+        } else {
+            uint32_t pk[FN / 2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = d_row(wm * WM + fm * 16 + 4 * g + r);
-            if (row < 0) continue;
-            const size_t to = (size_t)row * args.N + col0;
-            if constexpr (F32) {
-                float* dst = static_cast<float*>(args.d) + to;
-#pragma unroll
-                for (int q = 0; q < FN; q += 4)
-                    put(reinterpret_cast<v4f*>(dst + q), (v4f){acc[fm][q][r], acc[fm][q + 1][r], acc[fm][q + 2][r], acc[fm][q + 3][r]});
-            } else {
-                uint32_t pk[FN / 2];
-#pragma unroll
-                for (int q = 0; q < FN; q += 2) {
-                    const v2f x = {acc[fm][q][r], acc[fm][q + 1][r]};
-                    pk[q / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
-                }
-                uint16_t* dst = static_cast<uint16_t*>(args.d) + to;
-                if constexpr (FN == 8) put(reinterpret_cast<v4i*>(dst), (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]});
-                else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+            for (int q = 0; q < FN; q += 2) {
+                const v2f x = {acc[fm][q][r], acc[fm][q + 1][r]};
+                pk[q / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
             }
+            uint16_t* dst = static_cast<uint16_t*>(args.d) + to;
+            if constexpr (FN == 8) put(reinterpret_cast<v4i*>(dst), (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]});
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+        }
+    };
+    const int lane_row = wm * WM + 4 * g;
+    if (list) {
+        // all row numbers first: one wait for them (a load and a wait per row: 3.7 us of 12.5 at 300 x 7168 x 2048)
+        int rows[FM][4];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rows[fm][r] = args.perm[row0 + lane_row + fm * 16 + r];
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (rows[fm][r] >= 0) store(fm, r, (size_t)rows[fm][r] * args.N + col0);
+    } else {
+        const size_t first = (size_t)(row0 + lane_row) * args.N + col0;
+        if (count >= BM) {
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) store(fm, r, first + (size_t)(fm * 16 + r) * args.N);
+        } else {
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (lane_row + fm * 16 + r < count) store(fm, r, first + (size_t)(fm * 16 + r) * args.N);
         }
     }
 #endif
-}
-
-// The row tiles in use: their number lies on the device unless the product is dense
-__device__ inline int row_tiles(const GemmFp4Args& args, int bm) {
-    const int n = args.dense_rows > 0 ? (args.dense_rows + bm - 1) / bm : __builtin_amdgcn_readfirstlane(args.meta[0]);
-    return min(n, args.max_tiles);
 }
 
 template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
 __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void gemm_fp4_tiled(GemmFp4Args args) {
     using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
-    const int num_mt = row_tiles(args, BM);
-    const int v = xcd_tile(num_mt * ((args.N + kBN - 1) / kBN), blockIdx.x);
+    const RowTiles rt = row_tiles(args, BM);
+    const int v = xcd_tile(rt.total * ((args.N + kBN - 1) / kBN), blockIdx.x);
     if (v < 0) return;
-    tiled_part<BM, WAVES_M, WAVES_N, F32, NT>(args, smem, num_mt, v, 0);
+    tiled_part<BM, WAVES_M, WAVES_N, F32, NT>(args, smem, rt, v, 0);
 }
 
 // 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where those are no more than
@@ -659,17 +725,18 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void gemm_fp4_tiled(GemmFp4A
 template <bool F32>
 __global__ __launch_bounds__(256, 1) void gemm_fp4_rounds(GemmFp4Args args) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[160 * 1024];
-    const int num_mt = row_tiles(args, 256), total = num_mt * ((args.N + kBN - 1) / kBN);
+    const RowTiles rt = row_tiles(args, 256);
+    const int total = rt.total * ((args.N + kBN - 1) / kBN);
     const int rem = total % kCus, full = rem <= kCus / 2 ? total - rem : total;
     if ((int)blockIdx.x < full) {
-        tiled_part<256, 2, 2, F32, false>(args, smem, num_mt, xcd_tile(full, blockIdx.x), 0);
+        tiled_part<256, 2, 2, F32, false>(args, smem, rt, xcd_tile(full, blockIdx.x), 0);
         return;
     }
     const int parts = rem <= kCus / 4 ? 4 : 2;
     const int u = xcd_tile((total - full) * parts, blockIdx.x - full);
     if (u < 0) return;
-    if (parts == 4) tiled_part<64, 1, 4, F32, false>(args, smem, num_mt, full + u / 4, u % 4);
-    else tiled_part<128, 2, 2, F32, false>(args, smem, num_mt, full + u / 2, u % 2);
+    if (parts == 4) tiled_part<64, 1, 4, F32, false>(args, smem, rt, full + u / 4, u % 4);
+    else tiled_part<128, 2, 2, F32, false>(args, smem, rt, full + u / 2, u % 2);
 }
 
 template <int BM, int WAVES_M, int WAVES_N>

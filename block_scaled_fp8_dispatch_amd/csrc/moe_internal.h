@@ -225,10 +225,13 @@ struct GemmFp4Args {
     size_t b_group, b_ntile, bs_group, bs_ntile;
     int K, N;
     uint32_t rows;             // of A: nothing is read past them
-    // Row tiles of block_m rows: dense_rows > 0: rows 0 .. dense_rows-1; otherwise the lists of
-    // the routing (perm: A and D row of each padded row, -1 padding)
+    // Row tiles of block_m rows: dense_rows > 0: rows 0 .. dense_rows-1; masked_m: the first masked_m[g] of each
+    // group's max_m rows (at most kMaskedGroups groups); otherwise the lists of the routing (perm: A and D row of each
+    // padded row, -1 padding; null without lists)
     int block_m;
     int dense_rows;
+    const int32_t* masked_m;
+    int groups, max_m;
     const int32_t* perm;
     const int32_t* meta;
     const int32_t* tile_expert;
@@ -237,6 +240,7 @@ struct GemmFp4Args {
     void* d;
     int out_f32;
 };
+constexpr int kMaskedGroups = 64;
 enum class Fp4Kernel {
     kTiled256, kTiled128, kTiled64, kSkinny64x64, kSkinny64x32, kSkinny32x64, kSkinny32x32, kSkinny16x32, kSkinny16
 };
