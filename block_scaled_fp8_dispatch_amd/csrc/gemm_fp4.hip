@@ -769,28 +769,29 @@ hipError_t launch_skinny(bool nt, const GemmFp4Args& a, hipStream_t stream) {
 }
 
 // Microseconds of a product with each kernel. Tiled: rounds of the workgroups that the CUs hold, each fixed + step per 128 K
-// (64 rows: two on a CU, a last round of one on a CU takes 0.63 of it). Skinny: fixed + wave per pair of K steps that a wave
-// takes + for every 256 workgroups tile + step per 128 K. Fitted to 73 products from 1 x 256 x 512 to 7698 x 2704 x 3200 and 18
-// groups of about 25 rows, each timed with every kernel, weights from memory: what the model picks is 2 % slower than the
-// best of the kernels on average, 44 % at most (982 x 576 x 3584).
-// A list's 64-row tiles with few rows leave most workgroups of 16 or 32 rows without any and the others to a part of the CUs,
-// so that there all count.
+// (64 rows: two on a CU, a last round of one on a CU takes 0.58 of it). Skinny: fixed + the larger of wave per pair of K steps
+// that a wave takes and, per 256 workgroups, tile + step per 128 K; + each per 256 workgroups. Fitted to 90 products from 1 x 16
+// x 128 to 7698 x 2704 x 3200 and 31 groups of about 47 rows, each timed with every kernel, weights from memory, and the tiled
+// ones to 4096 x 4096 x 18432: what the model picks is 2 % slower than the best of the kernels on average, half again as slow at
+// worst (64 x 4096 x 4096).
+// A masked or listed product's 64-row tiles with few rows leave most workgroups of 16 or 32 rows without any and the others to
+// a part of the CUs, so that there all count.
 struct Cost {
     Fp4Kernel kernel;
     int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
     int waves;                 // sharing K; 0: tiled
-    double fixed, step, wave, tile;
+    double fixed, step, wave, tile, each;
 };
-constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 6.8, 0.60, 0, 0},
-                           {Fp4Kernel::kTiled128, 128, 128, 256, 0, 7.6, 0.53, 0, 0},
-                           {Fp4Kernel::kTiled64, 64, 64, 256, 0, 9.2, 0.68, 0, 0},
-                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 2.12, 0.173, 1.64, 3.13},
-                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 1.73, 0.099, 1.26, 1.94},
-                           {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 1.45, 0.115, 1.54, 1.89},
-                           {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.44, 0.062, 1.23, 0.89},
-                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.50, 0.047, 0.95, 0.65},
-                           {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 1.79, 0.037, 1.10, 0.69}};
-constexpr double kAlone64 = 0.63;
+constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 6.8, 0.846, 0, 0, 0},
+                           {Fp4Kernel::kTiled128, 128, 128, 256, 0, 5.7, 0.504, 0, 0, 0},
+                           {Fp4Kernel::kTiled64, 64, 64, 256, 0, 6.4, 0.729, 0, 0, 0},
+                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 0.65, 0.245, 3.26, 0.06, 3.11},
+                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 0.67, 0.169, 2.63, 2.29, 0.20},
+                           {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 0.98, 0.179, 2.45, 1.54, 0.64},
+                           {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.45, 0.121, 1.49, 0.02, 0.69},
+                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.63, 0.080, 1.07, 0.00, 0.52},
+                           {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 2.20, 0.045, 1.08, 1.00, 0.16}};
+constexpr double kAlone64 = 0.58;
 
 }  // namespace
 
@@ -809,7 +810,8 @@ Fp4Plan fp4_plan(int groups, double rows, int max_rows, bool ragged, int N, int 
         const double tiles = std::ceil(mt) * cols;
         double t = 0;
         if (c.waves) {
-            t = c.fixed + c.wave * cdiv(cdiv(steps, 2), c.waves) + tiles / kCus * (c.tile + c.step * steps);
+            const double share = tiles / kCus;
+            t = c.fixed + std::max(c.wave * cdiv(cdiv(steps, 2), c.waves), share * (c.tile + c.step * steps)) + share * c.each;
         } else {
             const double round = c.fixed + c.step * steps, slots = c.kernel == Fp4Kernel::kTiled64 ? 2 * kCus : kCus;
             const double rounds = std::floor(tiles / slots), rem = tiles - rounds * slots;
