@@ -345,7 +345,10 @@ constexpr int kBStep = 2 * kBTileBytes;
 // Bytes of a chunk (4 steps) of a row's scales
 constexpr int kChunkRow = 4 * kStep / 32;
 
-template <int BM, int WAVES_M, int WAVES_N>
+// QUADS: A's scale words straight into registers, a block's 16 bytes a lane and load and four blocks an instruction, instead of 4
+// bytes and one block: a load costs by the lines it touches, 16 rows' in either form. K is a multiple of 512, so that rows end
+// with a block (8192 x 256 x 7168 29.5 -> 24.5 us, 2048 x 2048 x 18432 68 -> 59, 300 x 7168 x 7168 24 -> 21).
+template <int BM, int WAVES_M, int WAVES_N, bool QUADS = false>
 struct Fp4Cfg {
     static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
     static constexpr int FM = WM / 16, FN = WN / 16;
@@ -361,12 +364,13 @@ struct Fp4Cfg {
     static_assert(WAVES_M * WAVES_N == 4 && LDS_BYTES <= 160 * 1024 && DA >= 2 && DB >= 2, "");
 
     // A wave's loads go out in the order X(k), Y(k), X(k+1), ...; X(k): scale words, then B of step k+DB; Y(k): A of step k+DA.
-    // Scale words of X(k), u = k % 4: A's of the next chunk in steps 0, 1 and, with DB = 2, 2 (into LDS), or in even steps of the
-    // next block (into registers); B's of the next block in even steps
+    // Scale words of X(k), u = k % 4: A's of the next chunk in steps 0, 1 and, with DB = 2, 2 (into LDS), or of the next block in
+    // even steps or (QUADS) of the next four blocks in step 0 (into registers); B's of the next block in even steps
     static constexpr int S_STEPS = DB == 2 ? 3 : 2;                                 // so that they are there in step 3
     static constexpr int S_EACH = (S_DMA + S_STEPS - 1) / S_STEPS;
     static constexpr int staged(int u) { return u >= S_STEPS ? 0 : u == S_STEPS - 1 ? S_DMA - u * S_EACH : S_EACH; }
-    static constexpr int scales(int u) { return staged(u) + (u % 2 ? 0 : FN + (STAGED ? 0 : FM)); }
+    static constexpr int direct(int u) { return STAGED || u % 2 || (QUADS && u) ? 0 : FM; }
+    static constexpr int scales(int u) { return staged(u) + direct(u) + (u % 2 ? 0 : FN); }
     // How many loads may be in flight at the second barrier of step k, when A and B of step k+1 and, in odd steps, the scale words
     // of X(k-1) have to be there: those behind the last one needed.
     static constexpr int in_flight(int u) {
@@ -374,7 +378,7 @@ struct Fp4Cfg {
         for (int d = 0;; ++d) {                        // X(k-d), then Y(k-d-1)
             if (DB <= d + 1) return n;                 // B of step k-d+DB
             n += B_DMA;
-            if (u % 2 && d == 1) return n;
+            if (u % 2 && d == 1) return n;             // (QUADS: needed in step 3, asked for in step 0)
             n += scales((u - d + 8) % 4);
             if (DA <= d + 2) return n;                 // A of step k-d-1+DA
             n += A_DMA;
@@ -383,11 +387,11 @@ struct Fp4Cfg {
 };
 
 // NT: B through non-temporal loads (one row tile reads it).
-template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, bool QUADS = false>
 __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, const RowTiles& rt, int v, int part) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty function
 #if defined(__HIP_DEVICE_COMPILE__)
-    using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
+    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, QUADS>;
     constexpr int WM = C::WM, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB, A_DMA = C::A_DMA, B_DMA = C::B_DMA;
     constexpr int kBAux = NT ? 2 : 0;
     uint8_t* const bring = smem + DA * C::A_BYTES;
@@ -435,14 +439,14 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int step = C::STAGED ? 8 * last_kc + 4 * ((lane >> 5) ^ h) + (lane & 3) : 4 * last_kb + g;
-        past_sf[h] = 4u * max(0, step - (nks - 1));
+        past_sf[h] = QUADS ? 16u * max(0, (last_kb & ~3) + g - last_kb) : 4u * max(0, step - (nks - 1));
     }
 #pragma unroll
     for (int f = 0; f < NSA; ++f) {
         if constexpr (C::STAGED)
             sa_off[f] = a_row(8 * (wave * NSA + f) + ((lane >> 2) & 7)) * (uint32_t)(args.K / 32) + 16u * ((lane >> 5) ^ (f & 1)) + 4u * (lane & 3);
         else
-            sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)(args.K / 32) + 4u * g;
+            sa_off[f] = a_row(wm * WM + f * 16 + l) * (uint32_t)(args.K / 32) + (QUADS ? 16u : 4u) * g;
     }
     const ByteSelect sel = byte_select(g);
     const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)args.a, 0, (int)(args.rows * (uint32_t)(args.K / 2)), kRsrcWord3);
@@ -464,9 +468,30 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                                                  kc * kBTileBytes + (i & 15) * kFragBytes, 0, kBAux);
     };
     // scale words of a block of two steps: A's as loaded, and by byte of the K step in the block as the products take them
-    uint32_t raw[FM], sa[2][FM], sb[2][FN];
+    uint32_t raw[FM], sa[2][FM], sb[2][FN], next[FM];
+    v4i quad[FM];
     auto load_sa = [&](int kb, int f) __attribute__((always_inline)) {
         raw[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[f] - (kb == last_kb ? past_sf[0] : 0u), kb * 16, 0);
+    };
+    // QUADS: lane 16b + i has row i's 16 bytes of block 4 kq + b (blocks past the last: its)
+    const int last_kq = last_kb >> 2;
+    auto load_quad = [&](int kq, int f) __attribute__((always_inline)) {
+        const int q = min(kq, last_kq);
+        quad[f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_asf, sa_off[f] - (q == last_kq ? past_sf[0] : 0u), q * 64, 0));
+    };
+    // the words of blocks 2 * pair and 2 * pair + 1, of the four in quad: bytes by block of 32 within the lane, then lane row and
+    // word changed places
+    auto take_quad = [&](int pair, int f) __attribute__((always_inline)) {
+        const uint32_t d0 = quad[f].x, d1 = quad[f].y, d2 = quad[f].z, d3 = quad[f].w;
+        const uint32_t a = __builtin_amdgcn_perm(d1, d0, 0x05010400u), b = __builtin_amdgcn_perm(d1, d0, 0x07030602u);
+        const uint32_t c = __builtin_amdgcn_perm(d3, d2, 0x05010400u), d = __builtin_amdgcn_perm(d3, d2, 0x07030602u);
+        const uint32_t w0 = __builtin_amdgcn_perm(c, a, 0x05040100u), w1 = __builtin_amdgcn_perm(c, a, 0x07060302u);
+        const uint32_t w2 = __builtin_amdgcn_perm(d, b, 0x05040100u), w3 = __builtin_amdgcn_perm(d, b, 0x07060302u);
+        const auto p02 = __builtin_amdgcn_permlane32_swap(w0, w2, false, false), p13 = __builtin_amdgcn_permlane32_swap(w1, w3, false, false);
+        const bool second = pair & 1;
+        const auto y = __builtin_amdgcn_permlane16_swap(second ? p02[1] : p02[0], second ? p13[1] : p13[0], false, false);
+        sa[0][f] = y[0];
+        next[f] = y[1];
     };
     auto load_sb = [&](int kb, int f, int set) __attribute__((always_inline)) {
         sb[set][f] = __builtin_amdgcn_raw_buffer_load_b32(rs_bsf, lane * 4 + (wn * FN + f) * 256, kb * kBScaleBlockBytes, kBAux);
@@ -525,11 +550,12 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
         op -= C::staged(u);
         if (u % 2 == 0) {
             const int kb = min((ks >> 1) + 1, last_kb);
-            if (!C::STAGED && op < FM) {
-                load_sa(kb, op);
+            if (op < C::direct(u)) {
+                if constexpr (QUADS) load_quad((ks >> 3) + ((ks >> 2) & 1), op);     // (every second time again: no branch)
+                else load_sa(kb, op);
                 return;
             }
-            if (!C::STAGED) op -= FM;
+            op -= C::direct(u);
             if (op < FN) {
                 load_sb(kb, op, set);
                 return;
@@ -542,6 +568,7 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
         if constexpr (C::STAGED) stage_sa(0, i);
+        else if constexpr (QUADS) load_quad(0, i);
         else load_sa(0, i);
     }
 #pragma unroll
@@ -564,7 +591,8 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         if constexpr (C::STAGED) read_sa(0, f);
-        sa[0][f] = scale_words(0, f);
+        if constexpr (QUADS) take_quad(0, f);
+        else sa[0][f] = scale_words(0, f);
     }
     Pair a_cur, a_nx;
     v4i bq[2][FN];
@@ -593,7 +621,11 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
                 if constexpr (ODD) {
                     // the next block's scale words have landed: no wait of the compiler's own for them
-                    if constexpr (!C::STAGED) {
+                    if constexpr (QUADS) {
+                        if (U == 3)
+#pragma unroll
+                            for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(quad[f]));
+                    } else if constexpr (!C::STAGED) {
 #pragma unroll
                         for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(raw[f]));
                     }
@@ -616,8 +648,11 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                         if (ODD && C::STAGED && t < FM) read_sa((ks >> 1) + 1, t);
                         constexpr int LATE = ROW - FM;
                         if (ODD && t >= LATE) {
-                            sa[SET ^ 1][t - LATE] = scale_words((ks >> 1) + 1, t - LATE);
+                            if constexpr (!QUADS) sa[SET ^ 1][t - LATE] = scale_words((ks >> 1) + 1, t - LATE);
+                            else if (U == 3) take_quad((ks >> 2) + 1, t - LATE);
+                            else sa[1][t - LATE] = next[t - LATE];
                             asm volatile("" : "+v"(sa[SET ^ 1][t - LATE]));
+                            if (QUADS && U == 3) asm volatile("" : "+v"(next[t - LATE]));
                         }
                         if (t % Y_SPACE == 0 && t / Y_SPACE < A_DMA) load_a(ks + DA, t / Y_SPACE);
                     } else if (fm > 0 && ((fm - 1) * ROW + t) % X_SPACE == 0) {
@@ -710,14 +745,14 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
 #endif
 }
 
-template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT>
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, bool QUADS>
 __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void gemm_fp4_tiled(GemmFp4Args args) {
-    using C = Fp4Cfg<BM, WAVES_M, WAVES_N>;
+    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, QUADS>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     const RowTiles rt = row_tiles(args, BM);
     const int v = xcd_tile(rt.total * ((args.N + kBN - 1) / kBN), blockIdx.x);
     if (v < 0) return;
-    tiled_part<BM, WAVES_M, WAVES_N, F32, NT>(args, smem, rt, v, 0);
+    tiled_part<BM, WAVES_M, WAVES_N, F32, NT, QUADS>(args, smem, rt, v, 0);
 }
 
 // 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where those are no more than
@@ -739,14 +774,14 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rounds(GemmFp4Args args) {
     else tiled_part<128, 2, 2, F32, false>(args, smem, rt, full + u / 2, u % 2);
 }
 
-template <int BM, int WAVES_M, int WAVES_N>
+template <int BM, int WAVES_M, int WAVES_N, bool QUADS = false>
 hipError_t launch_tiled(unsigned grid, bool nt, const GemmFp4Args& a, hipStream_t stream) {
     if (a.out_f32) {
-        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, true><<<grid, 256, 0, stream>>>(a);
-        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, false><<<grid, 256, 0, stream>>>(a);
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, true, QUADS><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, false, QUADS><<<grid, 256, 0, stream>>>(a);
     } else {
-        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, true><<<grid, 256, 0, stream>>>(a);
-        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, false><<<grid, 256, 0, stream>>>(a);
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, true, QUADS><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, false, QUADS><<<grid, 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -843,7 +878,9 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
             break;
         }
         case Fp4Kernel::kTiled128: return launch_tiled<128, 2, 2>((unsigned)grid, plan.stream, a, stream);
-        case Fp4Kernel::kTiled64: return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
+        case Fp4Kernel::kTiled64:
+            if (a.K % 512 == 0) return launch_tiled<64, 1, 4, true>((unsigned)grid, plan.stream, a, stream);
+            return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x32: return launch_skinny<4, 2, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 2>(plan.stream, a, stream);
