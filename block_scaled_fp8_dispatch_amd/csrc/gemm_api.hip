@@ -459,7 +459,7 @@ int moe_fp4_gemm(void* d, int32_t d_type, const uint8_t* a, const uint8_t* a_sf,
     const GemmWs W = gemm_ws(m, 1);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
-    const Fp4Plan plan = fp4_plan(1, m, m, false, n, k);
+    const Fp4Plan plan = fp4_plan(1, m, m, m, false, n, k);
     const int BM = plan.block_m;
     GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, 1, n, k, packed_b, W, BM, cdiv(m, BM));
     g.dense_rows = m;
@@ -480,7 +480,7 @@ int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Fp4Plan plan = fp4_plan(groups, (double)m / groups, m, true, n, k);
+    const Fp4Plan plan = fp4_plan(groups, (double)m / groups, m, m, true, n, k);
     const int BM = plan.block_m;
     if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
     GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, W, BM, cdiv(m, BM) + groups);
@@ -505,7 +505,7 @@ int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (max_m == 0) return MOE_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int rows_each = expected_m < 1 ? 1 : expected_m < max_m ? expected_m : max_m;
-    const Fp4Plan plan = fp4_plan(groups, rows_each, (int)rows, true, n, k);
+    const Fp4Plan plan = fp4_plan(groups, rows_each, max_m, (int)rows, true, n, k);
     const int BM = plan.block_m;
     GemmFp4Args g = fp4_args(d, d_type, a, a_sf, (int)rows, groups, n, k, packed_b, W, BM, groups * cdiv(max_m, BM));
     // one wave's load of the counts in the GEMM's prologue instead of a launch

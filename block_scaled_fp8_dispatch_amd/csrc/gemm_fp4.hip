@@ -804,33 +804,41 @@ hipError_t launch_skinny(bool nt, const GemmFp4Args& a, hipStream_t stream) {
 }
 
 // Microseconds of a product with each kernel. Tiled: rounds of the workgroups that the CUs hold, each fixed + step per 128 K
-// (64 rows: two on a CU, a last round of one on a CU takes 0.58 of it). Skinny: fixed + the larger of wave per pair of K steps
-// that a wave takes and, per 256 workgroups, tile + step per 128 K; + each per 256 workgroups. Fitted to 90 products from 1 x 16
-// x 128 to 7698 x 2704 x 3200 and 31 groups of about 47 rows, each timed with every kernel, weights from memory, and the tiled
-// ones to 4096 x 4096 x 18432: what the model picks is 2 % slower than the best of the kernels on average, half again as slow at
-// worst (64 x 4096 x 4096).
+// (64 rows: two on a CU, a last round of one on a CU takes 0.57 of it, and where K is a multiple of 512 a step 0.9). Skinny:
+// fixed + the larger of wave per pair of K steps that a wave takes and, per 256 workgroups, step per 128 K; + each per 256
+// workgroups. Fitted to 260 products from 1 x 16 x 128 to 7698 x 2704 x 3200, 512 x 4096 x 7168 and 32 groups of about 150 rows,
+// each timed with every kernel, weights from memory: what the model picks is 1.8 % slower than the best of the kernels on
+// average, a third slower at worst (77 x 2944 x 5120).
 // A masked or listed product's 64-row tiles with few rows leave most workgroups of 16 or 32 rows without any and the others to
 // a part of the CUs, so that there all count.
 struct Cost {
     Fp4Kernel kernel;
     int block_m, bm, bn;       // rows of its row tiles, rows and columns per workgroup
     int waves;                 // sharing K; 0: tiled
-    double fixed, step, wave, tile, each;
+    double fixed, step, wave, each;
 };
-constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 6.8, 0.846, 0, 0, 0},
-                           {Fp4Kernel::kTiled128, 128, 128, 256, 0, 5.7, 0.504, 0, 0, 0},
-                           {Fp4Kernel::kTiled64, 64, 64, 256, 0, 6.4, 0.729, 0, 0, 0},
-                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 0.65, 0.245, 3.26, 0.06, 3.11},
-                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 0.67, 0.169, 2.63, 2.29, 0.20},
-                           {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 0.98, 0.179, 2.45, 1.54, 0.64},
-                           {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.45, 0.121, 1.49, 0.02, 0.69},
-                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.63, 0.080, 1.07, 0.00, 0.52},
-                           {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 2.20, 0.045, 1.08, 1.00, 0.16}};
-constexpr double kAlone64 = 0.58;
+constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 7.9, 0.8, 0, 0},
+                           {Fp4Kernel::kTiled128, 128, 128, 256, 0, 5.75, 0.504, 0, 0},
+                           {Fp4Kernel::kTiled64, 64, 64, 256, 0, 6.0, 0.729, 0, 0},
+                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 1.50, 0.237, 3.32, 3.95},
+                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 0.44, 0.237, 2.96, 3.05},
+                           {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 1.66, 0.198, 2.24, 1.50},
+                           {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.66, 0.150, 1.62, 0.27},
+                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.14, 0.087, 1.27, 0.63},
+                           {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 2.08, 0.065, 0.98, 0.65}};
+constexpr double kAlone64 = 0.574, kQuads64 = 0.895;
+
+// Row tiles of bm rows. Groups of unknown length: spread from half to one and a half times the expected rows
+double row_tiles_of(int groups, double rows, int most, bool ragged, int bm) {
+    if (!ragged) return groups * std::ceil(rows / bm);
+    double tiles = 0;
+    for (int i = 0; i < 8; ++i) tiles += std::ceil(std::min<double>(most, rows * (9 + 2 * i) / 16) / bm);
+    return groups * tiles / 8;
+}
 
 }  // namespace
 
-Fp4Plan fp4_plan(int groups, double rows, int max_rows, bool ragged, int N, int K) {
+Fp4Plan fp4_plan(int groups, double rows, int most, int max_rows, bool ragged, int N, int K) {
     Fp4Plan best{};
     double least = 0;
     const int steps = K / kBK;
@@ -839,22 +847,21 @@ Fp4Plan fp4_plan(int groups, double rows, int max_rows, bool ragged, int N, int 
         // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
         const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cols;
         if (c.kernel != Fp4Kernel::kTiled128 && grid * (c.waves ? c.waves * 64 : 256) >= (1ull << 32)) continue;
-        // groups of unknown length end in a tile that is half full on average
-        double mt = groups * (!ragged ? std::ceil(rows / c.bm) : rows > c.bm ? rows / c.bm + 0.5 : 1.0);
-        if (ragged && c.bm < 64) mt = groups * std::max(1.0, rows / 64 + 0.5) * (64 / c.bm);
-        const double tiles = std::ceil(mt) * cols;
+        const int unit = ragged ? std::max(c.bm, 64) : c.bm;
+        const double tiles = std::ceil(row_tiles_of(groups, rows, most, ragged, unit) * (unit / c.bm)) * cols;
         double t = 0;
         if (c.waves) {
             const double share = tiles / kCus;
-            t = c.fixed + std::max(c.wave * cdiv(cdiv(steps, 2), c.waves), share * (c.tile + c.step * steps)) + share * c.each;
+            t = c.fixed + std::max(c.wave * cdiv(cdiv(steps, 2), c.waves), share * c.step * steps) + share * c.each;
         } else {
-            const double round = c.fixed + c.step * steps, slots = c.kernel == Fp4Kernel::kTiled64 ? 2 * kCus : kCus;
+            const bool two = c.kernel == Fp4Kernel::kTiled64;
+            const double round = c.fixed + c.step * (two && K % 512 == 0 ? kQuads64 : 1.0) * steps, slots = two ? 2 * kCus : kCus;
             const double rounds = std::floor(tiles / slots), rem = tiles - rounds * slots;
             t = rounds * round;
             // the parts of the 256-row tiles' last round: of 64 rows, kCosts[2], or 128, kCosts[1]
             if (c.kernel == Fp4Kernel::kTiled256 && rem > 0 && rem <= kCus / 4) t += kCosts[2].fixed + kCosts[2].step * steps;
             else if (c.kernel == Fp4Kernel::kTiled256 && rem > 0 && rem <= kCus / 2) t += kCosts[1].fixed + kCosts[1].step * steps;
-            else if (c.kernel == Fp4Kernel::kTiled64 && rem > 0 && rem <= kCus) t += kAlone64 * round;
+            else if (two && rem > 0 && rem <= kCus) t += kAlone64 * round;
             else if (rem > 0) t += round;
         }
         if (best.block_m == 0 || t < least) {
@@ -883,8 +890,8 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
             return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x32: return launch_skinny<4, 2, 8, 1>(plan.stream, a, stream);
-        case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 2>(plan.stream, a, stream);
-        case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 2>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 1>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny16x32: return launch_skinny<1, 2, 8, 3>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny16: return launch_skinny<1, 1, 16, 2>(plan.stream, a, stream);
     }

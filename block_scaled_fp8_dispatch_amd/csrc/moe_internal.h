@@ -244,14 +244,14 @@ constexpr int kMaskedGroups = 64;
 enum class Fp4Kernel {
     kTiled256, kTiled128, kTiled64, kSkinny64x64, kSkinny64x32, kSkinny32x64, kSkinny32x32, kSkinny16x32, kSkinny16
 };
-// The kernel for groups of about rows_per_group rows (ragged: known on the device only; at most max_rows in all), the
+// The kernel for groups of about rows_per_group rows (ragged: known on the device only; at most `most` each and max_rows in all), the
 // height of its row tiles, and whether one row tile per group reads B
 struct Fp4Plan {
     Fp4Kernel kernel;
     int block_m;
     bool stream;
 };
-Fp4Plan fp4_plan(int groups, double rows_per_group, int max_rows, bool ragged, int N, int K);
+Fp4Plan fp4_plan(int groups, double rows_per_group, int most, int max_rows, bool ragged, int N, int K);
 hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_t stream);
 
 // Root-mean-square norm with FP8 output (norm.hip)
