@@ -621,10 +621,11 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(WN_) : "memory");
                 if constexpr (ODD) {
                     // the next block's scale words have landed: no wait of the compiler's own for them
+                    // (QUADS: needed in step 3 only; a use in step 1 keeps the loads, which the waits count, in the steps behind the
+                    // loop too)
                     if constexpr (QUADS) {
-                        if (U == 3)
 #pragma unroll
-                            for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(quad[f]));
+                        for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(quad[f]));
                     } else if constexpr (!C::STAGED) {
 #pragma unroll
                         for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(raw[f]));
@@ -821,7 +822,6 @@ constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 7.9, 0.8, 0,
                            {Fp4Kernel::kTiled128, 128, 128, 256, 0, 5.75, 0.504, 0, 0},
                            {Fp4Kernel::kTiled64, 64, 64, 256, 0, 6.0, 0.729, 0, 0},
                            {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 1.50, 0.237, 3.32, 3.95},
-                           {Fp4Kernel::kSkinny64x32, 64, 64, 32, 8, 0.44, 0.237, 2.96, 3.05},
                            {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 1.66, 0.198, 2.24, 1.50},
                            {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.66, 0.150, 1.62, 0.27},
                            {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.14, 0.087, 1.27, 0.63},
@@ -889,7 +889,6 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
             if (a.K % 512 == 0) return launch_tiled<64, 1, 4, true>((unsigned)grid, plan.stream, a, stream);
             return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
-        case Fp4Kernel::kSkinny64x32: return launch_skinny<4, 2, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny16x32: return launch_skinny<1, 2, 8, 3>(plan.stream, a, stream);

@@ -242,7 +242,7 @@ struct GemmFp4Args {
 };
 constexpr int kMaskedGroups = 64;
 enum class Fp4Kernel {
-    kTiled256, kTiled128, kTiled64, kSkinny64x64, kSkinny64x32, kSkinny32x64, kSkinny32x32, kSkinny16x32, kSkinny16
+    kTiled256, kTiled128, kTiled64, kSkinny64x64, kSkinny32x64, kSkinny32x32, kSkinny16x32, kSkinny16
 };
 // The kernel for groups of about rows_per_group rows (ragged: known on the device only; at most `most` each and max_rows in all), the
 // height of its row tiles, and whether one row tile per group reads B
