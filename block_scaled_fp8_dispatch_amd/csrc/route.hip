@@ -471,7 +471,7 @@ __global__ __launch_bounds__(1024) void gemm_layout_kernel(int G, int max_m,
     }
 }
 
-// Rows of the FP8 x FP8 contiguous GEMM grouped by their id in one launch: as the routing above,
+// Rows of the FP8 x FP8 and FP4 x FP4 contiguous GEMMs grouped by their id in one launch: as the routing above,
 // but a row's place within its group does not matter (each row of D depends on its own row of A
 // only), so places are handed out by LDS atomics, one per wave and group. Full tiles first, then
 // each group's last, partly filled one.
