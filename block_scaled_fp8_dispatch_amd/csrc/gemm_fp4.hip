@@ -10,7 +10,7 @@
 // Skinny kernel. Operands go from memory straight into the registers of the wave that multiplies them: 16 bytes a lane are a
 // whole operand, and the two K steps of a pair use whole 128-byte lines of A's rows. A workgroup owns a tile of BM rows x FN
 // fragments of columns, and its WAVES waves share K, taking a pair in turn and keeping sums of their own, which meet in LDS at
-// the end. A wave keeps DEPTH pairs in flight. Bound by latency and, with more of them on a CU, by its loads (64 x 4096 x 4096 6.9 us,
+// the end. A wave keeps DEPTH pairs in flight. Bound by latency and, with more of them on a CU, by its loads (64 x 4096 x 4096 7.0 us,
 // 33 x 7168 x 2048 6.1, 1 x 7168 x 18432 13.6: 5.2 TB/s of weights).
 //
 // Tiled kernel. Tiles of 256, 128 or 64 rows x 256 columns in four waves, steps of 256 of K through rings in LDS that are filled
@@ -138,14 +138,13 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
     const int f0 = vin / gu * FN, tile = f0 >> 4, frag = f0 & 15;   // fragments frag .. frag + FN-1 of a 256-column tile
     const int nks = p.K / kBK;
 
-    uint32_t a_off[FM], sa_off[FM];
+    auto a_row = [&](int r) __attribute__((always_inline)) -> uint32_t {
+        const int d = d_row(r);
+        return d < 0 ? 0u : (uint32_t)d;                         // padding rows read row 0 and are never stored
+    };
+    uint32_t a_off[FM];
 #pragma unroll
-    for (int f = 0; f < FM; ++f) {
-        const int d = d_row(f * 16 + l);
-        const uint32_t row = d < 0 ? 0u : (uint32_t)d;           // padding rows read row 0 and are never stored
-        a_off[f] = row * (uint32_t)(p.K / 2) + 16u * g;
-        sa_off[f] = row * (uint32_t)(p.K / 32);
-    }
+    for (int f = 0; f < FM; ++f) a_off[f] = a_row(f * 16 + l) * (uint32_t)(p.K / 2) + 16u * g;
     const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, (int)(p.rows * (uint32_t)(p.K / 2)), kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_asf = __builtin_amdgcn_make_buffer_rsrc((void*)p.a_sf, 0, (int)(p.rows * (uint32_t)(p.K / 32)), kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
@@ -163,9 +162,41 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
         v4i a[2][FM], b[2][FN];
         uint32_t sa[FM], sb[FN];
     } st[DEPTH];
-    // A's scales: lane 16g + i loads the four bytes of row i for the pair's step g % 2, takes the other step's from the lane 16
-    // away, and picks byte g of both
+    // A's scales, 4 bytes a row and K step. A load costs by the lines it touches, and the words of 16 rows lie in 16. With few
+    // rows lane 16g + i loads row i's word of the pair's step g % 2 and takes the other step's from the lane 16 away. With 64 rows
+    // (SHARED) the workgroup brings the words of 256 K steps into LDS, 16 of a row by 16 lanes, rows two banks apart, and a lane
+    // reads both steps' from there (192 x 4096 x 7168 16.3 -> 14.2 us, 64 x 7168 x 18432 40 -> 33.4; the kernel of 32 x 64 28 ->
+    // 25.5 there, but 5.6 -> 6.4 at 16 x 7168 x 2048 by the barrier). Of both words it picks byte g.
+    constexpr bool SHARED = FM == 4;
+    constexpr int kWords = 256, kRowWords = kWords + 2;
+    constexpr int GROUPS = WAVES * 4, RG = BM < GROUPS ? BM : GROUPS, ROWS = BM / RG, BATCH = 4;   // of 16 lanes; rows at once, in turn
+    static_assert(!SHARED || RG == GROUPS, "every group of lanes has rows of its own");
+    __shared__ __attribute__((aligned(16))) uint32_t a_scales[SHARED ? BM * kRowWords : 1];
     const uint32_t sel = (uint32_t)g | (uint32_t)(g + 4) << 8 | 0x0c0c0000u;
+    constexpr int NSA = SHARED ? ROWS : FM;
+    uint32_t sa_off[NSA];
+#pragma unroll
+    for (int r = 0; r < NSA; ++r) sa_off[r] = a_row(SHARED ? (tid >> 4) + r * RG : r * 16 + l) * (uint32_t)(p.K / 32);
+    auto stage_scales = [&](int first) __attribute__((always_inline)) {
+        const int words = min(kWords, nks - first);
+        for (int base = 0; base < words; base += 16 * BATCH) {
+            uint32_t x[BATCH][ROWS];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const int w = base + 16 * b + l;
+                    if (w < words) x[b][r] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[r] + 4u * (first + w), 0, 0);
+                }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const int w = base + 16 * b + l;
+                    if (w < words) a_scales[((tid >> 4) + r * RG) * kRowWords + w] = x[b][r];
+                }
+        }
+    };
     // Pair `i` of this wave. The second step of the last pair may lie past K: its loads repeat the first's, and its scales are 0
     // on both sides (B's as packed), 2^-254, by which its products vanish
     auto load = [&](Stage& s, int i) __attribute__((always_inline)) {
@@ -180,9 +211,11 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
             for (int f = 0; f < FM; ++f)
                 s.a[h][f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_a, a_off[f], at * (kBK / 2), 0));
         }
-        const uint32_t at = 4u * (uint32_t)min(ks + (g & 1), nks - 1);
+        if constexpr (!SHARED) {
+            const uint32_t at = 4u * (uint32_t)min(ks + (g & 1), nks - 1);
 #pragma unroll
-        for (int f = 0; f < FM; ++f) s.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[f] + at, 0, 0);
+            for (int f = 0; f < FM; ++f) s.sa[f] = __builtin_amdgcn_raw_buffer_load_b32(rs_asf, sa_off[f] + at, 0, 0);
+        }
         // both steps' bytes of a fragment lie together
 #pragma unroll
         for (int n = 0; n < FN; ++n)
@@ -193,8 +226,13 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
         uint32_t sa[FM];
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
-            const auto q = __builtin_amdgcn_permlane16_swap(s.sa[f], s.sa[f], false, false);
-            sa[f] = __builtin_amdgcn_perm(q[1], q[0], sel) & keep;
+            if constexpr (SHARED) {
+                const uint2 w = *reinterpret_cast<const uint2*>(a_scales + (f * 16 + l) * kRowWords + (2 * (i * WAVES + wave) & (kWords - 1)));
+                sa[f] = __builtin_amdgcn_perm(w.y, w.x, sel) & keep;
+            } else {
+                const auto q = __builtin_amdgcn_permlane16_swap(s.sa[f], s.sa[f], false, false);
+                sa[f] = __builtin_amdgcn_perm(q[1], q[0], sel) & keep;
+            }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -209,19 +247,29 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
                 }
             }
     };
-    // n pairs of this wave: DEPTH in flight, then each multiplied and its registers loaded again while there are more
-    const int pairs = (nks + 1) >> 1, n = (pairs - wave + WAVES - 1) / WAVES;
-    if (n < DEPTH) {
+    // All pairs (SHARED: those whose scales LDS holds) at a time, this wave's i0 to n-1: DEPTH in flight, then each multiplied and
+    // its registers loaded again while there are more
+    const int pairs = (nks + 1) >> 1, chunk = SHARED ? kWords / 2 : pairs;
+    for (int first = 0; first < pairs; first += chunk) {
+        const int i0 = first / WAVES, n = (min(pairs, first + chunk) - wave + WAVES - 1) / WAVES;
+        if constexpr (SHARED) {
+            if (first > 0) __syncthreads();                     // every wave is through with the words before
+            stage_scales(2 * first);
+        }
+        if (n - i0 < DEPTH) {
 #pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i)
-            if (i < n) load(st[i], i);
+            for (int i = 0; i < DEPTH - 1; ++i)
+                if (i0 + i < n) load(st[i], i0 + i);
+            if constexpr (SHARED) __syncthreads();
 #pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i)
-            if (i < n) multiply(st[i], i);
-    } else {
+            for (int i = 0; i < DEPTH - 1; ++i)
+                if (i0 + i < n) multiply(st[i], i0 + i);
+            continue;
+        }
 #pragma unroll
-        for (int i = 0; i < DEPTH; ++i) load(st[i], i);
-        int i = 0;
+        for (int i = 0; i < DEPTH; ++i) load(st[i], i0 + i);
+        if constexpr (SHARED) __syncthreads();
+        int i = i0;
         // the last DEPTH pairs, the first of them in stage S
         auto rest = [&](auto first) __attribute__((always_inline)) {
             constexpr int S = decltype(first)::value;
@@ -243,12 +291,9 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_fp4_skinny(GemmFp4Args p) {
             if (turn(IntC<0>{})) break;
             if constexpr (DEPTH > 1)
                 if (turn(IntC<1 % DEPTH>{})) break;
-            if constexpr (DEPTH > 2)
-                if (turn(IntC<2 % DEPTH>{})) break;
-            if constexpr (DEPTH > 3)
-                if (turn(IntC<3 % DEPTH>{})) break;
         }
     }
+    static_assert(DEPTH <= 2, "");
 
     // Row of the tile and column of D of a lane's sums: rows 16f + 4g + r, columns col .. col + FN-1 (lane column j of fragment
     // f is column 128 * (f / 8) + 8j + f % 8 of its tile; all FN or none: N is a multiple of 16)
@@ -821,7 +866,7 @@ hipError_t launch_skinny(bool nt, const GemmFp4Args& a, hipStream_t stream) {
 // fixed + the larger of wave per pair of K steps that a wave takes and, per 256 workgroups, step per 128 K; + each per 256
 // workgroups. Fitted to 260 products from 1 x 16 x 128 to 7698 x 2704 x 3200, 512 x 4096 x 7168 and 32 groups of about 150 rows,
 // each timed with every kernel, weights from memory: what the model picks is 1.8 % slower than the best of the kernels on
-// average, a third slower at worst (77 x 2944 x 5120).
+// average, a third slower at worst (24 groups of about one row, 320 x 2816).
 // A masked or listed product's 64-row tiles with few rows leave most workgroups of 16 or 32 rows without any and the others to
 // a part of the CUs, so that there all count.
 struct Cost {
@@ -833,10 +878,10 @@ struct Cost {
 constexpr Cost kCosts[] = {{Fp4Kernel::kTiled256, 256, 256, 256, 0, 7.9, 0.8, 0, 0},
                            {Fp4Kernel::kTiled128, 128, 128, 256, 0, 5.75, 0.504, 0, 0},
                            {Fp4Kernel::kTiled64, 64, 64, 256, 0, 6.0, 0.729, 0, 0},
-                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 1.50, 0.237, 3.32, 3.95},
+                           {Fp4Kernel::kSkinny64x64, 64, 64, 64, 8, 1.50, 0.237, 3.00, 3.95},
                            {Fp4Kernel::kSkinny32x64, 64, 32, 64, 8, 1.66, 0.198, 2.24, 1.50},
                            {Fp4Kernel::kSkinny32x32, 64, 32, 32, 8, 1.66, 0.150, 1.62, 0.27},
-                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.14, 0.087, 1.27, 0.63},
+                           {Fp4Kernel::kSkinny16x32, 64, 16, 32, 8, 1.14, 0.087, 1.27, 0.40},
                            {Fp4Kernel::kSkinny16, 64, 16, 16, 16, 2.08, 0.065, 0.98, 0.65}};
 constexpr double kAlone64 = 0.574, kQuads64 = 0.895;
 
@@ -903,7 +948,7 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
         case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 1>(plan.stream, a, stream);
-        case Fp4Kernel::kSkinny16x32: return launch_skinny<1, 2, 8, 3>(plan.stream, a, stream);
+        case Fp4Kernel::kSkinny16x32: return launch_skinny<1, 2, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny16: return launch_skinny<1, 1, 16, 2>(plan.stream, a, stream);
     }
     return hipGetLastError();

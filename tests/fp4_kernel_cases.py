@@ -16,6 +16,7 @@ CASES = [
     ("dense", 3100, 1, 368, 640, 0, "tiled 64", False),
     ("dense", 300, 1, 4272, 2560, 0, "tiled 64", False),
     ("dense", 2100, 1, 368, 4608, 0, "skinny 64x64", False),
+    ("dense", 900, 1, 640, 40064, 0, "skinny 64x64", False),     # scales of more K steps than LDS holds at once
     ("dense", 128, 1, 2608, 3712, 0, "skinny 32x64", False),
     ("dense", 2600, 1, 112, 896, 0, "skinny 32x32", False),
     ("dense", 700, 1, 256, 128, 0, "skinny 16x32", False),
@@ -33,7 +34,7 @@ CASES = [
     ("contiguous", 1000, 10, 256, 3712, 0, "skinny 32x64", False),
     ("contiguous", 1747, 66, 16, 5120, 0, "skinny 32x64", True),
     ("contiguous", 1300, 5, 528, 256, 0, "skinny 32x32", False),
-    ("contiguous", 100, 10, 368, 896, 0, "skinny 32x32", True),
+    ("contiguous", 150, 10, 480, 1152, 0, "skinny 32x32", True),
     ("contiguous", 1000, 10, 48, 896, 0, "skinny 16x32", False),
     ("contiguous", 16, 3, 368, 896, 0, "skinny 16x32", True),
     ("contiguous", 300, 3, 48, 4608, 0, "skinny 16", False),
