@@ -402,18 +402,21 @@ constexpr int kBStep = 2 * kBTileBytes;
 // Bytes of a chunk (4 steps) of a row's scales
 constexpr int kChunkRow = 4 * kStep / 32;
 
-// QUADS: A's scale words straight into registers, a block's 16 bytes a lane and load and four blocks an instruction, instead of 4
-// bytes and one block: a load costs by the lines it touches, 16 rows' in either form. K is a multiple of 512, so that rows end
-// with a block (8192 x 256 x 7168 29.5 -> 24.5 us, 2048 x 2048 x 18432 68 -> 59, 300 x 7168 x 7168 24 -> 21).
-template <int BM, int WAVES_M, int WAVES_N, bool QUADS = false>
+// A's scale words: through LDS where there is room, or straight into registers (64 rows with two workgroups on a CU, whose
+// operands fill its LDS). There kQuads loads a block's 16 bytes a lane and four blocks an instruction, kWords 4 bytes and one
+// block: a load costs by the lines it touches, 16 rows' in either form. kQuads needs rows of whole blocks, K a multiple of 512
+// (8192 x 256 x 7168 29.5 -> 24.5 us, 2048 x 2048 x 18432 68 -> 59, 300 x 7168 x 7168 24 -> 21).
+enum class AScales { kStaged, kQuads, kWords };
+
+template <int BM, int WAVES_M, int WAVES_N, AScales S>
 struct Fp4Cfg {
     static constexpr int WM = BM / WAVES_M, WN = kBN / WAVES_N;
     static constexpr int FM = WM / 16, FN = WN / 16;
     static constexpr int A_BYTES = BM * kARow;
-    // A's scale words through LDS, where there is room (64 rows: two workgroups share the CU's)
-    static constexpr bool STAGED = BM >= 128;
+    static constexpr bool STAGED = S == AScales::kStaged, QUADS = S == AScales::kQuads;
+    static_assert(STAGED || BM == 64, "");
     static constexpr int S_BYTES = STAGED ? BM * kChunkRow : 0;
-    // ring slots: 144 KB with 256 rows, 152 with 128, 80 with 64
+    // ring slots: 144 KB with 256 rows, 152 with 128, 80 with 64 (84 staged)
     static constexpr int DA = BM == 128 ? 3 : 2, DB = BM == 128 ? 3 : 2;
     static constexpr int LDS_BYTES = DA * A_BYTES + DB * kBStep + 2 * S_BYTES;
     static constexpr int A_DMA = A_BYTES / 1024 / 4, B_DMA = kBStep / 1024 / 4;   // 1 KB loads per wave and step
@@ -444,11 +447,12 @@ struct Fp4Cfg {
 };
 
 // NT: B through non-temporal loads (one row tile reads it).
-template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, bool QUADS = false>
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, AScales S = AScales::kStaged>
 __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Args& args, uint8_t* smem, const RowTiles& rt, int v, int part) {
     // gfx950 buffer descriptors are a device-only type: the host pass sees an empty function
 #if defined(__HIP_DEVICE_COMPILE__)
-    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, QUADS>;
+    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, S>;
+    constexpr bool QUADS = C::QUADS;
     constexpr int WM = C::WM, FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB, A_DMA = C::A_DMA, B_DMA = C::B_DMA;
     constexpr int kBAux = NT ? 2 : 0;
     uint8_t* const bring = smem + DA * C::A_BYTES;
@@ -803,14 +807,14 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
 #endif
 }
 
-template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, bool QUADS>
+template <int BM, int WAVES_M, int WAVES_N, bool F32, bool NT, AScales S>
 __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void gemm_fp4_tiled(GemmFp4Args args) {
-    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, QUADS>;
+    using C = Fp4Cfg<BM, WAVES_M, WAVES_N, S>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS_BYTES];
     const RowTiles rt = row_tiles(args, BM);
     const int v = xcd_tile(rt.total * ((args.N + kBN - 1) / kBN), blockIdx.x);
     if (v < 0) return;
-    tiled_part<BM, WAVES_M, WAVES_N, F32, NT, QUADS>(args, smem, rt, v, 0);
+    tiled_part<BM, WAVES_M, WAVES_N, F32, NT, S>(args, smem, rt, v, 0);
 }
 
 // 256 x 256 tiles in rounds of one per CU; a last round at most half full runs as parts of 64 rows where those are no more than
@@ -832,14 +836,14 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_rounds(GemmFp4Args args) {
     else tiled_part<128, 2, 2, F32, false>(args, smem, rt, full + u / 2, u % 2);
 }
 
-template <int BM, int WAVES_M, int WAVES_N, bool QUADS = false>
+template <int BM, int WAVES_M, int WAVES_N, AScales S>
 hipError_t launch_tiled(unsigned grid, bool nt, const GemmFp4Args& a, hipStream_t stream) {
     if (a.out_f32) {
-        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, true, QUADS><<<grid, 256, 0, stream>>>(a);
-        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, false, QUADS><<<grid, 256, 0, stream>>>(a);
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, true, S><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, true, false, S><<<grid, 256, 0, stream>>>(a);
     } else {
-        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, true, QUADS><<<grid, 256, 0, stream>>>(a);
-        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, false, QUADS><<<grid, 256, 0, stream>>>(a);
+        if (nt) gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, true, S><<<grid, 256, 0, stream>>>(a);
+        else gemm_fp4_tiled<BM, WAVES_M, WAVES_N, false, false, S><<<grid, 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -941,10 +945,10 @@ hipError_t launch_gemm_fp4(const Fp4Plan& plan, const GemmFp4Args& a, hipStream_
             else gemm_fp4_rounds<false><<<blocks, 256, 0, stream>>>(a);
             break;
         }
-        case Fp4Kernel::kTiled128: return launch_tiled<128, 2, 2>((unsigned)grid, plan.stream, a, stream);
+        case Fp4Kernel::kTiled128: return launch_tiled<128, 2, 2, AScales::kStaged>((unsigned)grid, plan.stream, a, stream);
         case Fp4Kernel::kTiled64:
-            if (a.K % 512 == 0) return launch_tiled<64, 1, 4, true>((unsigned)grid, plan.stream, a, stream);
-            return launch_tiled<64, 1, 4>((unsigned)grid, plan.stream, a, stream);
+            if (a.K % 512 == 0) return launch_tiled<64, 1, 4, AScales::kQuads>((unsigned)grid, plan.stream, a, stream);
+            return launch_tiled<64, 1, 4, AScales::kWords>((unsigned)grid, plan.stream, a, stream);
         case Fp4Kernel::kSkinny64x64: return launch_skinny<4, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x64: return launch_skinny<2, 4, 8, 1>(plan.stream, a, stream);
         case Fp4Kernel::kSkinny32x32: return launch_skinny<2, 2, 8, 1>(plan.stream, a, stream);
