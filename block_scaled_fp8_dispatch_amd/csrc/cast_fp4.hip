@@ -39,10 +39,12 @@ typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
-// Past 2^23 elements (what the L2s do not hold anyway) loads and stores go past the caches (NT), and a thread has several
-// groups in flight; below, one (FP32 36864 x 7168 to FP4 208 us with one group, 208 with two and NT; bf16 8192 x 7168 27.2 and
-// 25.1; back 294 us with one, 207 with four, 36.2 and 25.8; 33 x 2048 back 2.28 us with one, 2.41 with four)
-constexpr size_t kPastCaches = size_t(1) << 23;
+// From 3 * 2^20 elements on loads and stores go past the caches (NT), and a thread has several groups in flight; below, one. FP32
+// 36864 x 7168 to FP4 208 us with one group, 208 with two and NT; bf16 8192 x 7168 27.2 and 25.1; back 294 us with one, 207 with four,
+// 36.2 and 25.8. 1000 x 7168 to FP4 5.6 and 4.9, back 6.4 and 5.0, from FP32 7.9 and 7.8, back 11.3 and 7.8; 256 x 7168, below,
+// 3.1 and 3.2, back 2.8 and 3.4, FP32 3.5 and 3.8, 3.6 and 4.3; behind the kernel that wrote the rows, 1000 x 4096 there and back gains
+// 3 us of 24, 400 x 7168 loses 1.4 of 18.
+constexpr size_t kPastCaches = size_t(3) << 20;
 template <bool NT>
 constexpr int kUnitsTo = NT ? 2 : 1;
 template <bool NT>

@@ -11,8 +11,6 @@
 // 128-column block, whose largest magnitude is four steps within them. One pass over memory: 8192 x 7168 with a residual read and
 // written moves 411 MB in 68 us, 6.0 TB/s, where a copy moves 5.1; 515 x 18432 with every output 85.6 MB in 19. Few rows are two
 // barriers, the loads' and the sum's latency (16 x 7168 3.1 us in a graph, an empty launch 1.95).
-#include <algorithm>
-
 #include "moe_internal.h"
 #include "moe_serving.h"
 
@@ -40,6 +38,7 @@ __device__ inline void put(void* p, const V& v) {
 }
 
 constexpr int kMaxThreads = 1024;
+constexpr int kCus = 256;                 // compute units of an MI355X
 
 // The sum over 16 lanes, in each of them: neighbours, pairs, the mirrored half row, the mirrored row
 __device__ inline float sum_of_16(float s) {
@@ -261,15 +260,18 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
                           float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
     NormArgs p{x, residual, weight, q, sf, normed, residual_out, cols, 4 * cdiv(cols, 512), eps};
     const bool wf32 = weight_type == MOE_F32;
-    // (what the L2s do not hold anyway goes past them)
-    const bool nt = (size_t)rows * cols > (size_t(8) << 20);
-    // Chunks per thread: one while there are fewer rows than fill the CUs, so that a row has as many waves as it can (16 x 7168:
-    // 3.1 us with one chunk, 3.6 with two, 4.9 with four), more, with more in flight each, where rows are many and wide (8192 x
-    // 7168: 75 us with one, 69 with two, 76 with four; 3000 x 4096: 17.3, 17.4 and 15.6; 3000 x 18432: 68 with three, 78 with
-    // four; 20000 x 1536: 37, 38 and 40)
-    constexpr int kMany = 1024;
-    const int least = cdiv(cols, 8 * kMaxThreads);
-    const int ch = rows < kMany || cols <= 2048 ? least : cols <= 4096 ? 4 : cols <= 8192 ? 2 : std::max(3, least);
+    // From a few MB on, loads and stores go past the caches: calls in turn over 1.2 GB, residual read and written, 256 x 7168 4.8 ->
+    // 4.6 us, 400 x 7168 7.8 -> 5.8, 1000 x 7168 13.8 -> 9.8, 8192 x 7168 75 -> 68. Between a kernel that writes x and one that
+    // reads normed, all three as often on the same few MB, 15.3 -> 14.6, 20.1 -> 18.0 and 27.0 -> 27.8; 128 x 7168, below, 11.9
+    // and 12.2.
+    const bool nt = (size_t)rows * cols > (size_t(1) << 20);
+    // Chunks per thread: one, or as few as 1024 threads allow, while at most two rows share a CU, so that a row has as many waves as
+    // it can (16 x 7168: 3.1 us with one chunk, 3.6 with two, 4.9 with four; 400 x 7168 5.8, 6.5, 8.8). With more rows 8 waves a
+    // row, so that three or four of them are under way on a CU (515 x 7168 8.6 with one chunk, 6.9 with two; 1000 x 10240 16.3 with
+    // two, 12.9 with three; 8192 x 7168 75, 69); four chunks, whose registers leave three rows on a CU, while all rows are there at
+    // once (515 x 16384 14.7 with two, 12.1 with four; 4000 x 16384 77 and 79).
+    const int least = cdiv(cols, 8 * kMaxThreads), eight = cdiv(cols, 8 * 512);
+    const int ch = rows > 2 * kCus && eight <= (rows <= 3 * kCus ? 4 : 3) ? eight : least;
     constexpr int kMost = 1 << 21;                      // rows of a launch: at most 2^31 threads
     for (int row0 = 0; row0 < rows; row0 += kMost) {
         const unsigned n = (unsigned)(rows - row0 < kMost ? rows - row0 : kMost);
