@@ -35,6 +35,7 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
@@ -751,10 +752,11 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
     const int fw = wn * FN;
     const int col0 = nt * kBN + 128 * (fw >> 3) + 8 * l + (fw & 7);
     if (col0 >= args.N) return;
-    // bf16 of tiles of 256 rows goes past the caches: all CUs store at once there (4096 x 7168 x 18432 249 -> 244 us, 8192^3 258 ->
-    // 250); FP32's 16-byte stores leave half a line each, which the caches put together (8192^3 past them: 361 us)
+    // bf16 goes past the caches: all CUs store at once (4096 x 7168 x 18432 249 -> 244 us, 8192^3 258 -> 250, 1024 x 7168 x 2048 15.7
+    // -> 14.6, 2048^3 10.5 -> 10.1; 3100 x 368 x 640, whose rows end within a line, 6.0 -> 6.2). FP32's 16-byte stores leave half a
+    // line each, which the caches put together (8192^3 past them 271 -> 361 us, 2048^3 13.1 -> 16.1)
     auto put = [&](auto* to, const auto& x) __attribute__((always_inline)) {
-        if constexpr (BM == 256 && !F32) __builtin_nontemporal_store(x, to);
+        if constexpr (!F32) __builtin_nontemporal_store(x, to);
         else *to = x;
     };
     auto store = [&](int fm, int r, size_t to) __attribute__((always_inline)) {
@@ -772,7 +774,7 @@ __device__ inline __attribute__((always_inline)) void tiled_part(const GemmFp4Ar
             }
             uint16_t* dst = static_cast<uint16_t*>(args.d) + to;
             if constexpr (FN == 8) put(reinterpret_cast<v4i*>(dst), (v4i){(int)pk[0], (int)pk[1], (int)pk[2], (int)pk[3]});
-            else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+            else put(reinterpret_cast<v2u*>(dst), (v2u){pk[0], pk[1]});
         }
     };
     const int lane_row = wm * WM + 4 * g;
