@@ -91,13 +91,13 @@ struct NormArgs {
     uint8_t* sf;
     uint16_t* normed;              // or null
     uint16_t* residual_out;        // or null
-    int cols, sf_stride;
+    uint32_t cols, sf_stride;      // (cols < 2^31: a column counter that steps past it stays within 32 bits, unsigned)
     float eps;
 };
 
 // h of the 8 columns at c of a row that starts at `at`
 template <bool NT>
-__device__ inline void load_h(const NormArgs& p, size_t at, int c, float (&h)[8]) {
+__device__ inline void load_h(const NormArgs& p, size_t at, uint32_t c, float (&h)[8]) {
     unpack8(get<NT, v4u>(p.x + at + c), h);
     if (p.residual) {
         float r[8];
@@ -108,7 +108,7 @@ __device__ inline void load_h(const NormArgs& p, size_t at, int c, float (&h)[8]
 }
 
 template <bool WF32>
-__device__ inline void load_w(const NormArgs& p, int c, float (&w)[8]) {
+__device__ inline void load_w(const NormArgs& p, uint32_t c, float (&w)[8]) {
     if constexpr (WF32) {
         const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + c);
         const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + c + 4);
@@ -133,9 +133,9 @@ __device__ inline uint32_t max_of_16(uint32_t m) {
     return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
 }
 
-// n of 8 columns -> normed, codes, and (every 16th lane) the block's scale byte. c < sf_stride * 128; past cols: zeros
+// n of 8 columns -> normed, codes, and (every 16th lane) the block's scale byte. Past cols: zeros, past sf_stride * 128: nothing
 template <bool NT>
-__device__ inline void store_n(const NormArgs& p, size_t row, int c, const float (&n)[8]) {
+__device__ inline void store_n(const NormArgs& p, size_t row, uint32_t c, const float (&n)[8]) {
     const bool active = c < p.cols;
     const size_t at = row * p.cols + c;
     if (active && p.normed) put<NT>(p.normed + at, pack8(n));
@@ -171,13 +171,13 @@ template <int CH, bool WF32, bool NT>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int row0) {
     __shared__ float part[kMaxThreads / 64];
     const size_t row = (size_t)row0 + blockIdx.x, at = row * p.cols;
-    const int t8 = threadIdx.x * 8, span = blockDim.x * 8;
+    const uint32_t t8 = threadIdx.x * 8, span = blockDim.x * 8;
     const float cols = (float)p.cols;
     if constexpr (CH > 0) {
         float h[CH][8], s = 0.f;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (span) + t8;
+            const uint32_t c = k * span + t8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
             if (c < p.cols) load_h<NT>(p, at, c, h[k]);
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
         const float r = inverse_root(s, cols, p.eps, f);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = k * (span) + t8;
+            const uint32_t c = k * span + t8;
             float n[8] = {};
             if (c < p.cols) {
                 if (p.residual_out) put<NT>(p.residual_out + at + c, pack8(h[k]));
@@ -209,11 +209,11 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
             store_n<NT>(p, row, c, n);
         }
     } else {
-        const int end = (p.cols + 511) / 512 * 512;     // whole waves
+        const uint32_t end = (p.cols + 511) / 512 * 512;     // whole waves
         float f = 1.0f;
         auto squares = [&]() {
             float q = 0.f;
-            for (int c = t8; c < p.cols; c += span) {
+            for (uint32_t c = t8; c < p.cols; c += span) {
                 float h[8];
                 load_h<false>(p, at, c, h);
 #pragma unroll
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
         f = square_scale(s, p.eps);
         if (f != 1.0f) s = squares();
         const float r = inverse_root(s, cols, p.eps, f);
-        for (int c = t8; c < end; c += span) {
+        for (uint32_t c = t8; c < end; c += span) {
             float h[8], n[8] = {};
             if (c < p.cols) {
                 load_h<false>(p, at, c, h);
@@ -241,10 +241,13 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
     }
 }
 
+// ceil(cols / n) of 1 to 2^31 - 1 columns
+int chunks_of(uint32_t cols, uint32_t n) { return (int)((cols - 1) / n + 1); }
+
 template <int CH>
 void launch(const NormArgs& p, bool wf32, bool nt, int row0, unsigned rows, hipStream_t stream) {
     // as many waves as the row needs
-    const int threads = CH > 0 ? 64 * cdiv(p.cols, 512 * CH) : kMaxThreads;
+    const int threads = CH > 0 ? 64 * chunks_of(p.cols, 512 * CH) : kMaxThreads;
     if (wf32) {
         if (nt) rmsnorm_kernel<CH, true, true><<<rows, threads, 0, stream>>>(p, row0);
         else rmsnorm_kernel<CH, true, false><<<rows, threads, 0, stream>>>(p, row0);
@@ -258,7 +261,7 @@ void launch(const NormArgs& p, bool wf32, bool nt, int row0, unsigned rows, hipS
 
 hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const void* weight, int weight_type, int rows, int cols,
                           float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
-    NormArgs p{x, residual, weight, q, sf, normed, residual_out, cols, 4 * cdiv(cols, 512), eps};
+    NormArgs p{x, residual, weight, q, sf, normed, residual_out, (uint32_t)cols, 4u * chunks_of(cols, 512), eps};
     const bool wf32 = weight_type == MOE_F32;
     // From a few MB on, loads and stores go past the caches: calls in turn over 1.2 GB, residual read and written, 256 x 7168 4.8 ->
     // 4.6 us, 400 x 7168 7.8 -> 5.8, 1000 x 7168 13.8 -> 9.8, 8192 x 7168 75 -> 68. Between a kernel that writes x and one that
@@ -270,7 +273,7 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
     // row, so that three or four of them are under way on a CU (515 x 7168 8.6 with one chunk, 6.9 with two; 1000 x 10240 16.3 with
     // two, 12.9 with three; 8192 x 7168 75, 69); four chunks, whose registers leave three rows on a CU, while all rows are there at
     // once (515 x 16384 14.7 with two, 12.1 with four; 4000 x 16384 77 and 79).
-    const int least = cdiv(cols, 8 * kMaxThreads), eight = cdiv(cols, 8 * 512);
+    const int least = chunks_of(cols, 8 * kMaxThreads), eight = chunks_of(cols, 8 * 512);
     const int ch = rows > 2 * kCus && eight <= (rows <= 3 * kCus ? 4 : 3) ? eight : least;
     constexpr int kMost = 1 << 21;                      // rows of a launch: at most 2^31 threads
     for (int row0 = 0; row0 < rows; row0 += kMost) {
