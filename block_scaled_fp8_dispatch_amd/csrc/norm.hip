@@ -211,15 +211,18 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
     } else {
         const uint32_t end = (p.cols + 511) / 512 * 512;     // whole waves
         float f = 1.0f;
+        // The chunks' sums are added in 64 bits: a thread takes up to 2^18 of them, and FP32 would round each into a sum that grows
+        // past it (2^30 equal columns: n 0.4 % off)
         auto squares = [&]() {
-            float q = 0.f;
+            double all = 0.0;
             for (uint32_t c = t8; c < p.cols; c += span) {
-                float h[8];
+                float h[8], q = 0.f;
                 load_h<false>(p, at, c, h);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q += (h[j] * f) * (h[j] * f);
+                all += (double)q;
             }
-            return block_sum(q, part);
+            return block_sum((float)all, part);
         };
         float s = squares();
         f = square_scale(s, p.eps);
