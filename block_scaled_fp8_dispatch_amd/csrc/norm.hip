@@ -166,6 +166,13 @@ __device__ inline float inverse_root(float sum, float cols, float eps, float f) 
     return 1.0f / __builtin_sqrtf(sum / cols + eps * f * f);
 }
 
+// h * f * r of a row whose squares were scaled by f, as first * second: a row scaled down has columns that f would take below FP32's
+// normal numbers, and |h| * r is at most 2^80 times the root of the columns; a row scaled up has columns that r would
+struct Factors {
+    float first, second;
+};
+__device__ inline Factors factors(float f, float r) { return f < 1.0f ? Factors{r, f} : Factors{f, r}; }
+
 // The threads hold CH chunks of 8 columns each in registers (CH = 0: any number, read again from memory for each pass)
 template <int CH, bool WF32, bool NT>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int row0) {
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
         s = squares();
         f = square_scale(s, p.eps);
         if (f != 1.0f) s = squares();
-        const float r = inverse_root(s, cols, p.eps, f);
+        const Factors by = factors(f, inverse_root(s, cols, p.eps, f));
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const uint32_t c = k * span + t8;
@@ -204,7 +211,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
                 float w[8];
                 load_w<WF32>(p, c, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n[j] = (h[k][j] * f) * r * w[j];
+                for (int j = 0; j < 8; ++j) n[j] = (h[k][j] * by.first) * by.second * w[j];
             }
             store_n<NT>(p, row, c, n);
         }
@@ -227,7 +234,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
         float s = squares();
         f = square_scale(s, p.eps);
         if (f != 1.0f) s = squares();
-        const float r = inverse_root(s, cols, p.eps, f);
+        const Factors by = factors(f, inverse_root(s, cols, p.eps, f));
         for (uint32_t c = t8; c < end; c += span) {
             float h[8], n[8] = {};
             if (c < p.cols) {
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int ro
                 float w[8];
                 load_w<WF32>(p, c, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n[j] = (h[j] * f) * r * w[j];
+                for (int j = 0; j < 8; ++j) n[j] = (h[j] * by.first) * by.second * w[j];
             }
             store_n<false>(p, row, c, n);
         }
