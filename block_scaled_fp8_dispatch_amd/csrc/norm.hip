@@ -155,10 +155,11 @@ __device__ inline void store_n(const NormArgs& p, size_t row, uint32_t c, const 
     if ((threadIdx.x & 15) == 0 && (c >> 7) < p.sf_stride) p.sf[row * p.sf_stride + (c >> 7)] = active ? (uint8_t)byte : (uint8_t)0;
 }
 
-// Squares leave FP32's range where |h| passes 2^64 or, with a tiny eps, where all of the row is below about 2^-63. Such rows
-// are scaled by a power of two before they are squared. `f`: that power, or 1
+// Squares leave FP32's range where |h| passes 2^64 or, with a tiny eps, where all of the row is below about 2^-63; with an eps
+// near its end their mean and eps do together. Such rows are scaled by a power of two before they are squared (a large eps hides
+// the squares that this loses). `f`: that power, or 1
 __device__ inline float square_scale(float sum, float eps) {
-    if (!(sum <= 3.4028235e38f)) return 0x1p-80f;
+    if (!(sum <= 3.4028235e38f) || eps > 0x1p100f) return 0x1p-80f;
     return sum < 0x1p-100f && eps < 0x1p-80f ? 0x1p80f : 1.0f;
 }
 

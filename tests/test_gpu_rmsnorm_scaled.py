@@ -39,3 +39,18 @@ def test_rows_of_the_smallest_numbers(cols, top):
     x = bf16(torch.ldexp(x, down))
     w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
     check(call(x, None, w, 2.0 ** -149), x, None, w, 2.0 ** -149)
+
+
+@pytest.mark.parametrize("cols", [128, 7168, 33024])
+@pytest.mark.parametrize("eps", [2.0 ** 99, 2.0 ** 101, 2.0 ** 127, (2 - 2.0 ** -23) * 2.0 ** 127])
+def test_large_eps(cols, eps):
+    """Up to the largest finite number: rows far below, about and far above its root, and rows whose mean square and eps are
+    finite each but not together."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.rand(7, cols, generator=g, device="cuda") + 0.5
+    x[1::2] *= -1
+    power = torch.tensor([-30, 0, 30, 50, 59, 64, 100], device="cuda")
+    x = bf16(torch.ldexp(x, power[:, None]))
+    x[4] = 1.8203125 * 2.0 ** 59
+    w = bf16(1 + 0.1 * torch.randn(cols, generator=g, device="cuda"))
+    check(call(x, None, w, eps), x, None, w, eps)
