@@ -47,7 +47,7 @@ int moe_cast_to_fp4(const void* x, int32_t x_type, int32_t rows, int32_t cols, u
                     hipStream_t stream);
 
 /* The cast back: x [rows][cols] = E2M1 * 2^(byte - 127), in x_type. Exact but for infinities above the type's range
- * (bytes of 252 and more can reach it) and NaN for a byte of 255. Arguments as moe_cast_to_fp4's. */
+ * (bytes of 253 and 254 can reach it) and NaN for a byte of 255. Arguments as moe_cast_to_fp4's. */
 int moe_cast_from_fp4(const uint8_t* x_fp4, const uint8_t* x_sf, int32_t rows, int32_t cols, void* x, int32_t x_type,
                       hipStream_t stream);
 
