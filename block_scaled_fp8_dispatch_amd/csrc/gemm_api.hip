@@ -148,8 +148,8 @@ bool fp8_shape_ok(int G, int N, int K, int d_type) {
 }
 
 // Whether tiles of 128 x 256, which exist for every output type, take a launch below 2^32 threads
-bool fp8_grid_ok(long long rows, int G, int N) {
-    return (rows / 128 + G) * cdiv(N, kBN) < (1ll << 24);
+bool fp8_grid_ok(int rows, int G, int N) {
+    return (long long)most_row_tiles(rows, G, 128) * cdiv(N, kBN) < (1ll << 24);
 }
 
 GemmFp8Args fp8_args(void* d, int d_type, const uint8_t* a, const uint8_t* a_sf, int N, int K, const uint8_t* b,
@@ -231,6 +231,9 @@ int fp4_cast_check(const void* x, int x_type, int rows, int cols, const void* q,
 }
 
 }  // namespace
+
+int most_row_tiles(int rows, int groups, int block_m) { return rows / block_m + groups; }
+
 }  // namespace moe
 
 using namespace moe;
@@ -401,7 +404,7 @@ int moe_m_grouped_fp8_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     const Fp8Plan plan = fp8_plan(groups, (double)m / groups, m, true, n, k, d_type == MOE_F32);
     const int BM = plan.block_m;
     if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
-    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, cdiv(m, BM) + groups);
+    const GemmFp8Args g = fp8_args(d, d_type, a, a_sf, n, k, b, b_sf, ws, W, BM, most_row_tiles(m, groups, BM));
     return launch_gemm_fp8(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -417,7 +420,7 @@ int moe_m_grouped_fp8_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (max_m < 0) return MOE_ERR_TOKENS;
     const long long rows = (long long)groups * max_m;
     if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
-    if (!fp8_grid_ok(rows, groups, n)) return MOE_ERR_SHAPE;
+    if (!fp8_grid_ok((int)rows, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws((int)rows, groups);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;
@@ -483,7 +486,7 @@ int moe_m_grouped_fp4_gemm_contiguous(void* d, int32_t d_type, const uint8_t* a,
     const Fp4Plan plan = fp4_plan(groups, (double)m / groups, m, m, true, n, k);
     const int BM = plan.block_m;
     if (group_rows(group_of_row, m, groups, BM, ws, W, stream) != hipSuccess) return MOE_ERR_HIP;
-    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, W, BM, cdiv(m, BM) + groups);
+    GemmFp4Args g = fp4_args(d, d_type, a, a_sf, m, groups, n, k, packed_b, W, BM, most_row_tiles(m, groups, BM));
     fp4_lists(g, ws, W);
     return launch_gemm_fp4(plan, g, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -499,7 +502,7 @@ int moe_m_grouped_fp4_gemm_masked(void* d, int32_t d_type, const uint8_t* a, con
     if (max_m < 0) return MOE_ERR_TOKENS;
     const long long rows = (long long)groups * max_m;
     if (!rows_ok(rows, groups, k)) return MOE_ERR_TOKENS;
-    if (!fp8_grid_ok(rows, groups, n)) return MOE_ERR_SHAPE;
+    if (!fp8_grid_ok((int)rows, groups, n)) return MOE_ERR_SHAPE;
     const GemmWs W = gemm_ws((int)rows, groups);
     if (workspace_bytes < W.partial) return MOE_ERR_WORKSPACE;
     if (max_m == 0) return MOE_OK;

@@ -907,8 +907,10 @@ Fp4Plan fp4_plan(int groups, double rows, int most, int max_rows, bool ragged, i
     const int steps = K / kBK;
     for (const Cost& c : kCosts) {
         const int cols = c.waves ? cdiv(N, 128) * (128 / c.bn) : cdiv(N, kBN);
-        // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128)
-        const uint64_t grid = (uint64_t)(max_rows / c.block_m + groups) * (c.block_m / c.bm) * cols;
+        // a launch has fewer than 2^32 threads (the caller has checked this for kTiled128); the 256-row tiles' last round may take
+        // kCus workgroups more
+        const uint64_t grid = (uint64_t)most_row_tiles(max_rows, groups, c.block_m) * (c.block_m / c.bm) * cols +
+                              (c.kernel == Fp4Kernel::kTiled256 ? kCus : 0);
         if (c.kernel != Fp4Kernel::kTiled128 && grid * (c.waves ? c.waves * 64 : 256) >= (1ull << 32)) continue;
         const int unit = ragged ? std::max(c.bm, 64) : c.bm;
         const double tiles = std::ceil(row_tiles_of(groups, rows, most, ragged, unit) * (unit / c.bm)) * cols;

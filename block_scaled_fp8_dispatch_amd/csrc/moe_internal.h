@@ -180,6 +180,10 @@ hipError_t launch_few(const moe_shape_t& s, const PackedLayout& P, const uint8_t
                       const int32_t* idx, const float* weights, int T, const uint8_t* packed, uint8_t* ws, uint16_t* y,
                       hipStream_t stream);
 
+// Most row tiles that `rows` rows (below 2^31 - 2^18) in `groups` groups can fill, each group's rows in tiles of their own: rows r_g
+// fill at most (r_g + block_m - 1) / block_m, together at most rows / block_m + groups - groups / block_m (gemm_api.hip)
+int most_row_tiles(int rows, int groups, int block_m);
+
 // FP8 x FP8 GEMM with 128-block scales (gemm_fp8.hip)
 enum class Fp8Kernel { kTiled256, kTiled256x224, kTiled128, kTiled64, kSkinny64, kSkinny32, kSkinny16x32, kSkinny16 };
 struct GemmFp8Args {
