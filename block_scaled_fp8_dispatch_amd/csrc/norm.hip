@@ -174,7 +174,7 @@ struct Factors {
 };
 __device__ inline Factors factors(float f, float r) { return f < 1.0f ? Factors{r, f} : Factors{f, r}; }
 
-// The threads hold CH chunks of 8 columns each in registers (CH = 0: any number, read again from memory for each pass)
+// The threads hold CH chunks of 8 columns each in registers (CH = 0: any number, read again for each pass, through the caches)
 template <int CH, bool WF32, bool NT>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs p, int row0) {
     __shared__ float part[kMaxThreads / 64];
@@ -259,11 +259,12 @@ template <int CH>
 void launch(const NormArgs& p, bool wf32, bool nt, int row0, unsigned rows, hipStream_t stream) {
     // as many waves as the row needs
     const int threads = CH > 0 ? 64 * chunks_of(p.cols, 512 * CH) : kMaxThreads;
+    constexpr bool PAST = CH > 0;              // (CH = 0 has no form past the caches)
     if (wf32) {
-        if (nt) rmsnorm_kernel<CH, true, true><<<rows, threads, 0, stream>>>(p, row0);
+        if (PAST && nt) rmsnorm_kernel<CH, true, PAST><<<rows, threads, 0, stream>>>(p, row0);
         else rmsnorm_kernel<CH, true, false><<<rows, threads, 0, stream>>>(p, row0);
     } else {
-        if (nt) rmsnorm_kernel<CH, false, true><<<rows, threads, 0, stream>>>(p, row0);
+        if (PAST && nt) rmsnorm_kernel<CH, false, PAST><<<rows, threads, 0, stream>>>(p, row0);
         else rmsnorm_kernel<CH, false, false><<<rows, threads, 0, stream>>>(p, row0);
     }
 }
@@ -274,7 +275,7 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
                           float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
     NormArgs p{x, residual, weight, q, sf, normed, residual_out, (uint32_t)cols, 4u * chunks_of(cols, 512), eps};
     const bool wf32 = weight_type == MOE_F32;
-    // From a few MB on, loads and stores go past the caches: calls in turn over 1.2 GB, residual read and written, 256 x 7168 4.8 ->
+    // From a few MB on, loads and stores of rows that registers hold go past the caches: calls in turn over 1.2 GB, residual read and written, 256 x 7168 4.8 ->
     // 4.6 us, 400 x 7168 7.8 -> 5.8, 1000 x 7168 13.8 -> 9.8, 8192 x 7168 75 -> 68. Between a kernel that writes x and one that
     // reads normed, all three as often on the same few MB, 15.3 -> 14.6, 20.1 -> 18.0 and 27.0 -> 27.8; 128 x 7168, below, 11.9
     // and 12.2.
