@@ -10,7 +10,8 @@
 // A workgroup owns a row and keeps it in registers: 8 columns per lane and chunk, so that the 16 lanes of a DPP row hold one
 // 128-column block, whose largest magnitude is four steps within them. One pass over memory: 8192 x 7168 with a residual read and
 // written moves 411 MB in 68 us, 6.0 TB/s, where a copy moves 5.1; 515 x 18432 with every output 85.6 MB in 19. Few rows are two
-// barriers, the loads' and the sum's latency (16 x 7168 3.1 us in a graph, an empty launch 1.95).
+// barriers, the loads' and the sum's latency (16 x 7168 3.1 us in a graph, an empty launch 1.95). Narrow rows leave lanes idle
+// (2^20 x 128 286 us, 1.4 TB/s), and rows past 32768 columns are read twice (1000 x 65536 with a residual 128 us, 3.6 TB/s).
 #include "moe_internal.h"
 #include "moe_serving.h"
 
