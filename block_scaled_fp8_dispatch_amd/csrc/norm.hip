@@ -283,9 +283,10 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
     const bool nt = (size_t)rows * cols > (size_t(1) << 20);
     // Chunks per thread: one, or as few as 1024 threads allow, while at most two rows share a CU, so that a row has as many waves as
     // it can (16 x 7168: 3.1 us with one chunk, 3.6 with two, 4.9 with four; 400 x 7168 5.8, 6.5, 8.8). With more rows 8 waves a
-    // row, so that three or four of them are under way on a CU (515 x 7168 8.6 with one chunk, 6.9 with two; 1000 x 10240 16.3 with
-    // two, 12.9 with three; 8192 x 7168 75, 69); four chunks, whose registers leave three rows on a CU, while all rows are there at
-    // once (515 x 16384 14.7 with two, 12.1 with four; 4000 x 16384 77 and 79).
+    // row, so that four of them are under way on a CU (515 x 7168 8.7 with one chunk, 6.9 with two; 1000 x 10240 16.1 with two, 12.7
+    // with three; 8192 x 7168 73 with one, 68 with two); four chunks up to three rows a CU (515 x 16384 14.7 with two, 11.9 with four;
+    // 4000 x 16384 76 and 78). The last rule misses up to a fifth: 1000 x 16384 22.0 with two, 19.9 with four, and past 8 waves
+    // 515 x 18432 19.8 with three, 16.0 with four, where 3000 x 18432 takes 67 and 70.
     const int least = chunks_of(cols, 8 * kMaxThreads), eight = chunks_of(cols, 8 * 512);
     const int ch = rows > 2 * kCus && eight <= (rows <= 3 * kCus ? 4 : 3) ? eight : least;
     constexpr int kMost = 1 << 21;                      // rows of a launch: at most 2^31 threads
