@@ -21,7 +21,8 @@
 // into the lanes' bytes.
 // 4096 x 7168 x 18432 takes 233 us, 8192^3 236 (bf16), 275 (FP32): 4.65 PFLOP/s (another card 245 and 4.4). The chip holds 1.96 GHz
 // of its 2.4 under it and the matrix units are busy in 53 % of the cycles; products of registers alone, nothing loaded, reach 7.1
-// PFLOP/s on the same operands and 9.5 on zeros, and the whole kernel a quarter more on zeros: power is what bounds it, then LDS reads and loads.
+// PFLOP/s on the same operands and 9.5 on zeros, and the whole kernel a quarter more on zeros: power is what bounds it, then LDS
+// reads and loads.
 // Few rows of many weights stream: 32 groups of about 32 rows x 4096 x 7168 83 us, 6.0 TB/s.
 #include <algorithm>
 #include <cmath>

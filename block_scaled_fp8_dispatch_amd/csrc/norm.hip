@@ -276,10 +276,10 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const voi
                           float eps, uint8_t* q, uint8_t* sf, uint16_t* normed, uint16_t* residual_out, hipStream_t stream) {
     NormArgs p{x, residual, weight, q, sf, normed, residual_out, (uint32_t)cols, 4u * chunks_of(cols, 512), eps};
     const bool wf32 = weight_type == MOE_F32;
-    // From a few MB on, loads and stores of rows that registers hold go past the caches: calls in turn over 1.2 GB, residual read and written, 256 x 7168 4.8 ->
-    // 4.6 us, 400 x 7168 7.8 -> 5.8, 1000 x 7168 13.8 -> 9.8, 8192 x 7168 75 -> 68. Between a kernel that writes x and one that
-    // reads normed, all three as often on the same few MB, 15.3 -> 14.6, 20.1 -> 18.0 and 27.0 -> 27.8; 128 x 7168, below, 11.9
-    // and 12.2.
+    // From a few MB on, loads and stores of rows that registers hold go past the caches: calls in turn over 1.2 GB, residual read
+    // and written, 256 x 7168 4.8 -> 4.6 us, 400 x 7168 7.8 -> 5.8, 1000 x 7168 13.8 -> 9.8, 8192 x 7168 75 -> 68. Between a kernel
+    // that writes x and one that reads normed, all three as often on the same few MB, 15.3 -> 14.6, 20.1 -> 18.0 and 27.0 -> 27.8;
+    // 128 x 7168, below, 11.9 and 12.2.
     const bool nt = (size_t)rows * cols > (size_t(1) << 20);
     // Chunks per thread: one, or as few as 1024 threads allow, while at most two rows share a CU, so that a row has as many waves as
     // it can (16 x 7168: 3.1 us with one chunk, 3.6 with two, 4.9 with four; 400 x 7168 5.8, 6.5, 8.8). With more rows 8 waves a
